@@ -8,6 +8,9 @@ binding of that ABI; it loads the in-tree library and fails loudly if it is
 missing.
 """
 from .binding import (  # noqa: F401
+    Adapters, AdamW, AdamWTensor, Rows, dictproj_adapter_backward, dictproj_adapter_forward, dictproj_adapters_create,
+    dictproj_adapters_set, dictproj_adapters_slot, dictproj_adamw_create, dictproj_adamw_step, dictproj_backward_input,
+    dictproj_forward_adapters, dictproj_group_reserve_backward, dictproj_rows_create, dictproj_rows_set,
     PATH_AUTO, PATH_DECODE, PATH_PREFILL, DECODE_AUTO, DECODE_FUSED, DECODE_SPLIT, dictproj_set_decode_kernels,
     dictproj_get_decode_kernels, IFMT, dictproj_layer_upload_bitmap, dictproj_pack_layer_bitmap,
     dictproj_layer_upload_blocks, dictproj_pack_layer_blocks, dictproj_layer_index_format, dictproj_layer_export_bitmap,

@@ -54,6 +54,12 @@ class DeviceLayer(C.Structure):
                 ("seg_start", C.c_void_p), ("s", C.c_float), ("k", C.c_int), ("d_out", C.c_int)]
 
 
+class AdamWTensor(C.Structure):
+    """dictproj_adamw_tensor: one tensor of an AdamW step (device addresses)."""
+    _fields_ = [("p", C.c_void_p), ("g", C.c_void_p), ("m", C.c_void_p), ("v", C.c_void_p), ("m_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("copy", C.c_void_p), ("n", C.c_longlong)]
+
+
 # (name, restype, argtypes) for every entry point declared in include/dictproj.h
 SIGNATURES = [
     ("dictproj_group_packed_sizes", C.c_int, [C.c_int, C.c_int, _szp, _szp]),
@@ -127,6 +133,24 @@ SIGNATURES = [
     ("dictproj_dictionary_stage_prefill", C.c_int, [C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p]),
     ("dictproj_forward_noalloc", C.c_int,
      [C.POINTER(DeviceGroup), C.POINTER(DeviceLayer), C.c_void_p, C.c_int, C.c_void_p, C.c_void_p]),
+    ("dictproj_adapters_create", C.c_int, [C.c_int] * 5 + [C.POINTER(C.c_void_p)]),
+    ("dictproj_free_adapters", None, [C.c_void_p]),
+    ("dictproj_adapters_set", C.c_int,
+     [C.c_void_p, C.c_int, C.c_int, C.c_float, C.c_void_p, C.c_void_p, C.c_void_p]),
+    ("dictproj_adapters_slot", C.c_int,
+     [C.c_void_p, C.c_int, C.POINTER(C.c_void_p), C.POINTER(C.c_void_p), _intp]),
+    ("dictproj_rows_create", C.c_int, [C.c_int, C.c_int, C.POINTER(C.c_void_p)]),
+    ("dictproj_free_rows", None, [C.c_void_p]),
+    ("dictproj_rows_set", C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_void_p]),
+    ("dictproj_adapter_forward", C.c_int, [C.c_void_p] * 6),
+    ("dictproj_forward_adapters", C.c_int, [C.c_void_p] * 7),
+    ("dictproj_adapter_backward", C.c_int, [C.c_void_p] * 8 + [C.c_int, C.c_void_p]),
+    ("dictproj_group_reserve_backward", C.c_int, [C.c_void_p, C.c_int]),
+    ("dictproj_backward_input", C.c_int,
+     [C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    ("dictproj_adamw_create", C.c_int, [C.POINTER(AdamWTensor), C.c_int, C.c_int, C.POINTER(C.c_void_p)]),
+    ("dictproj_free_adamw", None, [C.c_void_p]),
+    ("dictproj_adamw_step", C.c_int, [C.c_void_p, C.c_longlong] + [C.c_double] * 6 + [C.c_void_p]),
     ("dictproj_rank_for_budget", C.c_int, [C.c_double, C.c_int, C.c_int, C.c_int, C.c_int, _intp]),
     ("dictproj_budget", C.c_int, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_double, C.POINTER(C.c_double),
                                   C.POINTER(C.c_double), C.POINTER(C.c_double), C.POINTER(C.c_double)]),
@@ -727,6 +751,143 @@ def dictproj_forward_noalloc_status(group: DeviceGroup, layer: DeviceLayer, X_pt
     """Raw status of a no-allocation forward (no exception)."""
     return lib().dictproj_forward_noalloc(C.byref(group), C.byref(layer), C.c_void_p(X_ptr), M,
                                           C.c_void_p(Y_ptr), C.c_void_p(stream))
+
+
+# ---------------------------------------------------------------- adapters
+class Adapters:
+    """Owns a dictproj_adapters handle (a pool of low-rank adapters on the device)."""
+
+    def __init__(self, handle: int, d_in: int, d_out: int, max_rank: int, n_slots: int, max_tokens: int):
+        self.handle, self.d_in, self.d_out = handle, d_in, d_out
+        self.max_rank, self.n_slots, self.max_tokens = max_rank, n_slots, max_tokens
+
+    def free(self):
+        if self.handle:
+            lib().dictproj_free_adapters(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+class Rows:
+    """Owns a dictproj_rows handle (a batch's rows sorted by adapter slot)."""
+
+    def __init__(self, handle: int, max_rows: int, n_slots: int):
+        self.handle, self.max_rows, self.n_slots = handle, max_rows, n_slots
+
+    def free(self):
+        if self.handle:
+            lib().dictproj_free_rows(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+class AdamW:
+    """Owns a dictproj_adamw handle (the table of the tensors of a step)."""
+
+    def __init__(self, handle: int, n_tensors: int, state_bits: int):
+        self.handle, self.n_tensors, self.state_bits = handle, n_tensors, state_bits
+
+    def free(self):
+        if self.handle:
+            lib().dictproj_free_adamw(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+def dictproj_adapters_create(d_in: int, d_out: int, max_rank: int, n_slots: int, max_tokens: int) -> Adapters:
+    h = C.c_void_p()
+    _check(lib().dictproj_adapters_create(d_in, d_out, max_rank, n_slots, max_tokens, C.byref(h)))
+    return Adapters(h.value, d_in, d_out, max_rank, n_slots, max_tokens)
+
+
+def dictproj_adapters_set(adapters: Adapters, slot: int, rank: int, scale: float, A_ptr: int, B_ptr: int,
+                          stream: int = 0):
+    """A: device fp16 [rank][d_in], B: device fp16 [rank][d_out]; rank 0 empties the slot."""
+    _check(lib().dictproj_adapters_set(adapters.handle, slot, rank, float(scale), C.c_void_p(A_ptr or None),
+                                       C.c_void_p(B_ptr or None), C.c_void_p(stream)))
+
+
+def dictproj_adapters_slot(adapters: Adapters, slot: int) -> dict:
+    """Device addresses of a slot's weights: {'A', 'B', 'ld_B'}."""
+    a, b, ld = C.c_void_p(), C.c_void_p(), C.c_int()
+    _check(lib().dictproj_adapters_slot(adapters.handle, slot, C.byref(a), C.byref(b), C.byref(ld)))
+    return {"A": a.value, "B": b.value, "ld_B": ld.value}
+
+
+def dictproj_rows_create(max_rows: int, n_slots: int) -> Rows:
+    h = C.c_void_p()
+    _check(lib().dictproj_rows_create(max_rows, n_slots, C.byref(h)))
+    return Rows(h.value, max_rows, n_slots)
+
+
+def dictproj_rows_set(rows: Rows, ids_ptr: int, M: int, stream: int = 0):
+    """ids: device int32[M], the slot of each row (outside [0, n_slots): no adapter)."""
+    _check(lib().dictproj_rows_set(rows.handle, C.c_void_p(ids_ptr or None), M, C.c_void_p(stream)))
+
+
+def dictproj_adapter_forward(adapters: Adapters, rows: Rows, X_ptr: int, base_ptr: int, Y_ptr: int, stream: int = 0):
+    """Y = base + scale (X A^T) B for every row's own adapter (base_ptr 0: base = 0; may equal Y_ptr)."""
+    _check(lib().dictproj_adapter_forward(adapters.handle, rows.handle, C.c_void_p(X_ptr or None),
+                                          C.c_void_p(base_ptr or None), C.c_void_p(Y_ptr or None), C.c_void_p(stream)))
+
+
+def dictproj_forward_adapters(X_ptr: int, layer: Layer, group: Group, adapters: Adapters, rows: Rows, Y_ptr: int,
+                              stream: int = 0):
+    """The projection and the adapters of its rows: dictproj_forward, then dictproj_adapter_forward on Y."""
+    _check(lib().dictproj_forward_adapters(C.c_void_p(X_ptr or None), layer.handle, group.handle, adapters.handle,
+                                           rows.handle, C.c_void_p(Y_ptr or None), C.c_void_p(stream)))
+
+
+def dictproj_adapter_backward(adapters: Adapters, rows: Rows, X_ptr: int, dY_ptr: int, base_ptr: int, dX_ptr: int,
+                              dA_ptr: int, dB_ptr: int, accumulate: bool = False, stream: int = 0):
+    """dX = base + scale (dY B^T) A, and the gradients dA, dB (fp32) of every slot."""
+    _check(lib().dictproj_adapter_backward(adapters.handle, rows.handle, C.c_void_p(X_ptr or None),
+                                           C.c_void_p(dY_ptr or None), C.c_void_p(base_ptr or None),
+                                           C.c_void_p(dX_ptr or None), C.c_void_p(dA_ptr or None),
+                                           C.c_void_p(dB_ptr or None), int(accumulate), C.c_void_p(stream)))
+
+
+def dictproj_group_reserve_backward(group: Group, max_d_out: int):
+    """Reserve the group's scratch for dictproj_backward_input on layers with up to max_d_out columns."""
+    _check(lib().dictproj_group_reserve_backward(group.handle, max_d_out))
+
+
+def dictproj_backward_input(dY_ptr: int, M: int, layer: Layer, group: Group, dX_ptr: int, stream: int = 0):
+    """dX = dY C^T D^T, the input gradient of the frozen projection."""
+    _check(lib().dictproj_backward_input(C.c_void_p(dY_ptr or None), M, layer.handle, group.handle,
+                                         C.c_void_p(dX_ptr or None), C.c_void_p(stream)))
+
+
+def dictproj_adamw_create(tensors, state_bits: int = 32) -> AdamW:
+    """tensors: list of dicts with device addresses p, g, m, v (and m_scale, v_scale for
+    state_bits 8), optionally copy (fp16), and the element count n."""
+    arr = (AdamWTensor * len(tensors))(*[
+        AdamWTensor(t["p"] or None, t["g"] or None, t["m"] or None, t["v"] or None, t.get("m_scale") or None,
+                    t.get("v_scale") or None, t.get("copy") or None, t["n"]) for t in tensors])
+    h = C.c_void_p()
+    _check(lib().dictproj_adamw_create(arr, len(tensors), state_bits, C.byref(h)))
+    return AdamW(h.value, len(tensors), state_bits)
+
+
+def dictproj_adamw_step(adamw: AdamW, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999,
+                        eps: float = 1e-8, weight_decay: float = 0.01, grad_scale: float = 1.0, stream: int = 0):
+    _check(lib().dictproj_adamw_step(adamw.handle, step, float(lr), float(beta1), float(beta2), float(eps),
+                                     float(weight_decay), float(grad_scale), C.c_void_p(stream)))
 
 
 def dictproj_check(stream: int = 0):

@@ -42,11 +42,11 @@ static bool fault(const char* kind) {
   return f && std::strcmp(f, kind) == 0;
 }
 
-static cudaError_t dmalloc(void** p, size_t n) {
+cudaError_t dmalloc(void** p, size_t n) {
   if (fault("alloc")) return cudaErrorMemoryAllocation;
   return cudaMalloc(p, n ? n : 16);
 }
-static cudaError_t h2d(void* d, const void* h, size_t n) {
+cudaError_t h2d(void* d, const void* h, size_t n) {
   if (fault("copy")) return cudaErrorInvalidValue;
   return n ? cudaMemcpy(d, h, n, cudaMemcpyHostToDevice) : cudaSuccess;
 }
@@ -91,6 +91,7 @@ int ensure_device(int* dev_out) {
     if ((e = prepare_prefill_kernels(dev)) != cudaSuccess) return cuda_fail(e, "prefill kernel set-up");
     if ((e = prepare_fused_kernels(dev)) != cudaSuccess) return cuda_fail(e, "fused kernel set-up");
     if ((e = prepare_index_kernels(dev)) != cudaSuccess) return cuda_fail(e, "index-format kernel set-up");
+    if ((e = prepare_adapter_kernels(dev)) != cudaSuccess) return cuda_fail(e, "adapter kernel set-up");
     g_dev_ready[dev] = 1;
   }
   *dev_out = dev;
@@ -195,6 +196,7 @@ void dictproj_free_group(dictproj_group* g) {
   cudaFree(g->z32);
   cudaFree(g->z16);
   cudaFree(g->cdense);
+  cudaFree(g->ddense);
   cudaFree(g->fcodes);
   cudaFree(g->fscales);
   cudaFree(g->zx);

@@ -24,6 +24,11 @@ int cuda_fail(cudaError_t e, const char* what);
 // allocates nothing.
 int ensure_device(int* dev_out);
 
+// cudaMalloc / host-to-device copy of the ABI layer (with the host-side fault
+// injection of the error-path tests).
+cudaError_t dmalloc(void** p, size_t n);
+cudaError_t h2d(void* d, const void* h, size_t n);
+
 int pack_group_host(const float* D, int d_in, int k, uint8_t* codes, uint8_t* scales, float* s_D);
 int layer_packed_entries(const int32_t* col_ptr, int k, int d_out, size_t* total);
 int pack_layer_host(const int32_t* col_ptr, const int32_t* atom_idx, const float* vals, int k,
@@ -61,6 +66,7 @@ struct dictproj_group {
   uint16_t* z16;           // prefill Z, fp16 [max_tokens][k]
   uint16_t* cdense;        // prefill coefficient operand, fp16 [d_out][k] for d_out <= cdense_cols
   int cdense_cols;         // reserved output columns (dictproj_group_reserve_prefill)
+  uint16_t* ddense;        // input gradient: D^ densified, fp16 [k][d_in] (dictproj_group_reserve_backward), or null
   CUtensorMap codes_map;   // TMA map of codes: [k] rows x [d_in/2] bytes, box 32 x 256
   // fused decode kernel
   bool fused_ok;           // the fused kernel serves this group
@@ -98,4 +104,37 @@ struct dictproj_layer {
   uint32_t* cplan_off;     // [n_sm + 1]
   uint4* cplan;            // {o_a, o_b, E_a, E_b}
   int cplan_max;           // chunks of the busiest position
+};
+
+// A pool of low-rank adapters of one projection shape.
+struct dictproj_adapters {
+  int device;
+  int d_in, d_out, max_rank, n_slots, max_tokens;
+  int rp;                  // stored rank rows per slot: max_rank rounded up to 16 (zero past a slot's rank)
+  int ld_b;                // row stride of B: d_out rounded up to 8 (zero columns past d_out)
+  int n_sm;
+  uint16_t* A;             // fp16 [n_slots][rp][d_in]
+  uint16_t* B;             // fp16 [n_slots][rp][ld_b]
+  int* rank;               // [n_slots], 0 = empty
+  float* scale;            // [n_slots]
+  // backward pass: scale * U and scale * T of the planned rows, in plan order
+  float* u;                // fp32 [max_tokens][rp]
+  float* t;                // fp32 [max_tokens][rp]
+};
+
+// A batch's rows sorted by adapter slot (stable), and the tiles they form.
+struct dictproj_rows {
+  int device;
+  int max_rows, n_slots;
+  int M;                   // rows of the last dictproj_rows_set (0: none yet)
+  int* perm;               // [max_rows] row numbers by slot, rows without an adapter last
+  int* start;              // [n_slots + 2] first position of each slot, of the rows without one, M
+};
+
+struct dictproj_adamw {
+  int device;
+  int n_tensors, bits, n_sm;
+  long long chunks;        // kAdamwChunk-element pieces of all tensors
+  dictproj_adamw_tensor* tensors;  // device copy of the table
+  long long* first;        // device [n_tensors + 1] first chunk of each tensor
 };

@@ -118,5 +118,29 @@ cudaError_t launch_densify_coeff(const dictproj_layer* l, __half* Cd, cudaStream
 cudaError_t launch_coeff_prefill(const dictproj_layer* l, const __half* Z, const __half* Cd, int M, __half* Y,
                                  cudaStream_t stream);
 cudaError_t take_prefill_error(unsigned int* out);
+// Input gradient: Dd[j][i] = D^ densified to fp16, [k][d_in]
+cudaError_t launch_densify_dict(const dictproj_group* g, __half* Dd, cudaStream_t stream);
+// out[M][N] = scale A[M][K] B[K][N] (fp16 row-major operands, fp32 accumulation)
+cudaError_t launch_gemm_nn(const __half* A, const __half* B, int M, int N, int K, float scale, __half* out,
+                           cudaStream_t stream);
+
+// adapters (adapter.cu)
+cudaError_t prepare_adapter_kernels(int device);
+cudaError_t launch_adapter_set(const dictproj_adapters* a, int slot, int rank, float scale, const __half* A,
+                               const __half* B, cudaStream_t stream);
+cudaError_t launch_rows_plan(const dictproj_rows* r, const int* ids, int M, cudaStream_t stream);
+cudaError_t launch_adapter_forward(const dictproj_adapters* a, const dictproj_rows* r, const __half* X,
+                                   const __half* base, __half* Y, cudaStream_t stream);
+cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_rows* r, const __half* X,
+                                    const __half* dY, const __half* base, __half* dX, float* dA, float* dB,
+                                    bool accumulate, cudaStream_t stream);
+
+// optimiser (adamw.cu)
+constexpr int kAdamwChunk = 2048;  // elements of one work item, a multiple of DICTPROJ_ADAMW_BLOCK
+struct AdamwFactors {
+  float grad_scale, b1, omb1, b2, omb2, rbc2, eps, decay, alpha;
+  uint32_t step;
+};
+cudaError_t launch_adamw(const dictproj_adamw* w, const AdamwFactors& f, cudaStream_t stream);
 
 }  // namespace dictproj

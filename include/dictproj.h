@@ -397,6 +397,185 @@ int dictproj_coefficient_stage(const float* Z, int M, const dictproj_layer* laye
 int dictproj_dictionary_stage_prefill(const void* X, int M, const dictproj_group* group, void* Z, void* stream);
 
 /* ------------------------------------------------------------------------- */
+/* Low-rank adapters beside a projection: many requests at once, and training */
+/* ------------------------------------------------------------------------- */
+
+/* The packed factors of a projection are frozen; what a request or a fine-tune
+ * changes is a low-rank adapter beside them. Adapter s of rank r_s adds
+ *
+ *     T[m] = X[m] A_s^T,     Y[m] = base[m] + scale_s T[m] B_s      for the rows m of slot s
+ *
+ * to the projection's rows, A_s fp16 [r_s][d_in], B_s fp16 [r_s][d_out] (rank-major:
+ * row j of A is the j-th input direction, row j of B the j-th output direction).
+ *
+ * A pool (dictproj_adapters) owns the device copies of up to n_slots adapters of
+ * one projection shape, and the workspaces of the backward pass. A rows plan
+ * (dictproj_rows) sorts a batch's rows by the slot each row uses; every
+ * projection of a step shares one plan. Calls that use the same pool's backward
+ * pass, or that read a plan or a slot while another call writes it, must be
+ * ordered on one stream (or otherwise serialised). */
+typedef struct dictproj_adapters dictproj_adapters;
+typedef struct dictproj_rows dictproj_rows;
+
+#define DICTPROJ_MAX_RANK 128
+#define DICTPROJ_MAX_SLOTS 1024
+#define DICTPROJ_MAX_ROWS (1 << 20)
+
+/* A pool of n_slots empty slots (rank 0: such a slot's rows get base alone) on the
+ * current device; max_tokens bounds the rows of one call. d_in % 32 == 0,
+ * d_out >= 1 (any value), 1 <= max_rank <= DICTPROJ_MAX_RANK, 1 <= n_slots <=
+ * DICTPROJ_MAX_SLOTS, 1 <= max_tokens <= DICTPROJ_MAX_ROWS. Errors: NULL, SHAPE
+ * (d_in, d_out), RANGE (the others), OOM, CUDA. */
+int dictproj_adapters_create(int d_in, int d_out, int max_rank, int n_slots, int max_tokens,
+                             dictproj_adapters** out);
+void dictproj_free_adapters(dictproj_adapters* a); /* NULL is a no-op */
+
+/* Load an adapter into a slot: A device fp16 [rank][d_in], B device fp16
+ * [rank][d_out], 2-byte aligned, only read by this call. rank 0 empties the slot (A
+ * and B are not read and may be NULL). Asynchronous on `stream`; replaces
+ * what the slot held. Errors: NULL, RANGE (slot, rank), VALUE (scale not finite),
+ * ALIGN, MISMATCH (device), CUDA. */
+int dictproj_adapters_set(dictproj_adapters* a, int slot, int rank, float scale, const void* A, const void* B,
+                          void* stream);
+
+/* Where a slot's weights lie on the device, for an optimiser that writes them in
+ * place: *A fp16 [rank][d_in] and *B fp16 [rank][*ld_B], row stride *ld_B >= d_out
+ * elements (equal to d_out when d_out % 8 == 0; the columns past d_out must stay
+ * zero). Any output may be NULL. Errors: NULL, RANGE (slot). */
+int dictproj_adapters_slot(const dictproj_adapters* a, int slot, void** A, void** B, int* ld_B);
+
+/* A plan for batches of up to max_rows rows over a pool's n_slots slots (the
+ * limits of dictproj_adapters_create). Errors: NULL, RANGE, OOM, CUDA. */
+int dictproj_rows_create(int max_rows, int n_slots, dictproj_rows** out);
+void dictproj_free_rows(dictproj_rows* rows); /* NULL is a no-op */
+
+/* Plan a batch of M rows: ids device int32[M], ids[m] the slot of row m; any value
+ * outside [0, n_slots) means that the row uses no adapter. The ids are read on the
+ * device, so a captured call plans anew with what they hold at each replay. Rows
+ * of one slot need not be neighbours. Asynchronous on `stream`.
+ * Errors: NULL, RANGE (M outside [1, max_rows]), ALIGN (ids not 4-byte aligned),
+ * MISMATCH (device), CUDA. */
+int dictproj_rows_set(dictproj_rows* rows, const int* ids, int M, void* stream);
+
+/* Y = base + the adapters' part, over the M rows of the plan's last
+ * dictproj_rows_set: X device fp16 [M][d_in], base and Y device fp16 [M][d_out].
+ * base may be Y itself (the result of a dictproj_forward*: rows without an adapter
+ * are then not touched at all) or NULL (base = 0); rows without an adapter get
+ * base. T is summed in fp32 and used in two fp16 parts (22 bits or more); Y is
+ * rounded once. Masked or unused rows do not reach other rows: an infinity or NaN
+ * stays in its own row. Asynchronous on `stream`; one launch.
+ * Errors: NULL, RANGE (no rows planned, more than the pool's max_tokens, the plan
+ * made for another n_slots, Y overlapping X, or overlapping base without being
+ * base), ALIGN (16 bytes), MISMATCH (device), CUDA. */
+int dictproj_adapter_forward(const dictproj_adapters* a, const dictproj_rows* rows, const void* X, const void* base,
+                             void* Y, void* stream);
+
+/* The whole layer: Y = X D C (dictproj_forward) plus the adapters of the plan's
+ * rows. Everything is validated before the first launch. The projection's result
+ * is rounded to fp16 before the adapters' part is added and rounded again.
+ * Errors: those of dictproj_forward (M = the plan's rows) and of
+ * dictproj_adapter_forward, MISMATCH (pool and projection differ in d_in or d_out). */
+int dictproj_forward_adapters(const void* X, const dictproj_layer* layer, const dictproj_group* group,
+                              const dictproj_adapters* a, const dictproj_rows* rows, void* Y, void* stream);
+
+/* Gradients of dictproj_adapter_forward, with U[m] = dY[m] B_s^T:
+ *
+ *     dX[m] = base[m] + scale_s U[m] A_s
+ *     dA_s (+)= scale_s sum_{m of slot s} U[m]^T X[m]
+ *     dB_s (+)= scale_s sum_{m of slot s} T[m]^T dY[m]
+ *
+ * X, dY device fp16 as above; base and dX device fp16 [M][d_in] with base as in
+ * the forward (the input gradient of the projection itself, dictproj_backward_input,
+ * in the same buffer, or elsewhere, or NULL for 0); dA device fp32
+ * [n_slots][max_rank][d_in], dB device fp32 [n_slots][max_rank][d_out].
+ * accumulate == 0 overwrites every element of dA and dB: zero where a slot has no
+ * rows in the batch and past a slot's rank. accumulate != 0 adds. dX may be NULL
+ * (no input gradient) and dA and dB may both be NULL (only dX); not all three. The
+ * sums run in fp32 in a fixed order: repeated calls give the same bits.
+ * Asynchronous on `stream`. Errors as dictproj_adapter_forward (dX must not overlap
+ * X or dY, dA and dB must not overlap anything), NULL also when only one of dA, dB
+ * is given. */
+int dictproj_adapter_backward(const dictproj_adapters* a, const dictproj_rows* rows, const void* X, const void* dY,
+                              const void* base, void* dX, float* dA, float* dB, int accumulate, void* stream);
+
+/* Reserve what dictproj_backward_input needs for layers with up to max_d_out
+ * columns: the prefill coefficient scratch (dictproj_group_reserve_prefill) and
+ * the group's dense dictionary, fp16 [k][d_in] (2 * k * d_in bytes). Errors as
+ * dictproj_group_reserve_prefill. */
+int dictproj_group_reserve_backward(dictproj_group* g, int max_d_out);
+
+/* Input gradient of the frozen projection Y = X D C: dX = dY C^T D^T, dY device
+ * fp16 [M][d_out], dX device fp16 [M][d_in], 1 <= M <= max_tokens, d_out % 8 == 0.
+ * Every layer format is served. dZ = s_C dY C^T and dX = s_D dZ D^T are tensor-core
+ * products with fp32 accumulation; dZ is rounded to fp16 between them, as the
+ * prefill forward rounds Z (gradients below 2^-24 of it are lost: scale the loss).
+ * Asynchronous on `stream`, uses the group's scratch (one stream at a time).
+ * Errors: NULL, RANGE (M, or not reserved), SHAPE (d_out % 8), MISMATCH, ALIGN
+ * (dY, dX 16 bytes), CUDA. */
+int dictproj_backward_input(const void* dY, int M, const dictproj_layer* layer, const dictproj_group* group,
+                            void* dX, void* stream);
+
+/* AdamW over many tensors in one launch (the adapters of a whole stack are some
+ * hundred small tensors). All arithmetic is IEEE fp32, in this order, every
+ * operation rounded on its own:
+ *
+ *     g = grad * grad_scale
+ *     m' = m * beta1 + g * (1 - beta1)
+ *     v' = v * beta2 + (g * (1 - beta2)) * g
+ *     r' = sqrt(v')
+ *     p' = p * (1 - lr * weight_decay)
+ *          - (m' / (r' * (1 / sqrt(1 - beta2^step)) + eps)) * (lr / (1 - beta1^step))
+ *
+ * with the factors of the step, the beta and the lr computed in fp64 and rounded
+ * to fp32. copy (may be NULL) gets p' rounded to fp16: the working weights, e.g. a
+ * pool's slot.
+ *
+ * state_bits 32: m and v are fp32 arrays of n elements.
+ * state_bits 8: m is E4M3 codes uint8[n] with one fp32 scale per
+ *   DICTPROJ_ADAMW_BLOCK consecutive elements (of the tensor, the last block may be
+ *   short): value = code * scale, scale' = max(amax|m'| * (1 / 448), 2^-126), code' = the
+ *   E4M3 value nearest to m' / scale' (ties to even). v is held as r = sqrt(v),
+ *   v = r * r, in E4M3 codes with its own scales, scale' as for m from r'. A second
+ *   moment moves by a thousandth per step, far below half an 8-bit step, so r' is
+ *   rounded up or down in proportion to where it lies between two codes: code' =
+ *   (bits(r' / scale' * 2^-120) + d) >> 20, at most 0x7E and at least 1 where r' >
+ *   0, with d the 20 top bits of a hash of the element's number i in its tensor and
+ *   the step (all mod 2^32): h = i * 0x9E3779B9 + step * 0x6A09E667; h ^= h >> 16;
+ *   h *= 0xBB67AE85; h ^= h >> 15; h *= 0x6A09E667; d = h >> 12. The same inputs
+ *   give the same bits.
+ * A gradient that is not finite spreads into its element, and with 8-bit states
+ * into its block: check before the step.
+ *
+ * p, g, m, v (32 bits) and the scales must be 4-byte aligned, copy 2-byte; 16-byte
+ * alignment of all (4 for the codes) is faster. No two tensors may overlap. */
+#define DICTPROJ_ADAMW_BLOCK 128
+typedef struct dictproj_adamw_tensor {
+  float* p;          /* [n] master weights */
+  const float* g;    /* [n] gradients */
+  void* m;           /* [n] fp32, or uint8 E4M3 codes */
+  void* v;           /* [n] fp32, or uint8 E4M3 codes of sqrt(v) */
+  float* m_scale;    /* 8 bits: [ceil(n / 128)] */
+  float* v_scale;    /* 8 bits: [ceil(n / 128)] */
+  void* copy;        /* fp16 [n] or NULL */
+  long long n;       /* 0 <= n < 2^32 */
+} dictproj_adamw_tensor;
+typedef struct dictproj_adamw dictproj_adamw;
+
+/* Keep a table of the tensors on the current device (the tensors stay the
+ * caller's). Errors: NULL (an array, or a pointer of a tensor with n > 0), RANGE
+ * (n_tensors outside [1, 2^20], n, state_bits not 8 or 32, more than 2^31 - 1
+ * chunks of 2048 elements in all), ALIGN, OOM, CUDA. */
+int dictproj_adamw_create(const dictproj_adamw_tensor* tensors, int n_tensors, int state_bits, dictproj_adamw** out);
+void dictproj_free_adamw(dictproj_adamw* w); /* NULL is a no-op */
+
+/* One step of all tensors. step >= 1 counts from 1 and is taken by value: a
+ * captured call repeats the same step number. Asynchronous on `stream`.
+ * Errors: NULL, RANGE (step < 1, a beta outside [0, 1), eps < 0 or lr,
+ * weight_decay < 0), VALUE (a factor not finite), MISMATCH (device), CUDA. */
+int dictproj_adamw_step(const dictproj_adamw* w, long long step, double lr, double beta1, double beta2, double eps,
+                        double weight_decay, double grad_scale, void* stream);
+
+/* ------------------------------------------------------------------------- */
 /* Forward without allocation                                                 */
 /* ------------------------------------------------------------------------- */
 
