@@ -5,8 +5,14 @@
 //   dA_s = scale_s sum_m U[m]^T X[m],  dB_s = scale_s sum_m T[m]^T dY[m]
 //
 // A and B are stored rank-major ([rank][d_in], [rank][d_out]), so the forward and
-// the input gradient are one kernel with A and B exchanged: a contraction along
-// the rows of the first, an expansion along the rows of the second.
+// the input gradient are one kernel with A and B exchanged (k_adapter_rows): a
+// contraction along the rows of the first, an expansion along the rows of the
+// second. Both weight gradients are one kernel as well (k_adapter_grad).
+//
+// All of them move far more bytes than the legacy tensor path (mma.sync) needs time
+// for: a row of d elements is read or written once for 2 r d multiply-adds, and r is
+// at most 128. tcgen05 would need tiles of 128 rows of one slot, which a batch of
+// many requests does not have.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -24,6 +30,7 @@ namespace {
 // histogram (equal lanes found by match), a scan over (slot, warp) turns the counts
 // into positions, and the second pass over the ids scatters in row order, so the
 // result does not depend on timing. Bucket n_slots takes the rows without a slot.
+// Then the slots' rows are cut into tiles of 16 and of 64.
 constexpr int kPlanWarps = 32;
 
 __device__ __forceinline__ int plan_bucket(const int* ids, int m, int n_slots) {
@@ -31,11 +38,38 @@ __device__ __forceinline__ int plan_bucket(const int* ids, int m, int n_slots) {
   return id >= 0 && id < n_slots ? id : n_slots;
 }
 
+// Exclusive sum over the CTA's threads; *total gets the whole sum.
+__device__ __forceinline__ int block_exclusive_sum(int x, int* wsum, int* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int incl = x;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += t;
+  }
+  __syncthreads();  // wsum may still be read
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < kPlanWarps; ++w) {
+    const int s = wsum[w];
+    before += w < warp ? s : 0;
+    all += s;
+  }
+  *total = all;
+  return before + incl - x;
+}
+
 __global__ void __launch_bounds__(kPlanWarps * 32)
-    k_rows_plan(const int* __restrict__ ids, int M, int n_slots, int* __restrict__ perm, int* __restrict__ start) {
-  extern __shared__ int hist[];  // [kPlanWarps][n_slots + 1]
+    k_rows_plan(const int* __restrict__ ids, int M, int n_slots, int* __restrict__ perm, int* __restrict__ start,
+                int* __restrict__ n_tiles, int4* __restrict__ tiles16, int4* __restrict__ tiles64,
+                int* __restrict__ first64) {
+  extern __shared__ int plan_smem[];
   __shared__ int wsum[kPlanWarps];
   const int nb = n_slots + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* hist = plan_smem;                    // [kPlanWarps][nb]
+  int* begin = hist + kPlanWarps * nb;      // [nb + 1] first position of each bucket
+  int* tfirst = begin + nb + 1;             // [2][nb + 1] first tile of each bucket
   grid_dependency_wait();
   for (int i = threadIdx.x; i < kPlanWarps * nb; i += blockDim.x) hist[i] = 0;
   __syncthreads();
@@ -51,46 +85,47 @@ __global__ void __launch_bounds__(kPlanWarps * 32)
     __syncwarp();
   }
   __syncthreads();
-  // counts -> positions: per bucket over the warps, then over the buckets. The last
-  // bucket (no slot) starts where the slots' total ends.
-  int total = 0;
-  if ((int)threadIdx.x < n_slots)
+  // counts -> positions: per bucket over the warps, then over the buckets; the
+  // bucket without a slot comes last, behind the total of the others
+  const int s = threadIdx.x;
+  int count = 0;
+  if (s < n_slots)
     for (int w = 0; w < kPlanWarps; ++w) {
-      const int c = hist[w * nb + threadIdx.x];
-      hist[w * nb + threadIdx.x] = total;
-      total += c;
+      const int c = hist[w * nb + s];
+      hist[w * nb + s] = count;
+      count += c;
     }
-  int incl = total;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += t;
-  }
-  if (lane == 31) wsum[warp] = incl;
-  __syncthreads();
-  if (warp == 0) {
-    int s = wsum[lane];
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, s, off);
-      if (lane >= off) s += t;
-    }
-    wsum[lane] = s;
-  }
-  __syncthreads();
-  const int first = incl - total + (warp ? wsum[warp - 1] : 0);
-  if ((int)threadIdx.x < n_slots) {
-    start[threadIdx.x] = first;
-    for (int w = 0; w < kPlanWarps; ++w) hist[w * nb + threadIdx.x] += first;
+  int live;
+  const int first = block_exclusive_sum(count, wsum, &live);
+  if (s < n_slots) {
+    start[s] = begin[s] = first;
+    for (int w = 0; w < kPlanWarps; ++w) hist[w * nb + s] += first;
   }
   if (threadIdx.x == 0) {
-    int at = wsum[kPlanWarps - 1];
-    start[n_slots] = at;
-    start[n_slots + 1] = M;
+    start[n_slots] = begin[n_slots] = live;
+    start[n_slots + 1] = begin[nb] = M;
+    int at = live;
     for (int w = 0; w < kPlanWarps; ++w) {
       const int c = hist[w * nb + n_slots];
       hist[w * nb + n_slots] = at;
       at += c;
+    }
+  }
+  int last[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int T = q ? 64 : 16;
+    const int f = block_exclusive_sum((count + T - 1) / T, wsum, &last[q]);
+    if (s < n_slots) {
+      tfirst[q * (nb + 1) + s] = f;
+      if (q) first64[s] = f;
+    }
+    if (threadIdx.x == 0) {
+      const int all = last[q] + (M - live + T - 1) / T;
+      tfirst[q * (nb + 1) + n_slots] = last[q];
+      tfirst[q * (nb + 1) + nb] = all;
+      n_tiles[2 * q] = last[q];
+      n_tiles[2 * q + 1] = all;
     }
   }
   __syncthreads();
@@ -104,17 +139,22 @@ __global__ void __launch_bounds__(kPlanWarps * 32)
     if (in && lane == __ffs(eq) - 1) h[b] += __popc(eq);
     __syncwarp();
   }
-}
-
-// Slot that owns plan position p (n_slots: no adapter): the last s with start[s] <= p.
-__device__ __forceinline__ int slot_at(const int* start, int n_slots, int p) {
-  int lo = 0, hi = n_slots;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (start[mid] <= p) lo = mid;
-    else hi = mid - 1;
+  __syncthreads();  // the tiles name row numbers of perm
+  for (int q = 0; q < 2; ++q) {
+    const int T = q ? 64 : 16;
+    const int* tf = tfirst + q * (nb + 1);
+    int4* tiles = q ? tiles64 : tiles16;
+    for (int t = threadIdx.x; t < tf[nb]; t += blockDim.x) {
+      int a = 0, z = n_slots;  // the last bucket whose first tile is <= t (an empty bucket owns none)
+      while (a < z) {
+        const int mid = (a + z + 1) >> 1;
+        if (tf[mid] <= t) a = mid;
+        else z = mid - 1;
+      }
+      const int p = begin[a] + (t - tf[a]) * T;
+      tiles[t] = make_int4(a, p, min(T, begin[a + 1] - p), perm[p]);
+    }
   }
-  return lo;
 }
 
 // Copy an adapter into its slot, with zeros past its rank and past d_out.
@@ -135,100 +175,640 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// ---- simple kernels -----------------------------------------------------------------
-// T[p][j] = factor * In[row p] . P_s[j], one warp per (position, j)
-__global__ void __launch_bounds__(256)
-    k_contract(const __half* __restrict__ in, int K, const __half* __restrict__ P, int ld_p, int rp, int n_slots,
-               const int* __restrict__ rank, const float* __restrict__ scale, const int* __restrict__ perm,
-               const int* __restrict__ start, float* __restrict__ t) {
-  grid_dependency_wait();
-  const int p = blockIdx.x, s = slot_at(start, n_slots, p);
-  if (s >= n_slots) return;
-  const int r = rank[s], warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const __half* x = in + (size_t)perm[p] * K;
-  for (int j = warp; j < rp; j += 8) {
-    float acc = 0.f;
-    const __half* w = P + ((size_t)s * rp + j) * ld_p;
-    if (j < r)
-      for (int i = lane; i < K; i += 32) acc = fmaf(__half2float(x[i]), __half2float(w[i]), acc);
+// ---- helpers ------------------------------------------------------------------------
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t peer_smem(uint32_t local, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_peer_v4f(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_peer_v4f(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+// 16 bytes global -> shared, the last 16 - bytes of them zeros
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint32_t half2_bits(__half a, __half b) {
+  const __half2 h = __halves2half2(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Byte offset of 16-byte piece p of row `row` in a tile of PITCH-byte rows whose
+// pieces are permuted so that 8 rows' pieces of one column lie in different banks.
+template <int PITCH>
+__device__ __forceinline__ uint32_t swz(int row, int p) {
+  constexpr int per = PITCH / 16, shift = PITCH >= 128 ? 0 : PITCH == 64 ? 1 : 2, mask = per >= 8 ? 7 : per - 1;
+  return (uint32_t)(row * PITCH + 16 * (p ^ ((row >> shift) & mask)));
+}
+
+// 8 elements from column c of a row of n elements into shared memory, zeros past the
+// end; asynchronously where rows keep 16-byte alignment (vec: n % 8 == 0).
+__device__ __forceinline__ void load_piece(uint32_t dst, const __half* row, int c, int n, bool vec) {
+  if (vec) {
+    const bool in = c < n;
+    cp_async16(dst, in ? row + c : row, in ? 16 : 0);
+  } else {
+    uint32_t w[4];
 #pragma unroll
-    for (int off = 16; off; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-    if (lane == 0) t[(size_t)p * rp + j] = acc * scale[s];
+    for (int i = 0; i < 4; ++i) {
+      const unsigned short a = c + 2 * i < n ? __half_as_ushort(row[c + 2 * i]) : 0;
+      const unsigned short b = c + 2 * i + 1 < n ? __half_as_ushort(row[c + 2 * i + 1]) : 0;
+      w[i] = (uint32_t)a | ((uint32_t)b << 16);
+    }
+    sts16(dst, make_uint4(w[0], w[1], w[2], w[3]));
   }
 }
 
-// out[row p][n] = base + sum_j T[p][j] Q_s[j][n]
-__global__ void __launch_bounds__(256)
-    k_expand(const float* __restrict__ t, const __half* __restrict__ Q, int ld_q, int N, int rp, int n_slots,
-             const int* __restrict__ rank, const int* __restrict__ perm, const int* __restrict__ start,
-             const __half* __restrict__ base, __half* __restrict__ out) {
-  grid_dependency_wait();
-  const int p = blockIdx.x, s = slot_at(start, n_slots, p), n = blockIdx.y * 256 + threadIdx.x;
-  if (n >= N) return;
-  const size_t at = (size_t)perm[p] * N + n;
-  const int r = s < n_slots ? rank[s] : 0;
-  if (r == 0 && base == out) return;
-  float acc = base ? __half2float(base[at]) : 0.f;
-  for (int j = 0; j < r; ++j)
-    acc = fmaf(t[(size_t)p * rp + j], __half2float(Q[((size_t)s * rp + j) * ld_q + n]), acc);
-  out[at] = __float2half_rn(acc);
+// T in two fp16 parts: t * unit = high + low with |t * unit| < 2^14, so that the two
+// together keep 22 bits of it, or 2^-24 absolute (2^-38 of the tile's largest): the
+// MMA's fp16 operands then carry T as exactly as the fp32 sums that made it, whatever
+// its size. unit is a power of two.
+struct Split {
+  __half hi, lo;
+};
+__device__ __forceinline__ Split split_half(float t) {
+  Split s;
+  s.hi = __float2half_rn(t);
+  s.lo = __hisinf(s.hi) ? __float2half_rn(0.f) : __float2half_rn(t - __half2float(s.hi));
+  return s;
+}
+// 2^13 / 2^floor(log2 m), within fp32's normal range; 1 for m = 0.
+__device__ __forceinline__ float split_unit(float m) {
+  if (m == 0.f) return 1.f;
+  const int e = (int)((__float_as_uint(m) >> 23) & 255) - 127;  // -127 for a subnormal
+  return __uint_as_float((uint32_t)(min(13 - e, 126) + 127) << 23);
 }
 
-// G_s[j][i] (+)= sum over the slot's rows of T[p][j] In[row p][i]
-__global__ void __launch_bounds__(256)
-    k_weight_grad(const float* __restrict__ t, const __half* __restrict__ in, int K, int rp, int max_rank, int n_slots,
-                  const int* __restrict__ rank, const int* __restrict__ perm, const int* __restrict__ start,
-                  int accumulate, float* __restrict__ g) {
+// ---- rows: contraction and expansion in one launch --------------------------------------
+// A cluster of kCluster CTAs takes one tile of up to TM rows of one slot:
+//   1. CTA c contracts its share of the K columns of In with P_s (TM x K by K x r, warps
+//      split over rows and over the 16-column steps), summed over the warps in order;
+//   2. the CTAs' partial sums meet through distributed shared memory, in rank order;
+//   3. CTA c expands T into its share of the N columns of Out, adding base.
+// One ring of CW-column stages (cp.async) runs through both phases, so that the first
+// Q and base tiles arrive while T is being summed.
+constexpr int kCluster = 8;
+constexpr int kRowThreads = 256;
+
+struct RowsPass {
+  const __half* in;
+  const __half* P;
+  const __half* Q;
+  const __half* base;
+  __half* out;
+  __half* hi;  // parts of scale * T for the weight gradients, or null
+  __half* lo;
+  float* unit;
+  int K, N, ld_p, ld_q;
+};
+struct RowsArgs {
+  RowsPass pass[2];
+  const int* n_tiles;
+  const int4* tiles;
+  const int* perm;
+  const int* rank;
+  const float* scale;
+  int rp, n_slots;
+};
+
+template <int TM, int R>
+struct RowsShape {
+  static constexpr int CW = TM == 16 ? 128 : 64;  // columns of a stage
+  static constexpr int kPitch = 2 * CW;
+  static constexpr int kStages = R == 128 ? 3 : 4;
+  static constexpr int kInBytes = TM * kPitch, kStageBytes = (TM + R) * kPitch;
+  static constexpr int kRedBytes = TM == 16 ? 8 * TM * R * 4 : 0;  // the warps' sums
+  static constexpr int kPart = kStages * kStageBytes, kFull = kPart + TM * R * 4, kRed = kFull + TM * R * 4;
+  static constexpr int smem = kRed + kRedBytes;
+};
+
+template <int TM, int R>
+__global__ void __launch_bounds__(kRowThreads) k_adapter_rows(const __grid_constant__ RowsArgs g) {
+  using S = RowsShape<TM, R>;
+  constexpr int CW = S::CW, PITCH = S::kPitch, PIECES = PITCH / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int srow[TM];
+  __shared__ float smax[kRowThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rankc = blockIdx.x % kCluster, tile_no = blockIdx.x / kCluster;
+  const RowsPass& a = g.pass[blockIdx.y];
+  float* part = reinterpret_cast<float*>(smem + S::kPart);
+  float* full = reinterpret_cast<float*>(smem + S::kFull);
+  const uint32_t ring = smem_u32(smem);
+
   grid_dependency_wait();
-  const int i = blockIdx.x * 256 + threadIdx.x, j = blockIdx.y, s = blockIdx.z;
-  if (i >= K) return;
-  float acc = 0.f;
-  if (j < rank[s])
-    for (int p = start[s]; p < start[s + 1]; ++p)
-      acc = fmaf(t[(size_t)p * rp + j], __half2float(in[(size_t)perm[p] * K + i]), acc);
-  float* o = g + ((size_t)s * max_rank + j) * K + i;
-  *o = accumulate ? *o + acc : acc;
+  // rows whose output is already in place need no tile of their own
+  const bool in_place = a.out == nullptr || a.base == a.out;
+  const int4 tile = g.tiles[tile_no];
+  if (tile_no >= g.n_tiles[in_place ? 0 : 1]) return;  // the whole cluster
+  const int count = tile.z, slot = tile.x;
+  const int r = slot < g.n_slots ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
+  if (tid < TM) srow[tid] = tid < count ? g.perm[tile.y + tid] : 0;
+  const bool vec_in = (a.K & 7) == 0, vec_out = (a.N & 7) == 0;
+  const int kc = (a.K + CW - 1) / CW, nc = a.out ? (a.N + CW - 1) / CW : 0;
+  const int n_lo = nc * rankc / kCluster, nn = nc * (rankc + 1) / kCluster - n_lo;
+  __syncthreads();
+  if (r == 0) {  // base alone
+    if (!in_place)
+      for (int i = tid; i < count * nn * CW; i += kRowThreads) {
+        const int row = i / (nn * CW), c = n_lo * CW + i % (nn * CW);
+        if (c < a.N) {
+          const size_t at = (size_t)srow[row] * a.N + c;
+          a.out[at] = a.base ? a.base[at] : __float2half_rn(0.f);
+        }
+      }
+    return;
+  }
+  const float scale = g.scale[slot];
+  const int k_lo = kc * rankc / kCluster, nk = kc * (rankc + 1) / kCluster - k_lo;
+  const __half* P = a.P + (size_t)slot * g.rp * a.ld_p;
+  const __half* Q = a.Q + (size_t)slot * g.rp * a.ld_q;
+  // rows past the tile's stay zero in every stage
+  for (int i = tid; i < S::kStages * (TM - count) * PIECES; i += kRowThreads) {
+    const int st = i / ((TM - count) * PIECES), row = count + i / PIECES % (TM - count);
+    sts16(ring + st * S::kStageBytes + swz<PITCH>(row, i % PIECES), make_uint4(0, 0, 0, 0));
+  }
+  auto issue = [&](int i) {
+    if (i < nk + nn) {
+      const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
+      const bool first = i < nk;
+      const int col = first ? (k_lo + i) * CW : (n_lo + i - nk) * CW;
+      const __half* src = first ? a.in : a.base;
+      const int n = first ? a.K : a.N;
+      if (src)
+        for (int q = tid; q < count * PIECES; q += kRowThreads) {
+          const int row = q / PIECES, p = q % PIECES;
+          load_piece(st + swz<PITCH>(row, p), src + (size_t)srow[row] * n, col + 8 * p, n, first ? vec_in : vec_out);
+        }
+      const __half* w = first ? P : Q;
+      const int ld = first ? a.ld_p : a.ld_q;
+      for (int q = tid; q < r16 * PIECES; q += kRowThreads) {
+        const int row = q / PIECES, p = q % PIECES;
+        load_piece(st + S::kInBytes + swz<PITCH>(row, p), w + (size_t)row * ld, col + 8 * p, ld, true);
+      }
+    }
+    cp_async_commit();
+  };
+  for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+
+  const int rg = TM == 64 ? warp & 3 : 0, half = TM == 64 ? warp >> 2 : 0;
+  {  // 1. contraction
+    float acc[R / 8][4];
+#pragma unroll
+    for (int t = 0; t < R / 8; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+    for (int i = 0; i < nk; ++i) {
+      cp_async_wait<S::kStages - 2>();
+      __syncthreads();
+      issue(i + S::kStages - 1);
+      const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
+#pragma unroll
+      for (int kk = 0; kk < (TM == 64 ? 2 : 1); ++kk) {
+        const int k16 = TM == 64 ? half * 2 + kk : warp;
+        uint32_t af[4];
+        ldmatrix4(af, st + swz<PITCH>(rg * 16 + (lane & 15), 2 * k16 + (lane >> 4)));
+#pragma unroll
+        for (int t = 0; t < R / 16; ++t) {
+          if (16 * t >= r16) break;
+          uint32_t bf[4];
+          ldmatrix4(bf, st + S::kInBytes + swz<PITCH>(16 * t + (lane & 7) + (lane >> 4) * 8, 2 * k16 + ((lane >> 3) & 1)));
+          mma_16816(acc[2 * t], af, bf);
+          mma_16816(acc[2 * t + 1], af, bf + 2);
+        }
+      }
+    }
+    // the CTA's sum, warps in order
+    const int g0 = lane >> 2, c0 = 2 * (lane & 3);
+    if constexpr (TM == 16) {
+      float* red = reinterpret_cast<float*>(smem + S::kRed) + warp * TM * R;
+#pragma unroll
+      for (int t = 0; t < R / 8; ++t) {
+        *reinterpret_cast<float2*>(red + g0 * R + 8 * t + c0) = make_float2(acc[t][0], acc[t][1]);
+        *reinterpret_cast<float2*>(red + (g0 + 8) * R + 8 * t + c0) = make_float2(acc[t][2], acc[t][3]);
+      }
+      __syncthreads();
+      const float* all = reinterpret_cast<const float*>(smem + S::kRed);
+      for (int i = tid; i < count * R; i += kRowThreads) {
+        float x = all[i];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) x += all[w * TM * R + i];
+        part[i] = x;
+      }
+    } else {
+      float* mine = part + (rg * 16) * R;
+#pragma unroll 1
+      for (int h = 1; h >= 0; --h) {
+        if (half == h)
+#pragma unroll
+          for (int t = 0; t < R / 8; ++t) {
+            float2* lo = reinterpret_cast<float2*>(mine + g0 * R + 8 * t + c0);
+            float2* hi = reinterpret_cast<float2*>(mine + (g0 + 8) * R + 8 * t + c0);
+            const float2 x = h ? make_float2(0.f, 0.f) : *lo, y = h ? make_float2(0.f, 0.f) : *hi;
+            *lo = make_float2(acc[t][0] + x.x, acc[t][1] + x.y);
+            *hi = make_float2(acc[t][2] + y.x, acc[t][3] + y.y);
+          }
+        __syncthreads();
+      }
+    }
+  }
+  cluster_arrive();
+  cluster_wait();
+  // 2. the cluster's sum: scale * T, zero past the slot's rank
+  const uint32_t pbase = smem_u32(part), fbase = smem_u32(full);
+  auto summed = [&](int i) {  // four elements of the tile, CTAs in order
+    float4 x = ld_peer_v4f(peer_smem(pbase + 4 * i, 0));
+#pragma unroll
+    for (int c = 1; c < kCluster; ++c) {
+      const float4 y = ld_peer_v4f(peer_smem(pbase + 4 * i, c));
+      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    const int j = i % R;
+    return make_float4(j < r ? x.x * scale : 0.f, j + 1 < r ? x.y * scale : 0.f, j + 2 < r ? x.z * scale : 0.f,
+                       j + 3 < r ? x.w * scale : 0.f);
+  };
+  if constexpr (TM == 16) {  // few elements: every CTA sums all of them
+    for (int i = 4 * tid; i < TM * R; i += 4 * kRowThreads)
+      *reinterpret_cast<float4*>(full + i) = i < count * R ? summed(i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    cluster_arrive();  // waited for at the end: no CTA leaves while its sums are read
+  } else {  // each CTA sums its rows for all
+    constexpr int share = TM * R / kCluster;
+    for (int i = rankc * share + 4 * tid; i < (rankc + 1) * share; i += 4 * kRowThreads) {
+      const float4 x = summed(i);
+#pragma unroll
+      for (int c = 0; c < kCluster; ++c) st_peer_v4f(peer_smem(fbase + 4 * i, c), x);
+    }
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (TM == 16) __syncthreads();
+  float m = 0.f;
+  for (int i = tid; i < count * R; i += kRowThreads) {
+    const float x = fabsf(full[i]);
+    if (x <= 3.0e38f) m = fmaxf(m, x);  // an infinity or NaN does not decide the others' digits
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if (lane == 0) smax[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kRowThreads / 32; ++w) m = fmaxf(m, smax[w]);
+  const float unit = split_unit(m), back = 1.f / unit;
+  if (a.hi) {  // T for the weight gradients: this CTA's share of the rows
+    for (int i = tid; i < count * r16; i += kRowThreads) {
+      const int row = i / r16, j = i % r16;
+      if (row % kCluster != rankc) continue;
+      const Split s = split_half(full[row * R + j] * unit);
+      const size_t at = (size_t)(tile.y + row) * g.rp + j;
+      a.hi[at] = s.hi;
+      a.lo[at] = s.lo;
+    }
+    if (rankc == 0 && tid == 0) a.unit[tile_no] = back;
+  }
+  // 3. expansion
+  if (nn > 0) {
+    uint32_t thi[R / 16][4], tlo[R / 16][4];
+    const int g0 = rg * 16 + (lane >> 2), c0 = 2 * (lane & 3);
+#pragma unroll
+    for (int t = 0; t < R / 16; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float* f = full + (g0 + 8 * (q & 1)) * R + 16 * t + c0 + 8 * (q >> 1);
+        const Split x = split_half(f[0] * unit), y = split_half(f[1] * unit);
+        thi[t][q] = half2_bits(x.hi, y.hi);
+        tlo[t][q] = half2_bits(x.lo, y.lo);
+      }
+    constexpr int NT = TM == 64 ? 4 : 2;  // 8-column tiles of a warp in a stage
+    const int cw = TM == 64 ? 32 * half : 16 * warp;
+    for (int i = nk; i < nk + nn; ++i) {
+      cp_async_wait<S::kStages - 2>();
+      __syncthreads();
+      issue(i + S::kStages - 1);
+      const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
+      float acc[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+#pragma unroll
+      for (int t = 0; t < R / 16; ++t) {
+        if (16 * t >= r16) break;
+#pragma unroll
+        for (int n = 0; n < NT / 2; ++n) {
+          uint32_t bf[4];
+          ldmatrix4_t(bf, st + S::kInBytes + swz<PITCH>(16 * t + (lane & 15), cw / 8 + 2 * n + (lane >> 4)));
+          mma_16816(acc[2 * n], tlo[t], bf);
+          mma_16816(acc[2 * n], thi[t], bf);
+          mma_16816(acc[2 * n + 1], tlo[t], bf + 2);
+          mma_16816(acc[2 * n + 1], thi[t], bf + 2);
+        }
+      }
+      // base + acc, rounded once, over the base tile, then out in 16-byte pieces
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t at = st + swz<PITCH>(g0 + 8 * q, cw / 8 + n) + 2 * c0;
+          const uint32_t bw = a.base ? lds_u32(at) : 0u;
+          const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&bw));
+          const __half2 o = __floats2half2_rn(fmaf(acc[n][2 * q], back, b.x), fmaf(acc[n][2 * q + 1], back, b.y));
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(*reinterpret_cast<const uint32_t*>(&o)) : "memory");
+        }
+      __syncthreads();
+      const int col = (n_lo + i - nk) * CW;
+      for (int q = tid; q < count * PIECES; q += kRowThreads) {
+        const int row = q / PIECES, c = col + 8 * (q % PIECES);
+        __half* dst = a.out + (size_t)srow[row] * a.N + c;
+        const uint4 v = lds_u32x4(st + swz<PITCH>(row, q % PIECES));
+        if (vec_out) {
+          if (c < a.N) *reinterpret_cast<uint4*>(dst) = v;
+        } else {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + e < a.N) dst[e] = __ushort_as_half((unsigned short)(w[e >> 1] >> (16 * (e & 1))));
+        }
+      }
+    }
+  }
+  cp_async_wait<0>();
+  if (TM == 16) cluster_wait();
 }
 
-cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, void** args) {
+// ---- weight gradients --------------------------------------------------------------------
+// G_s[j][i] (+)= sum over the slot's rows of (scale T)[p][j] In[row p][i]: r x rows by
+// rows x kGradCols. A CTA owns kGradCols columns of one slot's gradient; a cluster
+// splits the slot's 64-row tiles and sums through distributed shared memory in rank
+// order. Per tile the products of T's two parts are accumulated by the MMA and then
+// added, times the tile's unit, to fp32 sums: a long sum is rounded to nearest once a
+// tile, not truncated at each MMA.
+constexpr int kGradCols = 128;
+constexpr int kGradThreads = 256;
+
+struct GradPass {
+  const __half* in;
+  const __half* hi;
+  const __half* lo;
+  const float* unit;
+  float* g;
+  int K, blocks;
+};
+struct GradArgs {
+  GradPass pass[2];
+  const int* start;
+  const int* first64;
+  const int* perm;
+  const int* rank;
+  int rp, max_rank, accumulate;
+};
+
+template <int R>
+struct GradShape {
+  static constexpr int kStages = 3, kInPitch = 2 * kGradCols, kTPitch = 2 * R;
+  static constexpr int kInBytes = 64 * kInPitch, kTBytes = 64 * kTPitch;
+  static constexpr int kStageBytes = kInBytes + 2 * kTBytes;
+  static constexpr int smem = kStages * kStageBytes > R * kGradCols * 4 ? kStages * kStageBytes : R * kGradCols * 4;
+};
+
+template <int R>
+__global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_constant__ GradArgs g) {
+  using S = GradShape<R>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = blockIdx.z, nsplit = gridDim.z, slot = blockIdx.y;
+  const int which = (int)blockIdx.x < g.pass[0].blocks ? 0 : 1;
+  const GradPass& a = g.pass[which];
+  const int col0 = ((int)blockIdx.x - (which ? g.pass[0].blocks : 0)) * kGradCols;
+  const uint32_t ring = smem_u32(smem);
+  grid_dependency_wait();
+  const int p0 = g.start[slot], rows = g.start[slot + 1] - p0, tile0 = g.first64[slot];
+  const int r = rows ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
+  float* out = a.g + (size_t)slot * g.max_rank * a.K;
+  const int width = min(kGradCols, a.K - col0);
+  if (r == 0) {
+    if (!g.accumulate)
+      for (int i = split * kGradThreads + tid; i < g.max_rank * width; i += nsplit * kGradThreads)
+        out[(size_t)(i / width) * a.K + col0 + i % width] = 0.f;
+    return;
+  }
+  const int nt_all = (rows + 63) / 64, t_lo = (int)((long)nt_all * split / nsplit);
+  const int nt = (int)((long)nt_all * (split + 1) / nsplit) - t_lo;
+  const bool vec = (a.K & 7) == 0;
+  auto issue = [&](int i) {
+    if (i < nt) {
+      const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
+      const int p = p0 + (t_lo + i) * 64, left = rows - (t_lo + i) * 64;
+      for (int q = tid; q < 64 * (S::kInPitch / 16); q += kGradThreads) {
+        const int row = q / (S::kInPitch / 16), c = q % (S::kInPitch / 16);
+        const uint32_t dst = st + swz<S::kInPitch>(row, c);
+        if (row < left) load_piece(dst, a.in + (size_t)g.perm[p + row] * a.K, col0 + 8 * c, a.K, vec);
+        else sts16(dst, make_uint4(0, 0, 0, 0));
+      }
+      const int pieces = r16 / 8;
+      for (int q = tid; q < 64 * pieces; q += kGradThreads) {
+        const int row = q / pieces, c = q % pieces;
+        const size_t at = (size_t)(p + min(row, left - 1)) * g.rp + 8 * c;
+        const uint32_t dst = st + S::kInBytes + swz<S::kTPitch>(row, c);
+        cp_async16(dst, a.hi + at, row < left ? 16 : 0);
+        cp_async16(dst + S::kTBytes, a.lo + at, row < left ? 16 : 0);
+      }
+    }
+    cp_async_commit();
+  };
+  for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+  float sum[R / 16][2][4];
+#pragma unroll
+  for (int t = 0; t < R / 16; ++t)
+#pragma unroll
+    for (int n = 0; n < 2; ++n) sum[t][n][0] = sum[t][n][1] = sum[t][n][2] = sum[t][n][3] = 0.f;
+  for (int i = 0; i < nt; ++i) {
+    cp_async_wait<S::kStages - 2>();
+    __syncthreads();
+    issue(i + S::kStages - 1);
+    const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
+    const float unit = a.unit[tile0 + t_lo + i];
+    uint32_t bf[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      ldmatrix4_t(bf[k], st + swz<S::kInPitch>(16 * k + (lane & 15), 2 * warp + (lane >> 4)));
+#pragma unroll
+    for (int t = 0; t < R / 16; ++t) {
+      if (16 * t >= r16) break;
+      float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t hi[4], lo[4];
+        const uint32_t at = st + S::kInBytes + swz<S::kTPitch>(16 * k + (lane & 7) + 8 * (lane >> 4), 2 * t + ((lane >> 3) & 1));
+        ldmatrix4_t(hi, at);
+        ldmatrix4_t(lo, at + S::kTBytes);
+        mma_16816(acc[0], lo, bf[k]);
+        mma_16816(acc[1], lo, bf[k] + 2);
+        mma_16816(acc[0], hi, bf[k]);
+        mma_16816(acc[1], hi, bf[k] + 2);
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum[t][n][q] = fmaf(acc[n][q], unit, sum[t][n][q]);
+    }
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+  float* part = reinterpret_cast<float*>(smem);  // [R][kGradCols], over the drained ring
+  const int g0 = lane >> 2, c0 = 16 * warp + 2 * (lane & 3);
+#pragma unroll
+  for (int t = 0; t < R / 16; ++t)
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<float2*>(part + (16 * t + g0 + 8 * q) * kGradCols + c0 + 8 * n) =
+            make_float2(sum[t][n][2 * q], sum[t][n][2 * q + 1]);
+  if (nsplit > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  // this CTA's share of the gradient's rows; rows past the rank are zero
+  const uint32_t pbase = smem_u32(part);
+  for (int i = split * kGradThreads + tid; i < g.max_rank * (kGradCols / 4); i += nsplit * kGradThreads) {
+    const int j = i / (kGradCols / 4), c = 4 * (i % (kGradCols / 4));
+    if (c >= width) continue;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (j < r)
+      for (int s = 0; s < nsplit; ++s) {
+        const float4 y = nsplit > 1 ? ld_peer_v4f(peer_smem(pbase + 4 * (j * kGradCols + c), s)) : *reinterpret_cast<const float4*>(part + j * kGradCols + c);
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      }
+    float* dst = out + (size_t)j * a.K + col0 + c;
+    if ((a.K & 3) == 0) {
+      if (g.accumulate) {
+        const float4 y = *reinterpret_cast<const float4*>(dst);
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      }
+      *reinterpret_cast<float4*>(dst) = x;
+    } else {
+      const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < width) dst[e] = g.accumulate ? dst[e] + v[e] : v[e];
+    }
+  }
+  if (nsplit > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+
+// ---- launches --------------------------------------------------------------------------
+cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, void** args,
+                       dim3 cluster = dim3(1, 1, 1)) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster.x;
+  attr[1].val.clusterDim.y = cluster.y;
+  attr[1].val.clusterDim.z = cluster.z;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster.x * cluster.y * cluster.z > 1 ? 2 : 1;
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
-cudaError_t contract(const dictproj_adapters* a, const dictproj_rows* r, const __half* in, int K, const uint16_t* P,
-                     int ld_p, float* t, cudaStream_t stream) {
-  int rp = a->rp, ns = a->n_slots;
-  void* args[] = {&in, &K, &P, &ld_p, &rp, &ns, (void*)&a->rank, (void*)&a->scale, (void*)&r->perm, (void*)&r->start, &t};
-  return launch_pdl((const void*)k_contract, dim3(r->M), dim3(256), 0, stream, args);
+template <int TM, int R>
+cudaError_t launch_rows(const RowsArgs& args, int passes, int tiles, cudaStream_t stream) {
+  void* a[] = {(void*)&args};
+  return launch_pdl((const void*)k_adapter_rows<TM, R>, dim3((unsigned)tiles * kCluster, passes), dim3(kRowThreads),
+                    RowsShape<TM, R>::smem, stream, a, dim3(kCluster, 1, 1));
 }
-cudaError_t expand(const dictproj_adapters* a, const dictproj_rows* r, const float* t, const uint16_t* Q, int ld_q,
-                   int N, const __half* base, __half* out, cudaStream_t stream) {
-  int rp = a->rp, ns = a->n_slots;
-  void* args[] = {&t, &Q, &ld_q, &N, &rp, &ns, (void*)&a->rank, (void*)&r->perm, (void*)&r->start, &base, &out};
-  return launch_pdl((const void*)k_expand, dim3(r->M, (N + 255) / 256), dim3(256), 0, stream, args);
+template <int TM>
+cudaError_t launch_rows_r(const RowsArgs& args, int passes, int tiles, cudaStream_t stream) {
+  if (args.rp <= 16) return launch_rows<TM, 16>(args, passes, tiles, stream);
+  if (args.rp <= 32) return launch_rows<TM, 32>(args, passes, tiles, stream);
+  if (args.rp <= 64) return launch_rows<TM, 64>(args, passes, tiles, stream);
+  return launch_rows<TM, 128>(args, passes, tiles, stream);
 }
-cudaError_t weight_grad(const dictproj_adapters* a, const dictproj_rows* r, const float* t, const __half* in, int K,
-                        bool accumulate, float* g, cudaStream_t stream) {
-  int rp = a->rp, ns = a->n_slots, mr = a->max_rank, acc = accumulate;
-  void* args[] = {&t, &in, &K, &rp, &mr, &ns, (void*)&a->rank, (void*)&r->perm, (void*)&r->start, &acc, &g};
-  return launch_pdl((const void*)k_weight_grad, dim3((K + 255) / 256, a->max_rank, a->n_slots), dim3(256), 0, stream, args);
+
+RowsArgs rows_args(const dictproj_adapters* a, const dictproj_rows* r, bool wide) {
+  RowsArgs g = {};
+  g.n_tiles = r->n_tiles + (wide ? 2 : 0);
+  g.tiles = r->tiles[wide];
+  g.perm = r->perm;
+  g.rank = a->rank;
+  g.scale = a->scale;
+  g.rp = a->rp;
+  g.n_slots = a->n_slots;
+  return g;
+}
+RowsPass rows_pass(const dictproj_adapters* a, bool forward, const __half* in, const __half* base, __half* out) {
+  const __half* A = reinterpret_cast<const __half*>(a->A);
+  const __half* B = reinterpret_cast<const __half*>(a->B);
+  RowsPass p = {};
+  p.in = in;
+  p.base = base;
+  p.out = out;
+  p.P = forward ? A : B;
+  p.Q = forward ? B : A;
+  p.K = forward ? a->d_in : a->d_out;
+  p.N = forward ? a->d_out : a->d_in;
+  p.ld_p = forward ? a->d_in : a->ld_b;
+  p.ld_q = forward ? a->ld_b : a->d_in;
+  return p;
+}
+cudaError_t launch_rows_any(const RowsArgs& g, bool wide, int passes, const dictproj_rows* r, cudaStream_t stream) {
+  const int tiles = adapter_tiles(r->M, r->n_slots, wide ? 64 : 16);
+  return wide ? launch_rows_r<64>(g, passes, tiles, stream) : launch_rows_r<16>(g, passes, tiles, stream);
+}
+
+template <int R>
+cudaError_t launch_grad(const GradArgs& args, dim3 grid, cudaStream_t stream) {
+  void* a[] = {(void*)&args};
+  return launch_pdl((const void*)k_adapter_grad<R>, grid, dim3(kGradThreads), GradShape<R>::smem, stream, a,
+                    dim3(1, 1, grid.z));
+}
+
+template <int TM, int R>
+cudaError_t allow_rows() {
+  return cudaFuncSetAttribute(k_adapter_rows<TM, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsShape<TM, R>::smem);
+}
+template <int R>
+cudaError_t allow_rank() {
+  cudaError_t e;
+  if ((e = allow_rows<16, R>()) || (e = allow_rows<64, R>())) return e;
+  return cudaFuncSetAttribute(k_adapter_grad<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, GradShape<R>::smem);
 }
 
 }  // namespace
 
 cudaError_t prepare_adapter_kernels(int device) {
   (void)device;
+  cudaError_t e;
+  if ((e = allow_rank<16>()) || (e = allow_rank<32>()) || (e = allow_rank<64>()) || (e = allow_rank<128>())) return e;
   return cudaFuncSetAttribute(k_rows_plan, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kPlanWarps * (DICTPROJ_MAX_SLOTS + 1) * (int)sizeof(int));
+                              (kPlanWarps + 3) * (DICTPROJ_MAX_SLOTS + 2) * (int)sizeof(int));
 }
 
 cudaError_t launch_adapter_set(const dictproj_adapters* a, int slot, int rank, float scale, const __half* A,
@@ -244,28 +824,59 @@ cudaError_t launch_adapter_set(const dictproj_adapters* a, int slot, int rank, f
 
 cudaError_t launch_rows_plan(const dictproj_rows* r, const int* ids, int M, cudaStream_t stream) {
   int ns = r->n_slots;
-  void* args[] = {&ids, &M, &ns, (void*)&r->perm, (void*)&r->start};
+  void* args[] = {&ids, &M, &ns, (void*)&r->perm, (void*)&r->start, (void*)&r->n_tiles, (void*)&r->tiles[0],
+                  (void*)&r->tiles[1], (void*)&r->first64};
   return launch_pdl((const void*)k_rows_plan, dim3(1), dim3(kPlanWarps * 32),
-                    (size_t)kPlanWarps * (ns + 1) * sizeof(int), stream, args);
+                    ((size_t)kPlanWarps * (ns + 1) + 3 * (ns + 2)) * sizeof(int), stream, args);
 }
 
 cudaError_t launch_adapter_forward(const dictproj_adapters* a, const dictproj_rows* r, const __half* X,
                                    const __half* base, __half* Y, cudaStream_t stream) {
-  cudaError_t e = contract(a, r, X, a->d_in, a->A, a->d_in, a->t, stream);
-  if (e != cudaSuccess) return e;
-  return expand(a, r, a->t, a->B, a->ld_b, a->d_out, base, Y, stream);
+  const bool wide = r->M >= 256 && r->M >= 32 * a->n_slots;
+  RowsArgs g = rows_args(a, r, wide);
+  g.pass[0] = rows_pass(a, true, X, base, Y);
+  return launch_rows_any(g, wide, 1, r, stream);
 }
 
 cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_rows* r, const __half* X,
                                     const __half* dY, const __half* base, __half* dX, float* dA, float* dB,
                                     bool accumulate, cudaStream_t stream) {
-  cudaError_t e = contract(a, r, dY, a->d_out, a->B, a->ld_b, a->u, stream);
-  if (e != cudaSuccess) return e;
-  if (dX && (e = expand(a, r, a->u, a->A, a->d_in, a->d_in, base, dX, stream))) return e;
-  if (!dA) return cudaSuccess;
-  if ((e = contract(a, r, X, a->d_in, a->A, a->d_in, a->t, stream))) return e;
-  if ((e = weight_grad(a, r, a->u, X, a->d_in, accumulate, dA, stream))) return e;
-  return weight_grad(a, r, a->t, dY, a->d_out, accumulate, dB, stream);
+  RowsArgs g = rows_args(a, r, true);
+  g.pass[0] = rows_pass(a, false, dY, base, dX);
+  g.pass[1] = rows_pass(a, true, X, nullptr, nullptr);
+  if (dA)
+    for (int i = 0; i < 2; ++i) {
+      g.pass[i].hi = reinterpret_cast<__half*>(a->part[i][0]);
+      g.pass[i].lo = reinterpret_cast<__half*>(a->part[i][1]);
+      g.pass[i].unit = a->unit[i];
+    }
+  cudaError_t e = launch_rows_any(g, true, dA ? 2 : 1, r, stream);
+  if (e != cudaSuccess || !dA) return e;
+  GradArgs w = {};
+  for (int i = 0; i < 2; ++i) {
+    w.pass[i].in = i ? dY : X;
+    w.pass[i].hi = g.pass[i].hi;
+    w.pass[i].lo = g.pass[i].lo;
+    w.pass[i].unit = a->unit[i];
+    w.pass[i].g = i ? dB : dA;
+    w.pass[i].K = i ? a->d_out : a->d_in;
+    w.pass[i].blocks = (w.pass[i].K + kGradCols - 1) / kGradCols;
+  }
+  w.start = r->start;
+  w.first64 = r->first64;
+  w.perm = r->perm;
+  w.rank = a->rank;
+  w.rp = a->rp;
+  w.max_rank = a->max_rank;
+  w.accumulate = accumulate;
+  const int blocks = w.pass[0].blocks + w.pass[1].blocks;
+  int split = 1;
+  while (split < 8 && blocks * a->n_slots * split < 3 * a->n_sm && 64 * a->n_slots * split < r->M) split *= 2;
+  const dim3 grid(blocks, a->n_slots, split);
+  if (a->rp <= 16) return launch_grad<16>(w, grid, stream);
+  if (a->rp <= 32) return launch_grad<32>(w, grid, stream);
+  if (a->rp <= 64) return launch_grad<64>(w, grid, stream);
+  return launch_grad<128>(w, grid, stream);
 }
 
 }  // namespace dictproj

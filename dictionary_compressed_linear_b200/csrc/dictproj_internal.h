@@ -117,10 +117,17 @@ struct dictproj_adapters {
   uint16_t* B;             // fp16 [n_slots][rp][ld_b]
   int* rank;               // [n_slots], 0 = empty
   float* scale;            // [n_slots]
-  // backward pass: scale * U and scale * T of the planned rows, in plan order
-  float* u;                // fp32 [max_tokens][rp]
-  float* t;                // fp32 [max_tokens][rp]
+  // backward pass: scale * U (index 0) and scale * T (1) of the planned rows, in plan
+  // order, as two fp16 parts times a power of two per 64-row tile (adapter.cu)
+  uint16_t* part[2][2];    // [pass][high, low] fp16 [max_tokens][rp]
+  float* unit[2];          // [pass] what a tile's parts are multiplied with, [adapter_tiles(64)]
 };
+
+// Most tiles of `rows` rows that M rows over n_slots slots (and no slot) can form.
+inline int adapter_tiles(int M, int n_slots, int rows) {
+  const int some = n_slots + 1 < M ? n_slots + 1 : M;
+  return M / rows + some < M ? M / rows + some : M;
+}
 
 // A batch's rows sorted by adapter slot (stable), and the tiles they form.
 struct dictproj_rows {
@@ -129,6 +136,11 @@ struct dictproj_rows {
   int M;                   // rows of the last dictproj_rows_set (0: none yet)
   int* perm;               // [max_rows] row numbers by slot, rows without an adapter last
   int* start;              // [n_slots + 2] first position of each slot, of the rows without one, M
+  // tiles of up to 16 (index 0) and 64 (1) rows of one slot, in plan order; those of
+  // rows without an adapter (slot n_slots) come last
+  int* n_tiles;            // [2][2] tiles of the slots, all tiles
+  int4* tiles[2];          // {slot, first position, rows, row number of the first}
+  int* first64;            // [n_slots] first 64-row tile of each slot
 };
 
 struct dictproj_adamw {

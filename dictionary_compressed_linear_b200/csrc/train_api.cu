@@ -102,10 +102,12 @@ int dictproj_adapters_create(int d_in, int d_out, int max_rank, int n_slots, int
     return cuda_fail(e, "adapters_create: SM count");
   }
   const size_t ab = (size_t)n_slots * a->rp * d_in * 2, bb = (size_t)n_slots * a->rp * a->ld_b * 2;
-  const size_t tb = (size_t)max_tokens * a->rp * sizeof(float);
+  const size_t pb = (size_t)max_tokens * a->rp * 2, ub = (size_t)adapter_tiles(max_tokens, n_slots, 64) * sizeof(float);
   if ((e = dmalloc((void**)&a->A, ab)) || (e = dmalloc((void**)&a->B, bb)) ||
       (e = dmalloc((void**)&a->rank, (size_t)n_slots * 4)) || (e = dmalloc((void**)&a->scale, (size_t)n_slots * 4)) ||
-      (e = dmalloc((void**)&a->u, tb)) || (e = dmalloc((void**)&a->t, tb))) {
+      (e = dmalloc((void**)&a->part[0][0], pb)) || (e = dmalloc((void**)&a->part[0][1], pb)) ||
+      (e = dmalloc((void**)&a->part[1][0], pb)) || (e = dmalloc((void**)&a->part[1][1], pb)) ||
+      (e = dmalloc((void**)&a->unit[0], ub)) || (e = dmalloc((void**)&a->unit[1], ub))) {
     dictproj_free_adapters(a);
     cudaGetLastError();
     return fail(DICTPROJ_ERR_OOM, "adapters_create: device allocation failed (%s)", cudaGetErrorName(e));
@@ -127,8 +129,11 @@ void dictproj_free_adapters(dictproj_adapters* a) {
   cudaFree(a->B);
   cudaFree(a->rank);
   cudaFree(a->scale);
-  cudaFree(a->u);
-  cudaFree(a->t);
+  for (int i = 0; i < 2; ++i) {
+    cudaFree(a->part[i][0]);
+    cudaFree(a->part[i][1]);
+    cudaFree(a->unit[i]);
+  }
   delete a;
 }
 
@@ -177,7 +182,10 @@ int dictproj_rows_create(int max_rows, int n_slots, dictproj_rows** out) {
   r->max_rows = max_rows;
   r->n_slots = n_slots;
   cudaError_t e;
-  if ((e = dmalloc((void**)&r->perm, (size_t)max_rows * 4)) || (e = dmalloc((void**)&r->start, (size_t)(n_slots + 2) * 4))) {
+  if ((e = dmalloc((void**)&r->perm, (size_t)max_rows * 4)) || (e = dmalloc((void**)&r->start, (size_t)(n_slots + 2) * 4)) ||
+      (e = dmalloc((void**)&r->n_tiles, 4 * sizeof(int))) || (e = dmalloc((void**)&r->first64, (size_t)n_slots * 4)) ||
+      (e = dmalloc((void**)&r->tiles[0], (size_t)adapter_tiles(max_rows, n_slots, 16) * sizeof(int4))) ||
+      (e = dmalloc((void**)&r->tiles[1], (size_t)adapter_tiles(max_rows, n_slots, 64) * sizeof(int4)))) {
     dictproj_free_rows(r);
     cudaGetLastError();
     return fail(DICTPROJ_ERR_OOM, "rows_create: device allocation failed (%s)", cudaGetErrorName(e));
@@ -190,6 +198,10 @@ void dictproj_free_rows(dictproj_rows* r) {
   if (!r) return;
   cudaFree(r->perm);
   cudaFree(r->start);
+  cudaFree(r->n_tiles);
+  cudaFree(r->first64);
+  cudaFree(r->tiles[0]);
+  cudaFree(r->tiles[1]);
   delete r;
 }
 
