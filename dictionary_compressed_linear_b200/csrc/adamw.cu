@@ -19,6 +19,29 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t two) {
+  const uint32_t h = e4m3x2_to_f16x2(two);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// x / s for many x and one s, correctly rounded. Markstein (1990): with y the correctly
+// rounded 1 / s, q = x y and q + y (x - q s), the residual by fma, is the rounded
+// quotient as long as nothing leaves the normal range. For 2^-90 <= s <= 2^100 only an x
+// below 2^-125 can make the residual subnormal; then x / s < 2^-35, which is code 0 with
+// and without the dither. Other scales (a block of zeros, of overflowing moments) divide.
+struct Divisor {
+  float s, y;
+  bool fast;
+};
+__device__ __forceinline__ Divisor divisor(float s) {
+  return Divisor{s, __fdiv_rn(1.f, s), s >= 0x1p-90f && s <= 0x1p100f};
+}
+template <bool FAST>
+__device__ __forceinline__ float quotient(float x, const Divisor& d) {
+  if (!FAST) return __fdiv_rn(x, d.s);
+  const float q = __fmul_rn(x, d.y);
+  return __fmaf_rn(__fmaf_rn(-q, d.s, x), d.y, q);
+}
 
 __device__ __forceinline__ uint32_t dither20(uint32_t i, uint32_t step) {
   uint32_t h = i * 0x9E3779B9u + step * 0x6A09E667u;
@@ -45,83 +68,127 @@ __device__ __forceinline__ Updated adamw_element(float p, float grad, float m, f
   return u;
 }
 
+// Largest of the warp's non-negative values (their bits order as integers; a NaN wins).
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int off = 16; off; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-  return x;
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
 }
 
-// One CTA per chunk of kAdamwChunk elements; a warp takes a block of 128 at a time.
+// Four consecutive values of a lane, zeros past n; one load where the arrays allow it.
+// MODE 2: a whole chunk of aligned arrays; 1: aligned, with a ragged end; 0: neither.
+template <int MODE, class V, class E>
+__device__ __forceinline__ V load4(const E* p, int i, int n) {
+  V v = {};
+  if (MODE == 2 || (MODE == 1 && i + 4 <= n)) return *reinterpret_cast<const V*>(p + i);
+  E* e = reinterpret_cast<E*>(&v);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (i + q < n) e[q] = p[i + q];
+  return v;
+}
+template <int MODE, class V, class E>
+__device__ __forceinline__ void store4(E* p, int i, int n, V v) {
+  if (MODE == 2 || (MODE == 1 && i + 4 <= n)) {
+    *reinterpret_cast<V*>(p + i) = v;
+    return;
+  }
+  const E* e = reinterpret_cast<const E*>(&v);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (i + q < n) p[i + q] = e[q];
+}
+
+// The codes of four elements of one block.
+template <bool FAST>
+__device__ __forceinline__ uint2 encode4(const Updated (&u)[4], const Divisor& dm, const Divisor& dr, uint32_t first, uint32_t step) {
+  uint2 c;
+  c.x = f32x2_to_e4m3x2(quotient<FAST>(u[0].m, dm), quotient<FAST>(u[1].m, dm)) |
+        f32x2_to_e4m3x2(quotient<FAST>(u[2].m, dm), quotient<FAST>(u[3].m, dm)) << 16;
+  c.y = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t code = (__float_as_uint(__fmul_rn(quotient<FAST>(u[q].r, dr), 0x1p-120f)) + dither20(first + (uint32_t)q, step)) >> 20;
+    code = max(min(code, 0x7Eu), u[q].r > 0.f ? 1u : 0u);
+    c.y |= code << (8 * q);
+  }
+  return c;
+}
+
+// A warp takes a block of 128 at a time, four elements a lane.
+template <int BITS, int MODE>
+__device__ __forceinline__ void adamw_chunk(const AdamwChunk& c, const AdamwFactors& f) {
+  constexpr int kPer = kAdamwChunk / kBlock / 8;  // blocks of a warp
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = (int)c.count;
+  float4 p[kPer], g[kPer], m[kPer], v[kPer];
+  uint32_t mc[kPer], vc[kPer];
+  float sm[kPer], sr[kPer];
+#pragma unroll
+  for (int b = 0; b < kPer; ++b) {  // all loads first
+    const int blk = warp + 8 * b, i = blk * kBlock + 4 * lane;
+    p[b] = load4<MODE, float4>(c.p, i, n);
+    g[b] = load4<MODE, float4>(c.g, i, n);
+    if (BITS == 8) {
+      mc[b] = load4<MODE, uint32_t>(static_cast<const uint8_t*>(c.m), i, n);
+      vc[b] = load4<MODE, uint32_t>(static_cast<const uint8_t*>(c.v), i, n);
+      sm[b] = MODE == 2 || blk * kBlock < n ? c.m_scale[blk] : 0.f;
+      sr[b] = MODE == 2 || blk * kBlock < n ? c.v_scale[blk] : 0.f;
+    } else {
+      m[b] = load4<MODE, float4>(static_cast<const float*>(c.m), i, n);
+      v[b] = load4<MODE, float4>(static_cast<const float*>(c.v), i, n);
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < kPer; ++b) {
+    const int blk = warp + 8 * b, i = blk * kBlock + 4 * lane;
+    if (MODE < 2 && blk * kBlock >= n) break;
+    if (BITS == 8) {
+      const float2 m0 = e4m3x2_to_f32x2(mc[b]), m1 = e4m3x2_to_f32x2(mc[b] >> 16);
+      const float2 r0 = e4m3x2_to_f32x2(vc[b]), r1 = e4m3x2_to_f32x2(vc[b] >> 16);
+      m[b] = make_float4(__fmul_rn(m0.x, sm[b]), __fmul_rn(m0.y, sm[b]), __fmul_rn(m1.x, sm[b]), __fmul_rn(m1.y, sm[b]));
+      const float x = __fmul_rn(r0.x, sr[b]), y = __fmul_rn(r0.y, sr[b]), z = __fmul_rn(r1.x, sr[b]), w = __fmul_rn(r1.y, sr[b]);
+      v[b] = make_float4(__fmul_rn(x, x), __fmul_rn(y, y), __fmul_rn(z, z), __fmul_rn(w, w));
+    }
+    const Updated u[4] = {adamw_element(p[b].x, g[b].x, m[b].x, v[b].x, f), adamw_element(p[b].y, g[b].y, m[b].y, v[b].y, f),
+                          adamw_element(p[b].z, g[b].z, m[b].z, v[b].z, f), adamw_element(p[b].w, g[b].w, m[b].w, v[b].w, f)};
+    store4<MODE>(c.p, i, n, make_float4(u[0].p, u[1].p, u[2].p, u[3].p));
+    if (c.copy) {
+      const __half2 lo = __floats2half2_rn(u[0].p, u[1].p), hi = __floats2half2_rn(u[2].p, u[3].p);
+      store4<MODE>(reinterpret_cast<unsigned short*>(c.copy), i, n,
+                  make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi)));
+    }
+    if (BITS == 32) {
+      store4<MODE>(static_cast<float*>(c.m), i, n, make_float4(u[0].m, u[1].m, u[2].m, u[3].m));
+      store4<MODE>(static_cast<float*>(c.v), i, n, make_float4(u[0].v, u[1].v, u[2].v, u[3].v));
+      continue;
+    }
+    // past n every value is what zeros become: p = m = v = 0, which decides no scale
+    const Divisor dm = divisor(fmaxf(__fmul_rn(warp_max(fmaxf(fmaxf(fabsf(u[0].m), fabsf(u[1].m)), fmaxf(fabsf(u[2].m), fabsf(u[3].m)))), kScalePerAmax), kTinyScale));
+    const Divisor dr = divisor(fmaxf(__fmul_rn(warp_max(fmaxf(fmaxf(u[0].r, u[1].r), fmaxf(u[2].r, u[3].r))), kScalePerAmax), kTinyScale));
+    if (lane == 0) {
+      c.m_scale[blk] = dm.s;
+      c.v_scale[blk] = dr.s;
+    }
+    const uint32_t e = c.first + (uint32_t)i;
+    const uint2 codes = dm.fast && dr.fast ? encode4<true>(u, dm, dr, e, f.step) : encode4<false>(u, dm, dr, e, f.step);
+    store4<MODE>(static_cast<uint8_t*>(c.m), i, n, codes.x);
+    store4<MODE>(static_cast<uint8_t*>(c.v), i, n, codes.y);
+  }
+}
+
+// One CTA per chunk; its record holds the pointers, so that the data is one load away.
+// Bound by the bytes (30 a weight with 32-bit states, 18 with 8-bit ones) as long as the
+// arithmetic of an 8-bit step, some 80 instructions a weight, hides behind them: five
+// CTAs an SM (48 registers) measured 136 us for 44 M weights (5.9 TB/s), four 149 us, six
+// (40 registers, spills) 150 us; divisions by the compiler's sequence and maxima by
+// shuffles 177 us. With 32-bit states the registers serve loads in flight instead
+// (14 tensors of 65536: 4.2 us without a limit, 4.9 us at 48).
 template <int BITS>
-__global__ void __launch_bounds__(256)
-    k_adamw(const dictproj_adamw_tensor* __restrict__ tensors, const long long* __restrict__ first, int n_tensors,
-            AdamwFactors f) {
+__global__ void __launch_bounds__(256, BITS == 8 ? 5 : 1) k_adamw(const AdamwChunk* __restrict__ chunks, AdamwFactors f) {
   grid_dependency_wait();
-  const long long c = blockIdx.x;
-  int lo = 0, hi = n_tensors - 1;  // the last tensor whose first chunk is <= c (an empty tensor owns none)
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (first[mid] <= c) lo = mid;
-    else hi = mid - 1;
-  }
-  const dictproj_adamw_tensor T = tensors[lo];
-  const long long e0 = (c - first[lo]) * kAdamwChunk;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __half* copy = static_cast<__half*>(T.copy);
-  for (int b = warp; b < kAdamwChunk / kBlock; b += 8) {
-    const long long base = e0 + (long long)b * kBlock;
-    if (base >= T.n) break;
-    float sm = 0.f, sr = 0.f;
-    if (BITS == 8) {
-      sm = T.m_scale[base / kBlock];
-      sr = T.v_scale[base / kBlock];
-    }
-    Updated u[4];
-    float am = 0.f, ar = 0.f;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const long long i = base + 32 * q + lane;
-      u[q] = Updated{0.f, 0.f, 0.f, 0.f};
-      if (i < T.n) {
-        float m, v;
-        if (BITS == 8) {
-          m = __fmul_rn(e4m3_to_f32(static_cast<const uint8_t*>(T.m)[i]), sm);
-          const float r = __fmul_rn(e4m3_to_f32(static_cast<const uint8_t*>(T.v)[i]), sr);
-          v = __fmul_rn(r, r);
-        } else {
-          m = static_cast<const float*>(T.m)[i];
-          v = static_cast<const float*>(T.v)[i];
-        }
-        u[q] = adamw_element(T.p[i], T.g[i], m, v, f);
-        T.p[i] = u[q].p;
-        if (copy) copy[i] = __float2half_rn(u[q].p);
-        if (BITS == 32) {
-          static_cast<float*>(T.m)[i] = u[q].m;
-          static_cast<float*>(T.v)[i] = u[q].v;
-        }
-        am = fmaxf(am, fabsf(u[q].m));
-        ar = fmaxf(ar, u[q].r);
-      }
-    }
-    if (BITS == 8) {
-      sm = fmaxf(__fmul_rn(warp_max(am), kScalePerAmax), kTinyScale);
-      sr = fmaxf(__fmul_rn(warp_max(ar), kScalePerAmax), kTinyScale);
-      if (lane == 0) {
-        T.m_scale[base / kBlock] = sm;
-        T.v_scale[base / kBlock] = sr;
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const long long i = base + 32 * q + lane;
-        if (i >= T.n) continue;
-        static_cast<uint8_t*>(T.m)[i] = (uint8_t)f32x2_to_e4m3x2(__fdiv_rn(u[q].m, sm), 0.f);
-        uint32_t code = (__float_as_uint(__fmul_rn(__fdiv_rn(u[q].r, sr), 0x1p-120f)) + dither20((uint32_t)i, f.step)) >> 20;
-        code = min(code, 0x7Eu);
-        if (u[q].r > 0.f) code = max(code, 1u);
-        static_cast<uint8_t*>(T.v)[i] = (uint8_t)code;
-      }
-    }
-  }
+  trigger_dependents();
+  const AdamwChunk c = chunks[blockIdx.x];
+  if (c.vec && c.count == kAdamwChunk) adamw_chunk<BITS, 2>(c, f);
+  else if (c.vec) adamw_chunk<BITS, 1>(c, f);
+  else adamw_chunk<BITS, 0>(c, f);
 }
 
 }  // namespace
@@ -137,9 +204,8 @@ cudaError_t launch_adamw(const dictproj_adamw* w, const AdamwFactors& f, cudaStr
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  int n = w->n_tensors;
   AdamwFactors ff = f;
-  void* args[] = {(void*)&w->tensors, (void*)&w->first, &n, &ff};
+  void* args[] = {(void*)&w->table, &ff};
   return cudaLaunchKernelExC(&cfg, w->bits == 8 ? (const void*)k_adamw<8> : (const void*)k_adamw<32>, args);
 }
 

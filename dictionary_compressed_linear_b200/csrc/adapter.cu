@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_rows(const __grid_const
   const uint32_t ring = smem_u32(smem);
 
   grid_dependency_wait();
+  trigger_dependents();
   // rows whose output is already in place need no tile of their own
   const bool in_place = a.out == nullptr || a.base == a.out;
   const int4 tile = g.tiles[tile_no];
@@ -598,6 +599,7 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
   const int col0 = ((int)blockIdx.x - (which ? g.pass[0].blocks : 0)) * kGradCols;
   const uint32_t ring = smem_u32(smem);
   grid_dependency_wait();
+  trigger_dependents();
   const int p0 = g.start[slot], rows = g.start[slot + 1] - p0, tile0 = g.first64[slot];
   const int r = rows ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
   float* out = a.g + (size_t)slot * g.max_rank * a.K;

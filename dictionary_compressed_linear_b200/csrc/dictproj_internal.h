@@ -143,10 +143,26 @@ struct dictproj_rows {
   int* first64;            // [n_slots] first 64-row tile of each slot
 };
 
+namespace dictproj {
+constexpr int kAdamwChunk = 2048;  // elements of one work item, a multiple of DICTPROJ_ADAMW_BLOCK
+// Up to kAdamwChunk consecutive elements of one tensor, the pointers at the first of them.
+struct AdamwChunk {
+  float* p;
+  const float* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  void* copy;
+  uint32_t first;          // number of the first element in its tensor
+  uint16_t count;
+  uint16_t vec;            // every pointer is aligned to four of its elements
+};
+}  // namespace dictproj
+
 struct dictproj_adamw {
   int device;
-  int n_tensors, bits, n_sm;
-  long long chunks;        // kAdamwChunk-element pieces of all tensors
-  dictproj_adamw_tensor* tensors;  // device copy of the table
-  long long* first;        // device [n_tensors + 1] first chunk of each tensor
+  int bits;
+  long long chunks;
+  dictproj::AdamwChunk* table;  // device
 };

@@ -136,7 +136,6 @@ cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_r
                                     bool accumulate, cudaStream_t stream);
 
 // optimiser (adamw.cu)
-constexpr int kAdamwChunk = 2048;  // elements of one work item, a multiple of DICTPROJ_ADAMW_BLOCK
 struct AdamwFactors {
   float grad_scale, b1, omb1, b2, omb2, rbc2, eps, decay, alpha;
   uint32_t step;

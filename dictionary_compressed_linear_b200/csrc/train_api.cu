@@ -338,48 +338,62 @@ int dictproj_adamw_create(const dictproj_adamw_tensor* tensors, int n_tensors, i
     return fail(DICTPROJ_ERR_RANGE, "adamw_create: n_tensors=%d outside [1, 2^20]", n_tensors);
   if (state_bits != 8 && state_bits != 32)
     return fail(DICTPROJ_ERR_RANGE, "adamw_create: state_bits=%d is neither 8 nor 32", state_bits);
-  std::vector<long long> first;
-  try {
-    first.resize((size_t)n_tensors + 1);
-  } catch (...) {
-    return fail(DICTPROJ_ERR_OOM, "adamw_create: host allocation failed");
-  }
-  first[0] = 0;
+  const int sb = state_bits / 8;  // bytes of a state's element
+  long long chunks = 0;
   for (int i = 0; i < n_tensors; ++i) {
     const dictproj_adamw_tensor& t = tensors[i];
     if (t.n < 0 || t.n >= (1ll << 32)) return fail(DICTPROJ_ERR_RANGE, "adamw_create: tensor %d: n=%lld", i, t.n);
-    first[i + 1] = first[i] + (t.n + kAdamwChunk - 1) / kAdamwChunk;
+    chunks += (t.n + kAdamwChunk - 1) / kAdamwChunk;
     if (t.n == 0) continue;
     if (!t.p || !t.g || !t.m || !t.v) return fail(DICTPROJ_ERR_NULL, "adamw_create: tensor %d: NULL array", i);
     if (state_bits == 8 && (!t.m_scale || !t.v_scale))
       return fail(DICTPROJ_ERR_NULL, "adamw_create: tensor %d: 8-bit states need their scales", i);
-    if (misaligned(t.p, 4) || misaligned(t.g, 4) || misaligned(t.copy, 2) ||
-        (state_bits == 32 && (misaligned(t.m, 4) || misaligned(t.v, 4))) ||
+    if (misaligned(t.p, 4) || misaligned(t.g, 4) || misaligned(t.copy, 2) || misaligned(t.m, sb) || misaligned(t.v, sb) ||
         (state_bits == 8 && (misaligned(t.m_scale, 4) || misaligned(t.v_scale, 4))))
       return fail(DICTPROJ_ERR_ALIGN, "adamw_create: tensor %d: an array is not aligned to its elements", i);
   }
-  if (first[n_tensors] > 0x7fffffffll)
+  if (chunks > 0x7fffffffll)
     return fail(DICTPROJ_ERR_RANGE, "adamw_create: more than 2^31 - 1 chunks of %d elements", kAdamwChunk);
   int dev, st;
   if ((st = ensure_device(&dev))) return st;
+  std::vector<AdamwChunk> table;
+  try {
+    table.resize((size_t)chunks);
+  } catch (...) {
+    return fail(DICTPROJ_ERR_OOM, "adamw_create: host allocation failed");
+  }
+  size_t at = 0;
+  for (int i = 0; i < n_tensors; ++i) {
+    const dictproj_adamw_tensor& t = tensors[i];
+    const bool vec = !misaligned(t.p, 16) && !misaligned(t.g, 16) && !misaligned(t.m, 4 * sb) &&
+                     !misaligned(t.v, 4 * sb) && !misaligned(t.copy, 8);
+    for (long long e = 0; e < t.n; e += kAdamwChunk) {
+      AdamwChunk& c = table[at++];
+      c.p = t.p + e;
+      c.g = t.g + e;
+      c.m = static_cast<char*>(t.m) + e * sb;
+      c.v = static_cast<char*>(t.v) + e * sb;
+      c.m_scale = t.m_scale ? t.m_scale + e / DICTPROJ_ADAMW_BLOCK : nullptr;
+      c.v_scale = t.v_scale ? t.v_scale + e / DICTPROJ_ADAMW_BLOCK : nullptr;
+      c.copy = t.copy ? static_cast<char*>(t.copy) + 2 * e : nullptr;
+      c.first = (uint32_t)e;
+      c.count = (uint16_t)std::min<long long>(kAdamwChunk, t.n - e);
+      c.vec = vec;
+    }
+  }
   dictproj_adamw* w = new (std::nothrow) dictproj_adamw();
   if (!w) return fail(DICTPROJ_ERR_OOM, "adamw_create: host allocation failed");
   w->device = dev;
-  w->n_tensors = n_tensors;
   w->bits = state_bits;
-  w->chunks = first[n_tensors];
-  const size_t tb = (size_t)n_tensors * sizeof(dictproj_adamw_tensor), fb = first.size() * sizeof(long long);
-  cudaError_t e = cudaDeviceGetAttribute(&w->n_sm, cudaDevAttrMultiProcessorCount, dev);
+  w->chunks = chunks;
+  const size_t bytes = table.size() * sizeof(AdamwChunk);
+  cudaError_t e = dmalloc((void**)&w->table, bytes);
   if (e != cudaSuccess) {
-    delete w;
-    return cuda_fail(e, "adamw_create: SM count");
-  }
-  if ((e = dmalloc((void**)&w->tensors, tb)) || (e = dmalloc((void**)&w->first, fb))) {
     dictproj_free_adamw(w);
     cudaGetLastError();
     return fail(DICTPROJ_ERR_OOM, "adamw_create: device allocation failed (%s)", cudaGetErrorName(e));
   }
-  if ((e = h2d(w->tensors, tensors, tb)) || (e = h2d(w->first, first.data(), fb))) {
+  if ((e = h2d(w->table, table.data(), bytes))) {
     dictproj_free_adamw(w);
     cudaGetLastError();
     return cuda_fail(e, "adamw_create: copy to device");
@@ -390,8 +404,7 @@ int dictproj_adamw_create(const dictproj_adamw_tensor* tensors, int n_tensors, i
 
 void dictproj_free_adamw(dictproj_adamw* w) {
   if (!w) return;
-  cudaFree(w->tensors);
-  cudaFree(w->first);
+  cudaFree(w->table);
   delete w;
 }
 
