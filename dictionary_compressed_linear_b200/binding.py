@@ -818,8 +818,8 @@ def dictproj_adapters_create(d_in: int, d_out: int, max_rank: int, n_slots: int,
 def dictproj_adapters_set(adapters: Adapters, slot: int, rank: int, scale: float, A_ptr: int, B_ptr: int,
                           stream: int = 0):
     """A: device fp16 [rank][d_in], B: device fp16 [rank][d_out]; rank 0 empties the slot."""
-    _check(lib().dictproj_adapters_set(adapters.handle, slot, rank, float(scale), C.c_void_p(A_ptr or None),
-                                       C.c_void_p(B_ptr or None), C.c_void_p(stream)))
+    _check(lib().dictproj_adapters_set(adapters.handle, slot, rank, float(scale), A_ptr,
+                                       B_ptr, stream))
 
 
 def dictproj_adapters_slot(adapters: Adapters, slot: int) -> dict:
@@ -837,29 +837,29 @@ def dictproj_rows_create(max_rows: int, n_slots: int) -> Rows:
 
 def dictproj_rows_set(rows: Rows, ids_ptr: int, M: int, stream: int = 0):
     """ids: device int32[M], the slot of each row (outside [0, n_slots): no adapter)."""
-    _check(lib().dictproj_rows_set(rows.handle, C.c_void_p(ids_ptr or None), M, C.c_void_p(stream)))
+    _check(lib().dictproj_rows_set(rows.handle, ids_ptr, M, stream))
 
 
 def dictproj_adapter_forward(adapters: Adapters, rows: Rows, X_ptr: int, base_ptr: int, Y_ptr: int, stream: int = 0):
     """Y = base + scale (X A^T) B for every row's own adapter (base_ptr 0: base = 0; may equal Y_ptr)."""
-    _check(lib().dictproj_adapter_forward(adapters.handle, rows.handle, C.c_void_p(X_ptr or None),
-                                          C.c_void_p(base_ptr or None), C.c_void_p(Y_ptr or None), C.c_void_p(stream)))
+    _check(lib().dictproj_adapter_forward(adapters.handle, rows.handle, X_ptr,
+                                          base_ptr, Y_ptr, stream))
 
 
 def dictproj_forward_adapters(X_ptr: int, layer: Layer, group: Group, adapters: Adapters, rows: Rows, Y_ptr: int,
                               stream: int = 0):
     """The projection and the adapters of its rows: dictproj_forward, then dictproj_adapter_forward on Y."""
-    _check(lib().dictproj_forward_adapters(C.c_void_p(X_ptr or None), layer.handle, group.handle, adapters.handle,
-                                           rows.handle, C.c_void_p(Y_ptr or None), C.c_void_p(stream)))
+    _check(lib().dictproj_forward_adapters(X_ptr, layer.handle, group.handle, adapters.handle,
+                                           rows.handle, Y_ptr, stream))
 
 
 def dictproj_adapter_backward(adapters: Adapters, rows: Rows, X_ptr: int, dY_ptr: int, base_ptr: int, dX_ptr: int,
                               dA_ptr: int, dB_ptr: int, accumulate: bool = False, stream: int = 0):
     """dX = base + scale (dY B^T) A, and the gradients dA, dB (fp32) of every slot."""
-    _check(lib().dictproj_adapter_backward(adapters.handle, rows.handle, C.c_void_p(X_ptr or None),
-                                           C.c_void_p(dY_ptr or None), C.c_void_p(base_ptr or None),
-                                           C.c_void_p(dX_ptr or None), C.c_void_p(dA_ptr or None),
-                                           C.c_void_p(dB_ptr or None), int(accumulate), C.c_void_p(stream)))
+    _check(lib().dictproj_adapter_backward(adapters.handle, rows.handle, X_ptr,
+                                           dY_ptr, base_ptr,
+                                           dX_ptr, dA_ptr,
+                                           dB_ptr, int(accumulate), stream))
 
 
 def dictproj_group_reserve_backward(group: Group, max_d_out: int):
@@ -869,8 +869,8 @@ def dictproj_group_reserve_backward(group: Group, max_d_out: int):
 
 def dictproj_backward_input(dY_ptr: int, M: int, layer: Layer, group: Group, dX_ptr: int, stream: int = 0):
     """dX = dY C^T D^T, the input gradient of the frozen projection."""
-    _check(lib().dictproj_backward_input(C.c_void_p(dY_ptr or None), M, layer.handle, group.handle,
-                                         C.c_void_p(dX_ptr or None), C.c_void_p(stream)))
+    _check(lib().dictproj_backward_input(dY_ptr, M, layer.handle, group.handle,
+                                         dX_ptr, stream))
 
 
 def dictproj_adamw_create(tensors, state_bits: int = 32) -> AdamW:
@@ -887,7 +887,7 @@ def dictproj_adamw_create(tensors, state_bits: int = 32) -> AdamW:
 def dictproj_adamw_step(adamw: AdamW, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999,
                         eps: float = 1e-8, weight_decay: float = 0.01, grad_scale: float = 1.0, stream: int = 0):
     _check(lib().dictproj_adamw_step(adamw.handle, step, float(lr), float(beta1), float(beta2), float(eps),
-                                     float(weight_decay), float(grad_scale), C.c_void_p(stream)))
+                                     float(weight_decay), float(grad_scale), stream))
 
 
 def dictproj_check(stream: int = 0):

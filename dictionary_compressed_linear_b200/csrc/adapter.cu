@@ -30,8 +30,9 @@ namespace {
 // histogram (equal lanes found by match), a scan over (slot, warp) turns the counts
 // into positions, and the second pass over the ids scatters in row order, so the
 // result does not depend on timing. Bucket n_slots takes the rows without a slot.
-// Then the slots' rows are cut into tiles of 16 and of 64.
+// Then the slots' rows are cut into tiles of kFewRows and of kWideRows.
 constexpr int kPlanWarps = 32;
+constexpr int kFewRows = 4, kWideRows = 64;
 
 __device__ __forceinline__ int plan_bucket(const int* ids, int m, int n_slots) {
   const int id = ids[m];
@@ -62,7 +63,7 @@ __device__ __forceinline__ int block_exclusive_sum(int x, int* wsum, int* total)
 
 __global__ void __launch_bounds__(kPlanWarps * 32)
     k_rows_plan(const int* __restrict__ ids, int M, int n_slots, int* __restrict__ perm, int* __restrict__ start,
-                int* __restrict__ n_tiles, int4* __restrict__ tiles16, int4* __restrict__ tiles64,
+                int* __restrict__ n_tiles, int4* __restrict__ tiles4, int4* __restrict__ tiles64,
                 int* __restrict__ first64) {
   extern __shared__ int plan_smem[];
   __shared__ int wsum[kPlanWarps];
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32)
   int last[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int T = q ? 64 : 16;
+    const int T = q ? kWideRows : kFewRows;
     const int f = block_exclusive_sum((count + T - 1) / T, wsum, &last[q]);
     if (s < n_slots) {
       tfirst[q * (nb + 1) + s] = f;
@@ -141,9 +142,9 @@ __global__ void __launch_bounds__(kPlanWarps * 32)
   }
   __syncthreads();  // the tiles name row numbers of perm
   for (int q = 0; q < 2; ++q) {
-    const int T = q ? 64 : 16;
+    const int T = q ? kWideRows : kFewRows;
     const int* tf = tfirst + q * (nb + 1);
-    int4* tiles = q ? tiles64 : tiles16;
+    int4* tiles = q ? tiles64 : tiles4;
     for (int t = threadIdx.x; t < tf[nb]; t += blockDim.x) {
       int a = 0, z = n_slots;  // the last bucket whose first tile is <= t (an empty bucket owns none)
       while (a < z) {
@@ -186,6 +187,11 @@ __device__ __forceinline__ uint32_t peer_smem(uint32_t local, uint32_t rank) {
 __device__ __forceinline__ float4 ld_peer_v4f(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_peer_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ void st_peer_v4f(uint32_t addr, float4 v) {
@@ -261,13 +267,6 @@ __device__ __forceinline__ float split_unit(float m) {
 }
 
 // ---- rows: contraction and expansion in one launch --------------------------------------
-// A cluster of kCluster CTAs takes one tile of up to TM rows of one slot:
-//   1. CTA c contracts its share of the K columns of In with P_s (TM x K by K x r, warps
-//      split over rows and over the 16-column steps), summed over the warps in order;
-//   2. the CTAs' partial sums meet through distributed shared memory, in rank order;
-//   3. CTA c expands T into its share of the N columns of Out, adding base.
-// One ring of CW-column stages (cp.async) runs through both phases, so that the first
-// Q and base tiles arrive while T is being summed.
 constexpr int kCluster = 8;
 constexpr int kRowThreads = 256;
 
@@ -292,21 +291,241 @@ struct RowsArgs {
   int rp, n_slots;
 };
 
-template <int TM, int R>
+// ---- few rows of a slot: serving ----------------------------------------------------------
+// A cluster of kCluster CTAs takes one tile of up to four rows of one slot and walks the
+// weights once, 16 bytes a lane straight from memory, on the CUDA cores (a weight meets
+// at most four rows: the tensor cores would have nothing to reuse).
+//   1. CTA c contracts its share of the K columns: warp w owns the ranks w, w + 8, ...;
+//   2. the CTAs' partial sums meet through distributed shared memory, in rank order;
+//   3. CTA c expands T into its share of the N columns: four lanes split the ranks of
+//      eight columns. Its part of Q is on its way to L2 since before 1.
+// Bound by latency: the chain is plan -> rank and rows -> X and P -> cluster -> Q.
+__device__ __forceinline__ void dot2(float& acc, uint32_t x2, uint32_t w2) {
+  asm("{\n\t.reg .f16 a, b, c, d;\n\tmov.b32 {a, b}, %1;\n\tmov.b32 {c, d}, %2;\n\t"
+      "fma.rn.f32.f16 %0, a, c, %0;\n\tfma.rn.f32.f16 %0, b, d, %0;\n\t}" : "+f"(acc) : "r"(x2), "r"(w2));
+}
+__device__ __forceinline__ void dot8(float& acc, const uint4& x, const uint4& w) {
+  dot2(acc, x.x, w.x);
+  dot2(acc, x.y, w.y);
+  dot2(acc, x.z, w.z);
+  dot2(acc, x.w, w.w);
+}
+// 8 elements from column c of a row of n elements, zeros past the end.
+__device__ __forceinline__ uint4 read_piece(const __half* row, int c, int n, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4*>(row + c);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned short a = c + 2 * i < n ? __half_as_ushort(row[c + 2 * i]) : 0;
+    const unsigned short b = c + 2 * i + 1 < n ? __half_as_ushort(row[c + 2 * i + 1]) : 0;
+    w[i] = (uint32_t)a | ((uint32_t)b << 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void write_piece(__half* row, int c, int n, bool vec, const uint4& v) {
+  if (vec) {
+    *reinterpret_cast<uint4*>(row + c) = v;
+    return;
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c + e < n) row[c + e] = __ushort_as_half((unsigned short)(w[e >> 1] >> (16 * (e & 1))));
+}
+
+struct FewTile {
+  int row[kFewRows];
+  int count, r, rankc;
+  float scale;
+  const __half* P;
+  const __half* Q;
+};
+
+// Rows [r_lo, r_hi) of pieces [lo, hi) to L2, by 128-byte lines.
+__device__ __forceinline__ void prefetch_rows(const __half* w, int ld, int lo, int hi, int r_lo, int r_hi) {
+  const int lines = (hi - lo + 7) / 8;
+  for (int i = threadIdx.x; i < (r_hi - r_lo) * lines; i += kRowThreads) {
+    const __half* q = w + (size_t)(r_lo + i / lines) * ld + 8 * (lo + 8 * (i % lines));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+  }
+}
+
+template <int R, int NR>
+__device__ __forceinline__ void few_rows(const RowsPass& a, const FewTile& f, float* part, float* full) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool vec_in = (a.K & 7) == 0, vec_out = (a.N & 7) == 0;
+  const int kp = (a.K + 7) / 8, np = (a.N + 7) / 8;
+  const int n_lo = np * f.rankc / kCluster, n_hi = np * (f.rankc + 1) / kCluster;
+  if (R > 16) prefetch_rows(f.Q, a.ld_q, n_lo, n_hi, 16, f.r);
+  float acc[R / 8][NR];
+#pragma unroll
+  for (int j = 0; j < R / 8; ++j)
+#pragma unroll
+    for (int m = 0; m < NR; ++m) acc[j][m] = 0.f;
+  const int k_hi = kp * (f.rankc + 1) / kCluster;
+#pragma unroll 2
+  for (int p = kp * f.rankc / kCluster + lane; p < k_hi; p += 32) {
+    uint4 x[NR];
+#pragma unroll
+    for (int m = 0; m < NR; ++m) x[m] = read_piece(a.in + (size_t)f.row[m] * a.K, 8 * p, a.K, vec_in);
+#pragma unroll
+    for (int j = 0; j < R / 8; ++j) {
+      const int rank = warp + 8 * j;
+      if (rank >= f.r) break;
+      const uint4 w = *reinterpret_cast<const uint4*>(f.P + (size_t)rank * a.ld_p + 8 * p);
+#pragma unroll
+      for (int m = 0; m < NR; ++m) dot8(acc[j][m], x[m], w);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < R / 8; ++j)
+#pragma unroll
+    for (int m = 0; m < NR; ++m) {
+      float x = acc[j][m];
+#pragma unroll
+      for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+      if (lane == 0) part[m * R + warp + 8 * j] = x;
+    }
+  cluster_arrive();
+  cluster_wait();
+  const uint32_t pbase = smem_u32(part);
+  for (int i = tid; i < NR * R; i += kRowThreads) {
+    float x[kCluster];
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) x[c] = ld_peer_f32(peer_smem(pbase + 4 * i, c));
+#pragma unroll
+    for (int c = 1; c < kCluster; ++c) x[0] += x[c];
+    full[i] = i % R < f.r ? x[0] * f.scale : 0.f;
+  }
+  cluster_arrive();  // waited for at the end: no CTA leaves while its sums are read
+  __syncthreads();
+  const int js = lane >> 3;
+  for (int p0 = n_lo + 8 * warp; p0 < n_hi; p0 += 8 * (kRowThreads / 32)) {  // the warp's lanes stay together
+    const int p = p0 + (lane & 7);
+    const bool in = p < n_hi;
+    float y[NR][8];
+#pragma unroll
+    for (int m = 0; m < NR; ++m)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[m][e] = 0.f;
+    uint4 b = make_uint4(0, 0, 0, 0);
+    const int row = f.row[0];
+    const bool mine = in && js < f.count && js < NR;
+    const __half* brow = nullptr;
+    __half* orow = nullptr;
+    if (mine) {
+      int mr = row;
+#pragma unroll
+      for (int m = 1; m < NR; ++m) mr = js == m ? f.row[m] : mr;
+      brow = a.base + (size_t)mr * a.N;
+      orow = a.out + (size_t)mr * a.N;
+      if (a.base) b = read_piece(brow, 8 * p, a.N, vec_out);
+    }
+    if (in)
+#pragma unroll 4
+      for (int j = js; j < f.r; j += 4) {
+        const uint4 w = *reinterpret_cast<const uint4*>(f.Q + (size_t)j * a.ld_q + 8 * p);
+        const float2 w0 = __half22float2(*reinterpret_cast<const __half2*>(&w.x)), w1 = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+        const float2 w2 = __half22float2(*reinterpret_cast<const __half2*>(&w.z)), w3 = __half22float2(*reinterpret_cast<const __half2*>(&w.w));
+#pragma unroll
+        for (int m = 0; m < NR; ++m) {
+          const float t = full[m * R + j];
+          y[m][0] = fmaf(t, w0.x, y[m][0]), y[m][1] = fmaf(t, w0.y, y[m][1]);
+          y[m][2] = fmaf(t, w1.x, y[m][2]), y[m][3] = fmaf(t, w1.y, y[m][3]);
+          y[m][4] = fmaf(t, w2.x, y[m][4]), y[m][5] = fmaf(t, w2.y, y[m][5]);
+          y[m][6] = fmaf(t, w3.x, y[m][6]), y[m][7] = fmaf(t, w3.y, y[m][7]);
+        }
+      }
+    float o[8];
+#pragma unroll
+    for (int m = 0; m < NR; ++m)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float x = y[m][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        o[e] = m == 0 || js == m ? x : o[e];
+      }
+    if (mine) {
+      const float2 b0 = __half22float2(*reinterpret_cast<const __half2*>(&b.x)), b1 = __half22float2(*reinterpret_cast<const __half2*>(&b.y));
+      const float2 b2 = __half22float2(*reinterpret_cast<const __half2*>(&b.z)), b3 = __half22float2(*reinterpret_cast<const __half2*>(&b.w));
+      const __half2 h0 = __floats2half2_rn(b0.x + o[0], b0.y + o[1]), h1 = __floats2half2_rn(b1.x + o[2], b1.y + o[3]);
+      const __half2 h2 = __floats2half2_rn(b2.x + o[4], b2.y + o[5]), h3 = __floats2half2_rn(b3.x + o[6], b3.y + o[7]);
+      write_piece(orow, 8 * p, a.N, vec_out,
+                  make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
+                             *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3)));
+    }
+  }
+  cluster_wait();
+}
+
+// base alone, for rows without an adapter: this CTA's share of the columns
+__device__ __forceinline__ void copy_rows(const RowsPass& a, const int* rows, int count, int rankc) {
+  const bool vec = (a.N & 7) == 0;
+  const int np = (a.N + 7) / 8, lo = np * rankc / kCluster, n = np * (rankc + 1) / kCluster - lo;
+  for (int i = threadIdx.x; i < count * n; i += kRowThreads) {
+    const size_t at = (size_t)rows[i / n] * a.N;
+    const int c = 8 * (lo + i % n);
+    write_piece(a.out + at, c, a.N, vec, a.base ? read_piece(a.base + at, c, a.N, vec) : make_uint4(0, 0, 0, 0));
+  }
+}
+
+template <int R>
+__global__ void __launch_bounds__(kRowThreads, R <= 32 ? 4 : 2) k_adapter_few(const __grid_constant__ RowsArgs g) {
+  __shared__ __align__(16) float part[kFewRows * R], full[kFewRows * R];
+  const RowsPass& a = g.pass[blockIdx.y];
+  const int tile_no = blockIdx.x / kCluster;
+  grid_dependency_wait();
+  trigger_dependents();
+  const bool in_place = a.out == nullptr || a.base == a.out;
+  const int4 tile = g.tiles[tile_no];
+  if (tile_no >= g.n_tiles[in_place ? 0 : 1]) return;  // the whole cluster
+  FewTile f;
+  f.count = tile.z;
+  f.rankc = blockIdx.x % kCluster;
+  if (tile.x < g.n_slots) {
+    f.P = a.P + (size_t)tile.x * g.rp * a.ld_p;
+    f.Q = a.Q + (size_t)tile.x * g.rp * a.ld_q;
+    // the first 16 ranks (every slot holds as many rows) start before the rank is known
+    const int kp = (a.K + 7) / 8, np = (a.N + 7) / 8;
+    prefetch_rows(f.P, a.ld_p, kp * f.rankc / kCluster, kp * (f.rankc + 1) / kCluster, 0, 16);
+    prefetch_rows(f.Q, a.ld_q, np * f.rankc / kCluster, np * (f.rankc + 1) / kCluster, 0, 16);
+  }
+  f.r = tile.x < g.n_slots ? g.rank[tile.x] : 0;
+  f.row[0] = tile.w;
+#pragma unroll
+  for (int m = 1; m < kFewRows; ++m) f.row[m] = m < f.count ? g.perm[tile.y + m] : tile.w;
+  if (f.r == 0) {
+    if (!in_place) copy_rows(a, g.perm + tile.y, f.count, f.rankc);
+    return;
+  }
+  f.scale = g.scale[tile.x];
+  if (f.count == 1) few_rows<R, 1>(a, f, part, full);
+  else few_rows<R, kFewRows>(a, f, part, full);
+}
+
+// ---- many rows of a slot: prefill and training ----------------------------------------------
+// A cluster of kCluster CTAs takes one tile of up to kWideRows rows of one slot:
+//   1. CTA c contracts its share of the K columns of In with P_s (rows x K by K x r on
+//      mma.sync, warps split over rows and over the 16-column steps);
+//   2. the CTAs' partial sums meet through distributed shared memory, in rank order;
+//   3. CTA c expands T into its share of the N columns of Out, adding base.
+// One ring of 64-column stages (cp.async) runs through both phases, so that the first
+// Q and base tiles arrive while T is being summed.
+template <int R>
 struct RowsShape {
-  static constexpr int CW = TM == 16 ? 128 : 64;  // columns of a stage
+  static constexpr int TM = kWideRows, CW = 64;  // rows, columns of a stage
   static constexpr int kPitch = 2 * CW;
   static constexpr int kStages = R == 128 ? 3 : 4;
   static constexpr int kInBytes = TM * kPitch, kStageBytes = (TM + R) * kPitch;
-  static constexpr int kRedBytes = TM == 16 ? 8 * TM * R * 4 : 0;  // the warps' sums
-  static constexpr int kPart = kStages * kStageBytes, kFull = kPart + TM * R * 4, kRed = kFull + TM * R * 4;
-  static constexpr int smem = kRed + kRedBytes;
+  static constexpr int kPart = kStages * kStageBytes, kFull = kPart + TM * R * 4;
+  static constexpr int smem = kFull + TM * R * 4;
 };
 
-template <int TM, int R>
+template <int R>
 __global__ void __launch_bounds__(kRowThreads) k_adapter_rows(const __grid_constant__ RowsArgs g) {
-  using S = RowsShape<TM, R>;
-  constexpr int CW = S::CW, PITCH = S::kPitch, PIECES = PITCH / 16;
+  using S = RowsShape<R>;
+  constexpr int TM = S::TM, CW = S::CW, PITCH = S::kPitch, PIECES = PITCH / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int srow[TM];
   __shared__ float smax[kRowThreads / 32];
@@ -331,14 +550,7 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_rows(const __grid_const
   const int n_lo = nc * rankc / kCluster, nn = nc * (rankc + 1) / kCluster - n_lo;
   __syncthreads();
   if (r == 0) {  // base alone
-    if (!in_place)
-      for (int i = tid; i < count * nn * CW; i += kRowThreads) {
-        const int row = i / (nn * CW), c = n_lo * CW + i % (nn * CW);
-        if (c < a.N) {
-          const size_t at = (size_t)srow[row] * a.N + c;
-          a.out[at] = a.base ? a.base[at] : __float2half_rn(0.f);
-        }
-      }
+    if (!in_place) copy_rows(a, srow, count, rankc);
     return;
   }
   const float scale = g.scale[slot];
@@ -373,7 +585,7 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_rows(const __grid_const
   };
   for (int i = 0; i < S::kStages - 1; ++i) issue(i);
 
-  const int rg = TM == 64 ? warp & 3 : 0, half = TM == 64 ? warp >> 2 : 0;
+  const int rg = warp & 3, half = warp >> 2;
   {  // 1. contraction
     float acc[R / 8][4];
 #pragma unroll
@@ -384,8 +596,8 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_rows(const __grid_const
       issue(i + S::kStages - 1);
       const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
 #pragma unroll
-      for (int kk = 0; kk < (TM == 64 ? 2 : 1); ++kk) {
-        const int k16 = TM == 64 ? half * 2 + kk : warp;
+      for (int kk = 0; kk < 2; ++kk) {
+        const int k16 = half * 2 + kk;
         uint32_t af[4];
         ldmatrix4(af, st + swz<PITCH>(rg * 16 + (lane & 15), 2 * k16 + (lane >> 4)));
 #pragma unroll
@@ -400,22 +612,7 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_rows(const __grid_const
     }
     // the CTA's sum, warps in order
     const int g0 = lane >> 2, c0 = 2 * (lane & 3);
-    if constexpr (TM == 16) {
-      float* red = reinterpret_cast<float*>(smem + S::kRed) + warp * TM * R;
-#pragma unroll
-      for (int t = 0; t < R / 8; ++t) {
-        *reinterpret_cast<float2*>(red + g0 * R + 8 * t + c0) = make_float2(acc[t][0], acc[t][1]);
-        *reinterpret_cast<float2*>(red + (g0 + 8) * R + 8 * t + c0) = make_float2(acc[t][2], acc[t][3]);
-      }
-      __syncthreads();
-      const float* all = reinterpret_cast<const float*>(smem + S::kRed);
-      for (int i = tid; i < count * R; i += kRowThreads) {
-        float x = all[i];
-#pragma unroll
-        for (int w = 1; w < 8; ++w) x += all[w * TM * R + i];
-        part[i] = x;
-      }
-    } else {
+    {
       float* mine = part + (rg * 16) * R;
 #pragma unroll 1
       for (int h = 1; h >= 0; --h) {
@@ -447,11 +644,7 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_rows(const __grid_const
     return make_float4(j < r ? x.x * scale : 0.f, j + 1 < r ? x.y * scale : 0.f, j + 2 < r ? x.z * scale : 0.f,
                        j + 3 < r ? x.w * scale : 0.f);
   };
-  if constexpr (TM == 16) {  // few elements: every CTA sums all of them
-    for (int i = 4 * tid; i < TM * R; i += 4 * kRowThreads)
-      *reinterpret_cast<float4*>(full + i) = i < count * R ? summed(i) : make_float4(0.f, 0.f, 0.f, 0.f);
-    cluster_arrive();  // waited for at the end: no CTA leaves while its sums are read
-  } else {  // each CTA sums its rows for all
+  {  // each CTA sums its rows for all
     constexpr int share = TM * R / kCluster;
     for (int i = rankc * share + 4 * tid; i < (rankc + 1) * share; i += 4 * kRowThreads) {
       const float4 x = summed(i);
@@ -461,7 +654,6 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_rows(const __grid_const
     cluster_arrive();
     cluster_wait();
   }
-  if (TM == 16) __syncthreads();
   float m = 0.f;
   for (int i = tid; i < count * R; i += kRowThreads) {
     const float x = fabsf(full[i]);
@@ -498,8 +690,8 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_rows(const __grid_const
         thi[t][q] = half2_bits(x.hi, y.hi);
         tlo[t][q] = half2_bits(x.lo, y.lo);
       }
-    constexpr int NT = TM == 64 ? 4 : 2;  // 8-column tiles of a warp in a stage
-    const int cw = TM == 64 ? 32 * half : 16 * warp;
+    constexpr int NT = 4;  // 8-column tiles of a warp in a stage
+    const int cw = 32 * half;
     for (int i = nk; i < nk + nn; ++i) {
       cp_async_wait<S::kStages - 2>();
       __syncthreads();
@@ -550,7 +742,6 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_rows(const __grid_const
     }
   }
   cp_async_wait<0>();
-  if (TM == 16) cluster_wait();
 }
 
 // ---- weight gradients --------------------------------------------------------------------
@@ -740,18 +931,12 @@ cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, size_t smem, cudaS
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
-template <int TM, int R>
-cudaError_t launch_rows(const RowsArgs& args, int passes, int tiles, cudaStream_t stream) {
+template <int R>
+cudaError_t launch_rows(const RowsArgs& args, bool wide, int passes, int tiles, cudaStream_t stream) {
   void* a[] = {(void*)&args};
-  return launch_pdl((const void*)k_adapter_rows<TM, R>, dim3((unsigned)tiles * kCluster, passes), dim3(kRowThreads),
-                    RowsShape<TM, R>::smem, stream, a, dim3(kCluster, 1, 1));
-}
-template <int TM>
-cudaError_t launch_rows_r(const RowsArgs& args, int passes, int tiles, cudaStream_t stream) {
-  if (args.rp <= 16) return launch_rows<TM, 16>(args, passes, tiles, stream);
-  if (args.rp <= 32) return launch_rows<TM, 32>(args, passes, tiles, stream);
-  if (args.rp <= 64) return launch_rows<TM, 64>(args, passes, tiles, stream);
-  return launch_rows<TM, 128>(args, passes, tiles, stream);
+  const void* fn = wide ? (const void*)k_adapter_rows<R> : (const void*)k_adapter_few<R>;
+  return launch_pdl(fn, dim3((unsigned)tiles * kCluster, passes), dim3(kRowThreads), wide ? RowsShape<R>::smem : 0,
+                    stream, a, dim3(kCluster, 1, 1));
 }
 
 RowsArgs rows_args(const dictproj_adapters* a, const dictproj_rows* r, bool wide) {
@@ -781,8 +966,11 @@ RowsPass rows_pass(const dictproj_adapters* a, bool forward, const __half* in, c
   return p;
 }
 cudaError_t launch_rows_any(const RowsArgs& g, bool wide, int passes, const dictproj_rows* r, cudaStream_t stream) {
-  const int tiles = adapter_tiles(r->M, r->n_slots, wide ? 64 : 16);
-  return wide ? launch_rows_r<64>(g, passes, tiles, stream) : launch_rows_r<16>(g, passes, tiles, stream);
+  const int tiles = adapter_tiles(r->M, r->n_slots, wide ? kWideRows : kFewRows);
+  if (g.rp <= 16) return launch_rows<16>(g, wide, passes, tiles, stream);
+  if (g.rp <= 32) return launch_rows<32>(g, wide, passes, tiles, stream);
+  if (g.rp <= 64) return launch_rows<64>(g, wide, passes, tiles, stream);
+  return launch_rows<128>(g, wide, passes, tiles, stream);
 }
 
 template <int R>
@@ -792,14 +980,11 @@ cudaError_t launch_grad(const GradArgs& args, dim3 grid, cudaStream_t stream) {
                     dim3(1, 1, grid.z));
 }
 
-template <int TM, int R>
-cudaError_t allow_rows() {
-  return cudaFuncSetAttribute(k_adapter_rows<TM, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsShape<TM, R>::smem);
-}
 template <int R>
 cudaError_t allow_rank() {
   cudaError_t e;
-  if ((e = allow_rows<16, R>()) || (e = allow_rows<64, R>())) return e;
+  if ((e = cudaFuncSetAttribute(k_adapter_rows<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsShape<R>::smem)))
+    return e;
   return cudaFuncSetAttribute(k_adapter_grad<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, GradShape<R>::smem);
 }
 

@@ -136,7 +136,7 @@ struct dictproj_rows {
   int M;                   // rows of the last dictproj_rows_set (0: none yet)
   int* perm;               // [max_rows] row numbers by slot, rows without an adapter last
   int* start;              // [n_slots + 2] first position of each slot, of the rows without one, M
-  // tiles of up to 16 (index 0) and 64 (1) rows of one slot, in plan order; those of
+  // tiles of up to 4 (index 0) and 64 (1) rows of one slot, in plan order; those of
   // rows without an adapter (slot n_slots) come last
   int* n_tiles;            // [2][2] tiles of the slots, all tiles
   int4* tiles[2];          // {slot, first position, rows, row number of the first}

@@ -184,7 +184,7 @@ int dictproj_rows_create(int max_rows, int n_slots, dictproj_rows** out) {
   cudaError_t e;
   if ((e = dmalloc((void**)&r->perm, (size_t)max_rows * 4)) || (e = dmalloc((void**)&r->start, (size_t)(n_slots + 2) * 4)) ||
       (e = dmalloc((void**)&r->n_tiles, 4 * sizeof(int))) || (e = dmalloc((void**)&r->first64, (size_t)n_slots * 4)) ||
-      (e = dmalloc((void**)&r->tiles[0], (size_t)adapter_tiles(max_rows, n_slots, 16) * sizeof(int4))) ||
+      (e = dmalloc((void**)&r->tiles[0], (size_t)adapter_tiles(max_rows, n_slots, 4) * sizeof(int4))) ||
       (e = dmalloc((void**)&r->tiles[1], (size_t)adapter_tiles(max_rows, n_slots, 64) * sizeof(int4)))) {
     dictproj_free_rows(r);
     cudaGetLastError();
