@@ -194,8 +194,8 @@ __device__ __forceinline__ float ld_peer_f32(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void st_peer_v4f(uint32_t addr, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+__device__ __forceinline__ void st_peer_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 // 16 bytes global -> shared, the last 16 - bytes of them zeros
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -228,22 +228,53 @@ __device__ __forceinline__ uint32_t swz(int row, int p) {
   return (uint32_t)(row * PITCH + 16 * (p ^ ((row >> shift) & mask)));
 }
 
-// 8 elements from column c of a row of n elements into shared memory, zeros past the
-// end; asynchronously where rows keep 16-byte alignment (vec: n % 8 == 0).
-__device__ __forceinline__ void load_piece(uint32_t dst, const __half* row, int c, int n, bool vec) {
-  if (vec) {
-    const bool in = c < n;
-    cp_async16(dst, in ? row + c : row, in ? 16 : 0);
-  } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const unsigned short a = c + 2 * i < n ? __half_as_ushort(row[c + 2 * i]) : 0;
-      const unsigned short b = c + 2 * i + 1 < n ? __half_as_ushort(row[c + 2 * i + 1]) : 0;
-      w[i] = (uint32_t)a | ((uint32_t)b << 16);
-    }
-    sts16(dst, make_uint4(w[0], w[1], w[2], w[3]));
+// 8 elements from column c of a row of n elements, zeros past the end. Rows of an odd
+// length start at any even byte: two aligned 16-byte loads and a shift, as long as both
+// lie inside the array (which ends at `end`), single elements otherwise.
+__device__ __forceinline__ uint4 read_piece(const __half* row, int c, int n, bool vec, const __half* end) {
+  if (vec) return c < n ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+  const uint4* q = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
+  if (c + 8 <= n && reinterpret_cast<uintptr_t>(q + 2) <= reinterpret_cast<uintptr_t>(end)) {
+    const uint4 a = q[0], b = q[1];
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const uint32_t words = (uint32_t)(at >> 2) & 3u, shift = 8u * ((uint32_t)at & 2u);
+    if (words & 2) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = w[6], w[5] = w[7];
+    if (words & 1) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
+    return make_uint4(__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift),
+                      __funnelshift_r(w[2], w[3], shift), __funnelshift_r(w[3], w[4], shift));
   }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned short a = c + 2 * i < n ? __half_as_ushort(row[c + 2 * i]) : 0;
+    const unsigned short b = c + 2 * i + 1 < n ? __half_as_ushort(row[c + 2 * i + 1]) : 0;
+    w[i] = (uint32_t)a | ((uint32_t)b << 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void write_piece(__half* row, int c, int n, bool vec, const uint4& v) {
+  if (vec) {
+    if (c < n) *reinterpret_cast<uint4*>(row + c) = v;
+    return;
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (c + 8 <= n) {
+    unsigned short* h = reinterpret_cast<unsigned short*>(row + c);
+    if ((reinterpret_cast<uintptr_t>(h) & 2) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(h)[i] = w[i];
+    } else {
+      h[0] = (unsigned short)w[0];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t*>(h + 1 + 2 * i) = __funnelshift_r(w[i], w[i + 1], 16);
+      h[7] = (unsigned short)(w[3] >> 16);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c + e < n) row[c + e] = __ushort_as_half((unsigned short)(w[e >> 1] >> (16 * (e & 1))));
 }
 
 // T in two fp16 parts: t * unit = high + low with |t * unit| < 2^14, so that the two
@@ -266,7 +297,7 @@ __device__ __forceinline__ float split_unit(float m) {
   return __uint_as_float((uint32_t)(min(13 - e, 126) + 127) << 23);
 }
 
-// ---- rows: contraction and expansion in one launch --------------------------------------
+// ---- contraction and expansion -------------------------------------------------------------
 constexpr int kCluster = 8;
 constexpr int kRowThreads = 256;
 
@@ -276,7 +307,7 @@ struct RowsPass {
   const __half* Q;
   const __half* base;
   __half* out;
-  __half* hi;  // parts of scale * T for the weight gradients, or null
+  __half* hi;  // the two parts of scale * T (many rows)
   __half* lo;
   float* unit;
   int K, N, ld_p, ld_q;
@@ -288,7 +319,7 @@ struct RowsArgs {
   const int* perm;
   const int* rank;
   const float* scale;
-  int rp, n_slots;
+  int rp, n_slots, rows, cluster;
 };
 
 // ---- few rows of a slot: serving ----------------------------------------------------------
@@ -310,29 +341,6 @@ __device__ __forceinline__ void dot8(float& acc, const uint4& x, const uint4& w)
   dot2(acc, x.z, w.z);
   dot2(acc, x.w, w.w);
 }
-// 8 elements from column c of a row of n elements, zeros past the end.
-__device__ __forceinline__ uint4 read_piece(const __half* row, int c, int n, bool vec) {
-  if (vec) return *reinterpret_cast<const uint4*>(row + c);
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const unsigned short a = c + 2 * i < n ? __half_as_ushort(row[c + 2 * i]) : 0;
-    const unsigned short b = c + 2 * i + 1 < n ? __half_as_ushort(row[c + 2 * i + 1]) : 0;
-    w[i] = (uint32_t)a | ((uint32_t)b << 16);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void write_piece(__half* row, int c, int n, bool vec, const uint4& v) {
-  if (vec) {
-    *reinterpret_cast<uint4*>(row + c) = v;
-    return;
-  }
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (c + e < n) row[c + e] = __ushort_as_half((unsigned short)(w[e >> 1] >> (16 * (e & 1))));
-}
-
 struct FewTile {
   int row[kFewRows];
   int count, r, rankc;
@@ -350,10 +358,9 @@ __device__ __forceinline__ void prefetch_rows(const __half* w, int ld, int lo, i
   }
 }
 
-template <int R, int NR>
-__device__ __forceinline__ void few_rows(const RowsPass& a, const FewTile& f, float* part, float* full) {
+template <int R, int NR, bool VEC>
+__device__ __forceinline__ void few_rows(const RowsPass& a, int n_rows, const FewTile& f, float* part, float* full) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool vec_in = (a.K & 7) == 0, vec_out = (a.N & 7) == 0;
   const int kp = (a.K + 7) / 8, np = (a.N + 7) / 8;
   const int n_lo = np * f.rankc / kCluster, n_hi = np * (f.rankc + 1) / kCluster;
   if (R > 16) prefetch_rows(f.Q, a.ld_q, n_lo, n_hi, 16, f.r);
@@ -367,7 +374,7 @@ __device__ __forceinline__ void few_rows(const RowsPass& a, const FewTile& f, fl
   for (int p = kp * f.rankc / kCluster + lane; p < k_hi; p += 32) {
     uint4 x[NR];
 #pragma unroll
-    for (int m = 0; m < NR; ++m) x[m] = read_piece(a.in + (size_t)f.row[m] * a.K, 8 * p, a.K, vec_in);
+    for (int m = 0; m < NR; ++m) x[m] = read_piece(a.in + (size_t)f.row[m] * a.K, 8 * p, a.K, VEC, a.in + (size_t)n_rows * a.K);
 #pragma unroll
     for (int j = 0; j < R / 8; ++j) {
       const int rank = warp + 8 * j;
@@ -419,7 +426,7 @@ __device__ __forceinline__ void few_rows(const RowsPass& a, const FewTile& f, fl
       for (int m = 1; m < NR; ++m) mr = js == m ? f.row[m] : mr;
       brow = a.base + (size_t)mr * a.N;
       orow = a.out + (size_t)mr * a.N;
-      if (a.base) b = read_piece(brow, 8 * p, a.N, vec_out);
+      if (a.base) b = read_piece(brow, 8 * p, a.N, VEC, a.base + (size_t)n_rows * a.N);
     }
     if (in)
 #pragma unroll 4
@@ -451,7 +458,7 @@ __device__ __forceinline__ void few_rows(const RowsPass& a, const FewTile& f, fl
       const float2 b2 = __half22float2(*reinterpret_cast<const __half2*>(&b.z)), b3 = __half22float2(*reinterpret_cast<const __half2*>(&b.w));
       const __half2 h0 = __floats2half2_rn(b0.x + o[0], b0.y + o[1]), h1 = __floats2half2_rn(b1.x + o[2], b1.y + o[3]);
       const __half2 h2 = __floats2half2_rn(b2.x + o[4], b2.y + o[5]), h3 = __floats2half2_rn(b3.x + o[6], b3.y + o[7]);
-      write_piece(orow, 8 * p, a.N, vec_out,
+      write_piece(orow, 8 * p, a.N, VEC,
                   make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
                              *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3)));
     }
@@ -459,18 +466,19 @@ __device__ __forceinline__ void few_rows(const RowsPass& a, const FewTile& f, fl
   cluster_wait();
 }
 
-// base alone, for rows without an adapter: this CTA's share of the columns
-__device__ __forceinline__ void copy_rows(const RowsPass& a, const int* rows, int count, int rankc) {
+// base alone, for rows without an adapter: pieces [lo, hi) of the columns
+__device__ __forceinline__ void copy_rows(const RowsPass& a, int n_rows, const int* rows, int count, int lo, int hi) {
   const bool vec = (a.N & 7) == 0;
-  const int np = (a.N + 7) / 8, lo = np * rankc / kCluster, n = np * (rankc + 1) / kCluster - lo;
+  const int n = hi - lo;
   for (int i = threadIdx.x; i < count * n; i += kRowThreads) {
     const size_t at = (size_t)rows[i / n] * a.N;
     const int c = 8 * (lo + i % n);
-    write_piece(a.out + at, c, a.N, vec, a.base ? read_piece(a.base + at, c, a.N, vec) : make_uint4(0, 0, 0, 0));
+    write_piece(a.out + at, c, a.N, vec, a.base ? read_piece(a.base + at, c, a.N, vec, a.base + (size_t)n_rows * a.N) : make_uint4(0, 0, 0, 0));
   }
 }
 
-template <int R>
+// VEC: K and N are multiples of 8, every row 16-byte aligned.
+template <int R, bool VEC>
 __global__ void __launch_bounds__(kRowThreads, R <= 32 ? 4 : 2) k_adapter_few(const __grid_constant__ RowsArgs g) {
   __shared__ __align__(16) float part[kFewRows * R], full[kFewRows * R];
   const RowsPass& a = g.pass[blockIdx.y];
@@ -496,250 +504,296 @@ __global__ void __launch_bounds__(kRowThreads, R <= 32 ? 4 : 2) k_adapter_few(co
 #pragma unroll
   for (int m = 1; m < kFewRows; ++m) f.row[m] = m < f.count ? g.perm[tile.y + m] : tile.w;
   if (f.r == 0) {
-    if (!in_place) copy_rows(a, g.perm + tile.y, f.count, f.rankc);
+    const int np = (a.N + 7) / 8;
+    if (!in_place)
+      copy_rows(a, g.rows, g.perm + tile.y, f.count, np * f.rankc / kCluster, np * (f.rankc + 1) / kCluster);
     return;
   }
   f.scale = g.scale[tile.x];
-  if (f.count == 1) few_rows<R, 1>(a, f, part, full);
-  else few_rows<R, kFewRows>(a, f, part, full);
+  if (f.count == 1) few_rows<R, 1, VEC>(a, g.rows, f, part, full);
+  else few_rows<R, kFewRows, VEC>(a, g.rows, f, part, full);
 }
 
 // ---- many rows of a slot: prefill and training ----------------------------------------------
-// A cluster of kCluster CTAs takes one tile of up to kWideRows rows of one slot:
-//   1. CTA c contracts its share of the K columns of In with P_s (rows x K by K x r on
-//      mma.sync, warps split over rows and over the 16-column steps);
-//   2. the CTAs' partial sums meet through distributed shared memory, in rank order;
-//   3. CTA c expands T into its share of the N columns of Out, adding base.
-// One ring of 64-column stages (cp.async) runs through both phases, so that the first
-// Q and base tiles arrive while T is being summed.
+// Two launches, so that each has a grid of its own: tiles x K-splits for the contraction,
+// tiles x column blocks for the expansion (one launch for both, a cluster a tile, left
+// each CTA a chain of eight loads and two cluster barriers, and at 2048 rows of rank 32
+// took 27 us). T passes through the pool's workspace in its two fp16 parts; the weight
+// gradients read the same parts.
+//
+// Contraction: a cluster splits the K columns of one tile of up to kWideRows rows; every
+// CTA streams its share in 64-column stages (cp.async) through mma.sync, the partial sums
+// meet through distributed shared memory, in rank order, and each CTA writes its share of
+// the tile's rows.
 template <int R>
-struct RowsShape {
+struct ContractShape {
   static constexpr int TM = kWideRows, CW = 64;  // rows, columns of a stage
   static constexpr int kPitch = 2 * CW;
-  static constexpr int kStages = R == 128 ? 3 : 4;
+  static constexpr int kStages = 4;
   static constexpr int kInBytes = TM * kPitch, kStageBytes = (TM + R) * kPitch;
-  static constexpr int kPart = kStages * kStageBytes, kFull = kPart + TM * R * 4;
-  static constexpr int smem = kFull + TM * R * 4;
+  static constexpr int kPart = kStages * kStageBytes;
+  static constexpr int smem = kPart + TM * R * 4;
 };
 
 template <int R>
-__global__ void __launch_bounds__(kRowThreads) k_adapter_rows(const __grid_constant__ RowsArgs g) {
-  using S = RowsShape<R>;
-  constexpr int TM = S::TM, CW = S::CW, PITCH = S::kPitch, PIECES = PITCH / 16;
+__global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_constant__ RowsArgs g) {
+  using S = ContractShape<R>;
+  constexpr int TM = S::TM, CW = S::CW, PITCH = S::kPitch, PIECES = PITCH / 16, STEP = kRowThreads / PIECES;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int srow[TM];
-  __shared__ float smax[kRowThreads / 32];
+  __shared__ __align__(16) float smax[kRowThreads / 32], cmax[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rankc = blockIdx.x % kCluster, tile_no = blockIdx.x / kCluster;
+  const int cluster = g.cluster, rankc = blockIdx.x % cluster, tile_no = blockIdx.x / cluster;
   const RowsPass& a = g.pass[blockIdx.y];
   float* part = reinterpret_cast<float*>(smem + S::kPart);
-  float* full = reinterpret_cast<float*>(smem + S::kFull);
   const uint32_t ring = smem_u32(smem);
 
   grid_dependency_wait();
   trigger_dependents();
-  // rows whose output is already in place need no tile of their own
-  const bool in_place = a.out == nullptr || a.base == a.out;
   const int4 tile = g.tiles[tile_no];
-  if (tile_no >= g.n_tiles[in_place ? 0 : 1]) return;  // the whole cluster
-  const int count = tile.z, slot = tile.x;
-  const int r = slot < g.n_slots ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
-  if (tid < TM) srow[tid] = tid < count ? g.perm[tile.y + tid] : 0;
-  const bool vec_in = (a.K & 7) == 0, vec_out = (a.N & 7) == 0;
-  const int kc = (a.K + CW - 1) / CW, nc = a.out ? (a.N + CW - 1) / CW : 0;
-  const int n_lo = nc * rankc / kCluster, nn = nc * (rankc + 1) / kCluster - n_lo;
-  __syncthreads();
-  if (r == 0) {  // base alone
-    if (!in_place) copy_rows(a, srow, count, rankc);
-    return;
-  }
+  if (tile_no >= g.n_tiles[0]) return;  // the whole cluster
+  const int count = tile.z, slot = tile.x, r = g.rank[slot], r16 = (r + 15) & ~15;
+  if (r == 0) return;
+  if (tid < TM) srow[tid] = tid < count ? g.perm[tile.y + tid] : tile.w;
+  const bool vec = (a.K & 7) == 0;
+  const int kc = (a.K + CW - 1) / CW, k_lo = kc * rankc / cluster, nk = kc * (rankc + 1) / cluster - k_lo;
   const float scale = g.scale[slot];
-  const int k_lo = kc * rankc / kCluster, nk = kc * (rankc + 1) / kCluster - k_lo;
-  const __half* P = a.P + (size_t)slot * g.rp * a.ld_p;
-  const __half* Q = a.Q + (size_t)slot * g.rp * a.ld_q;
-  // rows past the tile's stay zero in every stage
-  for (int i = tid; i < S::kStages * (TM - count) * PIECES; i += kRowThreads) {
-    const int st = i / ((TM - count) * PIECES), row = count + i / PIECES % (TM - count);
-    sts16(ring + st * S::kStageBytes + swz<PITCH>(row, i % PIECES), make_uint4(0, 0, 0, 0));
-  }
+  __syncthreads();
+  // this thread's 16-byte column and rows of a stage
+  const int piece = tid % PIECES, row0 = tid / PIECES;
+  const uint32_t spot = swz<PITCH>(row0, piece);
+  const __half* wp = a.P + ((size_t)slot * g.rp + row0) * a.ld_p + 8 * piece;
+  const __half* line[TM / STEP];
+#pragma unroll
+  for (int i = 0; i < TM / STEP; ++i) line[i] = a.in + (size_t)srow[row0 + STEP * i] * a.K;
   auto issue = [&](int i) {
-    if (i < nk + nn) {
-      const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
-      const bool first = i < nk;
-      const int col = first ? (k_lo + i) * CW : (n_lo + i - nk) * CW;
-      const __half* src = first ? a.in : a.base;
-      const int n = first ? a.K : a.N;
-      if (src)
-        for (int q = tid; q < count * PIECES; q += kRowThreads) {
-          const int row = q / PIECES, p = q % PIECES;
-          load_piece(st + swz<PITCH>(row, p), src + (size_t)srow[row] * n, col + 8 * p, n, first ? vec_in : vec_out);
-        }
-      const __half* w = first ? P : Q;
-      const int ld = first ? a.ld_p : a.ld_q;
-      for (int q = tid; q < r16 * PIECES; q += kRowThreads) {
-        const int row = q / PIECES, p = q % PIECES;
-        load_piece(st + S::kInBytes + swz<PITCH>(row, p), w + (size_t)row * ld, col + 8 * p, ld, true);
+    if (i < nk) {
+      const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes + spot;
+      const int col = (k_lo + i) * CW, c = col + 8 * piece;
+#pragma unroll
+      for (int q = 0; q < TM / STEP; ++q) {
+        const bool in = row0 + STEP * q < count && c < a.K;
+        if (vec) cp_async16(st + STEP * q * PITCH, line[q] + (in ? c : 0), in ? 16 : 0);
+        else sts16(st + STEP * q * PITCH, in ? read_piece(line[q], c, a.K, false, a.in + (size_t)g.rows * a.K) : make_uint4(0, 0, 0, 0));
       }
+      const bool in = c < a.ld_p;
+#pragma unroll
+      for (int j = 0; j < (R + STEP - 1) / STEP; ++j)
+        if (row0 + STEP * j < r16)
+          cp_async16(st + S::kInBytes + STEP * j * PITCH, in ? wp + (size_t)(STEP * j) * a.ld_p + col : wp, in ? 16 : 0);
     }
     cp_async_commit();
   };
   for (int i = 0; i < S::kStages - 1; ++i) issue(i);
 
-  const int rg = warp & 3, half = warp >> 2;
-  {  // 1. contraction
-    float acc[R / 8][4];
+  const int rg = warp & 3, half = warp >> 2, g0 = lane >> 2, c0 = 2 * (lane & 3);
+  float acc[R / 8][4];
 #pragma unroll
-    for (int t = 0; t < R / 8; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-    for (int i = 0; i < nk; ++i) {
-      cp_async_wait<S::kStages - 2>();
-      __syncthreads();
-      issue(i + S::kStages - 1);
-      const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
+  for (int t = 0; t < R / 8; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+  for (int i = 0; i < nk; ++i) {
+    cp_async_wait<S::kStages - 2>();
+    __syncthreads();
+    issue(i + S::kStages - 1);
+    const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        const int k16 = half * 2 + kk;
-        uint32_t af[4];
-        ldmatrix4(af, st + swz<PITCH>(rg * 16 + (lane & 15), 2 * k16 + (lane >> 4)));
-#pragma unroll
-        for (int t = 0; t < R / 16; ++t) {
-          if (16 * t >= r16) break;
-          uint32_t bf[4];
-          ldmatrix4(bf, st + S::kInBytes + swz<PITCH>(16 * t + (lane & 7) + (lane >> 4) * 8, 2 * k16 + ((lane >> 3) & 1)));
-          mma_16816(acc[2 * t], af, bf);
-          mma_16816(acc[2 * t + 1], af, bf + 2);
-        }
-      }
-    }
-    // the CTA's sum, warps in order
-    const int g0 = lane >> 2, c0 = 2 * (lane & 3);
-    {
-      float* mine = part + (rg * 16) * R;
-#pragma unroll 1
-      for (int h = 1; h >= 0; --h) {
-        if (half == h)
-#pragma unroll
-          for (int t = 0; t < R / 8; ++t) {
-            float2* lo = reinterpret_cast<float2*>(mine + g0 * R + 8 * t + c0);
-            float2* hi = reinterpret_cast<float2*>(mine + (g0 + 8) * R + 8 * t + c0);
-            const float2 x = h ? make_float2(0.f, 0.f) : *lo, y = h ? make_float2(0.f, 0.f) : *hi;
-            *lo = make_float2(acc[t][0] + x.x, acc[t][1] + x.y);
-            *hi = make_float2(acc[t][2] + y.x, acc[t][3] + y.y);
-          }
-        __syncthreads();
-      }
-    }
-  }
-  cluster_arrive();
-  cluster_wait();
-  // 2. the cluster's sum: scale * T, zero past the slot's rank
-  const uint32_t pbase = smem_u32(part), fbase = smem_u32(full);
-  auto summed = [&](int i) {  // four elements of the tile, CTAs in order
-    float4 x = ld_peer_v4f(peer_smem(pbase + 4 * i, 0));
-#pragma unroll
-    for (int c = 1; c < kCluster; ++c) {
-      const float4 y = ld_peer_v4f(peer_smem(pbase + 4 * i, c));
-      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-    }
-    const int j = i % R;
-    return make_float4(j < r ? x.x * scale : 0.f, j + 1 < r ? x.y * scale : 0.f, j + 2 < r ? x.z * scale : 0.f,
-                       j + 3 < r ? x.w * scale : 0.f);
-  };
-  {  // each CTA sums its rows for all
-    constexpr int share = TM * R / kCluster;
-    for (int i = rankc * share + 4 * tid; i < (rankc + 1) * share; i += 4 * kRowThreads) {
-      const float4 x = summed(i);
-#pragma unroll
-      for (int c = 0; c < kCluster; ++c) st_peer_v4f(peer_smem(fbase + 4 * i, c), x);
-    }
-    cluster_arrive();
-    cluster_wait();
-  }
-  float m = 0.f;
-  for (int i = tid; i < count * R; i += kRowThreads) {
-    const float x = fabsf(full[i]);
-    if (x <= 3.0e38f) m = fmaxf(m, x);  // an infinity or NaN does not decide the others' digits
-  }
-#pragma unroll
-  for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  if (lane == 0) smax[warp] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kRowThreads / 32; ++w) m = fmaxf(m, smax[w]);
-  const float unit = split_unit(m), back = 1.f / unit;
-  if (a.hi) {  // T for the weight gradients: this CTA's share of the rows
-    for (int i = tid; i < count * r16; i += kRowThreads) {
-      const int row = i / r16, j = i % r16;
-      if (row % kCluster != rankc) continue;
-      const Split s = split_half(full[row * R + j] * unit);
-      const size_t at = (size_t)(tile.y + row) * g.rp + j;
-      a.hi[at] = s.hi;
-      a.lo[at] = s.lo;
-    }
-    if (rankc == 0 && tid == 0) a.unit[tile_no] = back;
-  }
-  // 3. expansion
-  if (nn > 0) {
-    uint32_t thi[R / 16][4], tlo[R / 16][4];
-    const int g0 = rg * 16 + (lane >> 2), c0 = 2 * (lane & 3);
-#pragma unroll
-    for (int t = 0; t < R / 16; ++t)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float* f = full + (g0 + 8 * (q & 1)) * R + 16 * t + c0 + 8 * (q >> 1);
-        const Split x = split_half(f[0] * unit), y = split_half(f[1] * unit);
-        thi[t][q] = half2_bits(x.hi, y.hi);
-        tlo[t][q] = half2_bits(x.lo, y.lo);
-      }
-    constexpr int NT = 4;  // 8-column tiles of a warp in a stage
-    const int cw = 32 * half;
-    for (int i = nk; i < nk + nn; ++i) {
-      cp_async_wait<S::kStages - 2>();
-      __syncthreads();
-      issue(i + S::kStages - 1);
-      const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
-      float acc[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+    for (int kk = 0; kk < CW / 32; ++kk) {
+      const int k16 = half * (CW / 32) + kk;
+      uint32_t af[4];
+      ldmatrix4(af, st + swz<PITCH>(rg * 16 + (lane & 15), 2 * k16 + (lane >> 4)));
 #pragma unroll
       for (int t = 0; t < R / 16; ++t) {
         if (16 * t >= r16) break;
-#pragma unroll
-        for (int n = 0; n < NT / 2; ++n) {
-          uint32_t bf[4];
-          ldmatrix4_t(bf, st + S::kInBytes + swz<PITCH>(16 * t + (lane & 15), cw / 8 + 2 * n + (lane >> 4)));
-          mma_16816(acc[2 * n], tlo[t], bf);
-          mma_16816(acc[2 * n], thi[t], bf);
-          mma_16816(acc[2 * n + 1], tlo[t], bf + 2);
-          mma_16816(acc[2 * n + 1], thi[t], bf + 2);
-        }
-      }
-      // base + acc, rounded once, over the base tile, then out in 16-byte pieces
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint32_t at = st + swz<PITCH>(g0 + 8 * q, cw / 8 + n) + 2 * c0;
-          const uint32_t bw = a.base ? lds_u32(at) : 0u;
-          const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&bw));
-          const __half2 o = __floats2half2_rn(fmaf(acc[n][2 * q], back, b.x), fmaf(acc[n][2 * q + 1], back, b.y));
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(*reinterpret_cast<const uint32_t*>(&o)) : "memory");
-        }
-      __syncthreads();
-      const int col = (n_lo + i - nk) * CW;
-      for (int q = tid; q < count * PIECES; q += kRowThreads) {
-        const int row = q / PIECES, c = col + 8 * (q % PIECES);
-        __half* dst = a.out + (size_t)srow[row] * a.N + c;
-        const uint4 v = lds_u32x4(st + swz<PITCH>(row, q % PIECES));
-        if (vec_out) {
-          if (c < a.N) *reinterpret_cast<uint4*>(dst) = v;
-        } else {
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c + e < a.N) dst[e] = __ushort_as_half((unsigned short)(w[e >> 1] >> (16 * (e & 1))));
-        }
+        uint32_t bf[4];
+        ldmatrix4(bf, st + S::kInBytes + swz<PITCH>(16 * t + (lane & 7) + (lane >> 4) * 8, 2 * k16 + ((lane >> 3) & 1)));
+        mma_16816(acc[2 * t], af, bf);
+        mma_16816(acc[2 * t + 1], af, bf + 2);
       }
     }
+  }
+  // the CTA's sum: the second half of the steps, then the first on top
+  float* mine = part + (rg * 16) * R;
+#pragma unroll 1
+  for (int h = 1; h >= 0; --h) {
+    if (half == h)
+#pragma unroll
+      for (int t = 0; t < R / 8; ++t) {
+        if (8 * t >= r16) break;
+        float2* lo = reinterpret_cast<float2*>(mine + g0 * R + 8 * t + c0);
+        float2* hi = reinterpret_cast<float2*>(mine + (g0 + 8) * R + 8 * t + c0);
+        const float2 x = h ? make_float2(0.f, 0.f) : *lo, y = h ? make_float2(0.f, 0.f) : *hi;
+        *lo = make_float2(acc[t][0] + x.x, acc[t][1] + x.y);
+        *hi = make_float2(acc[t][2] + y.x, acc[t][3] + y.y);
+      }
+    __syncthreads();
+  }
+  cp_async_wait<0>();
+  cluster_arrive();
+  cluster_wait();
+  // the cluster's sum of this CTA's share, CTAs in order: scale * T, zero past the rank
+  float* own = reinterpret_cast<float*>(smem);  // [TM / cluster][R], over the drained ring
+  const uint32_t pbase = smem_u32(part);
+  const int share = TM / cluster, row_lo = rankc * share;
+  float m = 0.f;
+  for (int i = 4 * tid; i < share * R; i += 4 * kRowThreads) {
+    const int j = i % R, row = row_lo + i / R;
+    if (j >= r16 || row >= count) continue;
+    const uint32_t at = pbase + 4 * (row * R + j);
+    float4 x = ld_peer_v4f(peer_smem(at, 0));
+    for (int c = 1; c < cluster; ++c) {
+      const float4 y = ld_peer_v4f(peer_smem(at, c));
+      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    const float v[4] = {j < r ? x.x * scale : 0.f, j + 1 < r ? x.y * scale : 0.f, j + 2 < r ? x.z * scale : 0.f,
+                        j + 3 < r ? x.w * scale : 0.f};
+    *reinterpret_cast<float4*>(own + i) = make_float4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (fabsf(v[e]) <= 3.0e38f) m = fmaxf(m, fabsf(v[e]));  // an infinity or NaN does not decide the others' digits
+  }
+  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+  if (lane == 0) smax[warp] = m;
+  __syncthreads();
+  if (tid < cluster) {
+#pragma unroll
+    for (int w = 0; w < kRowThreads / 32; ++w) m = fmaxf(m, smax[w]);
+    st_peer_f32(peer_smem(smem_u32(cmax + rankc), tid), m);
+  }
+  cluster_arrive();
+  cluster_wait();
+  m = 0.f;
+  for (int c = 0; c < cluster; ++c) m = fmaxf(m, cmax[c]);
+  const float unit = split_unit(m);
+  if (rankc == 0 && tid == 0) a.unit[tile_no] = 1.f / unit;
+  for (int i = 4 * tid; i < share * R; i += 4 * kRowThreads) {
+    const int j = i % R, row = row_lo + i / R;
+    if (j >= r16 || row >= count) continue;
+    const float4 x = *reinterpret_cast<const float4*>(own + i);
+    const Split s0 = split_half(x.x * unit), s1 = split_half(x.y * unit), s2 = split_half(x.z * unit), s3 = split_half(x.w * unit);
+    const size_t at = (size_t)(tile.y + row) * g.rp + j;
+    *reinterpret_cast<uint2*>(a.hi + at) = make_uint2(half2_bits(s0.hi, s1.hi), half2_bits(s2.hi, s3.hi));
+    *reinterpret_cast<uint2*>(a.lo + at) = make_uint2(half2_bits(s0.lo, s1.lo), half2_bits(s2.lo, s3.lo));
+  }
+}
+
+// Expansion: a CTA takes a range of 128-column blocks of one tile; T's parts sit in MMA
+// fragments throughout, the base tile and r rows of Q of the next blocks arrive (cp.async)
+// while one is computed. The launch before is the contraction of the same call, which lets
+// this one start only after its own dependency wait: all that was written before the call
+// (plan, weights, base) is complete, so it is read before this kernel's wait, and only T
+// and the output come after it.
+template <int R>
+struct ExpandShape {
+  static constexpr int TM = kWideRows, CW = 128, kPitch = 2 * CW;
+  static constexpr int kStages = R <= 32 ? 3 : 2, kStageBytes = (TM + R) * kPitch;
+  static constexpr int smem = kStages * kStageBytes;
+};
+
+template <int R>
+__global__ void __launch_bounds__(kRowThreads) k_adapter_expand(const __grid_constant__ RowsArgs g) {
+  using S = ExpandShape<R>;
+  constexpr int TM = S::TM, CW = S::CW, PITCH = S::kPitch;
+  static_assert(kRowThreads == 16 * PITCH / 16, "a thread loads one 16-byte column of every 16th row");
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const RowsPass& a = g.pass[0];
+  trigger_dependents();
+  const int tile_no = blockIdx.y;
+  const bool in_place = a.base == a.out;
+  const int4 tile = g.tiles[tile_no];
+  if (tile_no >= g.n_tiles[in_place ? 0 : 1]) {
+    grid_dependency_wait();
+    return;
+  }
+  const int count = tile.z, slot = tile.x;
+  const int r = slot < g.n_slots ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
+  const bool vec = (a.N & 7) == 0;
+  const int blocks = (a.N + CW - 1) / CW, b_lo = blocks * blockIdx.x / gridDim.x;
+  const int nb = blocks * (blockIdx.x + 1) / gridDim.x - b_lo;
+  if (r == 0) {  // base alone
+    grid_dependency_wait();
+    if (!in_place)
+      copy_rows(a, g.rows, g.perm + tile.y, count, b_lo * (CW / 8), min((b_lo + nb) * (CW / 8), (a.N + 7) / 8));
+    return;
+  }
+  const int piece = tid & 15, row0 = tid >> 4;
+  const uint32_t spot = smem_u32(smem) + swz<PITCH>(row0, piece);
+  int row[TM / 16];
+#pragma unroll
+  for (int i = 0; i < TM / 16; ++i) row[i] = row0 + 16 * i < count ? g.perm[tile.y + row0 + 16 * i] : -1;
+  const __half* wq = a.Q + ((size_t)slot * g.rp + row0) * a.ld_q;
+  auto issue = [&](int i) {
+    if (i < nb) {
+      const uint32_t dst = spot + (uint32_t)(i % S::kStages) * S::kStageBytes;
+      const int c = (b_lo + i) * CW + 8 * piece;
+      const bool inq = c < a.ld_q;
+#pragma unroll
+      for (int j = 0; j < R / 16; ++j)
+        if (16 * j < r16) cp_async16(dst + (TM + 16 * j) * PITCH, wq + (inq ? (size_t)(16 * j) * a.ld_q + c : 0), inq ? 16 : 0);
+      if (a.base)
+#pragma unroll
+        for (int q = 0; q < TM / 16; ++q) {
+          const bool in = row[q] >= 0 && c < a.N;
+          const __half* line = a.base + (size_t)max(row[q], 0) * a.N;
+          if (vec) cp_async16(dst + 16 * q * PITCH, line + (in ? c : 0), in ? 16 : 0);
+          else sts16(dst + 16 * q * PITCH, in ? read_piece(line, c, a.N, false, a.base + (size_t)g.rows * a.N) : make_uint4(0, 0, 0, 0));
+        }
+    }
+    cp_async_commit();
+  };
+  for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+  grid_dependency_wait();
+  const int rg = warp & 3, half = warp >> 2, g0 = rg * 16 + (lane >> 2), c0 = 2 * (lane & 3);
+  uint32_t thi[R / 16][4], tlo[R / 16][4];
+#pragma unroll
+  for (int t = 0; t < R / 16; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int tr = g0 + 8 * (q & 1);
+      const size_t at = (size_t)(tile.y + tr) * g.rp + 16 * t + c0 + 8 * (q >> 1);
+      const bool in = tr < count && 16 * t < r16;
+      thi[t][q] = in ? *reinterpret_cast<const uint32_t*>(a.hi + at) : 0u;
+      tlo[t][q] = in ? *reinterpret_cast<const uint32_t*>(a.lo + at) : 0u;
+    }
+  const float back = a.unit[tile_no];
+  constexpr int NT = CW / 16;  // 8-column tiles of a warp
+  const int cw = 8 * NT * half;
+  for (int i = 0; i < nb; ++i) {
+    cp_async_wait<S::kStages - 2>();
+    __syncthreads();
+    issue(i + S::kStages - 1);
+    const uint32_t off = (uint32_t)(i % S::kStages) * S::kStageBytes, st = smem_u32(smem) + off;
+    float acc[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+#pragma unroll
+    for (int t = 0; t < R / 16; ++t) {
+      if (16 * t >= r16) break;
+#pragma unroll
+      for (int n = 0; n < NT / 2; ++n) {
+        uint32_t bf[4];
+        ldmatrix4_t(bf, st + swz<PITCH>(TM + 16 * t + (lane & 15), cw / 8 + 2 * n + (lane >> 4)));
+        mma_16816(acc[2 * n], tlo[t], bf);
+        mma_16816(acc[2 * n + 1], tlo[t], bf + 2);
+        mma_16816(acc[2 * n], thi[t], bf);
+        mma_16816(acc[2 * n + 1], thi[t], bf + 2);
+      }
+    }
+    // base + acc, rounded once, over the base tile, then out in 16-byte pieces
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t at = st + swz<PITCH>(g0 + 8 * q, cw / 8 + n) + 2 * c0;
+        const uint32_t bw = a.base ? lds_u32(at) : 0u;
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&bw));
+        const __half2 o = __floats2half2_rn(fmaf(acc[n][2 * q], back, b.x), fmaf(acc[n][2 * q + 1], back, b.y));
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(*reinterpret_cast<const uint32_t*>(&o)) : "memory");
+      }
+    __syncthreads();
+    const int c = (b_lo + i) * CW + 8 * piece;
+#pragma unroll
+    for (int q = 0; q < TM / 16; ++q)
+      if (row[q] >= 0) write_piece(a.out + (size_t)row[q] * a.N, c, a.N, vec, lds_u32x4(spot + off + 16 * q * PITCH));
   }
   cp_async_wait<0>();
 }
@@ -768,7 +822,7 @@ struct GradArgs {
   const int* first64;
   const int* perm;
   const int* rank;
-  int rp, max_rank, accumulate;
+  int rp, max_rank, accumulate, n_rows;
 };
 
 template <int R>
@@ -789,13 +843,13 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
   const GradPass& a = g.pass[which];
   const int col0 = ((int)blockIdx.x - (which ? g.pass[0].blocks : 0)) * kGradCols;
   const uint32_t ring = smem_u32(smem);
-  grid_dependency_wait();
   trigger_dependents();
   const int p0 = g.start[slot], rows = g.start[slot + 1] - p0, tile0 = g.first64[slot];
   const int r = rows ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
   float* out = a.g + (size_t)slot * g.max_rank * a.K;
   const int width = min(kGradCols, a.K - col0);
   if (r == 0) {
+    grid_dependency_wait();
     if (!g.accumulate)
       for (int i = split * kGradThreads + tid; i < g.max_rank * width; i += nsplit * kGradThreads)
         out[(size_t)(i / width) * a.K + col0 + i % width] = 0.f;
@@ -804,19 +858,41 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
   const int nt_all = (rows + 63) / 64, t_lo = (int)((long)nt_all * split / nsplit);
   const int nt = (int)((long)nt_all * (split + 1) / nsplit) - t_lo;
   const bool vec = (a.K & 7) == 0;
-  auto issue = [&](int i) {
+  // this thread's 16-byte column and rows of a stage; the row numbers of the next stage
+  // to be issued are loaded one stage ahead
+  const int piece = tid & 15, row0 = tid >> 4, col = col0 + 8 * piece;
+  const uint32_t spot = swz<S::kInPitch>(row0, piece);
+  int next[4];
+  auto fetch = [&](int i) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int p = (t_lo + i) * 64 + row0 + 16 * q;
+      next[q] = i < nt && p < rows ? g.perm[p0 + p] : -1;
+    }
+  };
+  auto issue_in = [&](int i) {
+    if (i < nt) {
+      const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t dst = st + spot + 16 * q * S::kInPitch;
+        const bool in = next[q] >= 0 && col < a.K;
+        const __half* line = a.in + (size_t)max(next[q], 0) * a.K;
+        if (vec) cp_async16(dst, line + (in ? col : 0), in ? 16 : 0);
+        else sts16(dst, in ? read_piece(line, col, a.K, false, a.in + (size_t)g.n_rows * a.K) : make_uint4(0, 0, 0, 0));
+      }
+      fetch(i + 1);
+    }
+  };
+  auto issue_t = [&](int i) {
     if (i < nt) {
       const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
       const int p = p0 + (t_lo + i) * 64, left = rows - (t_lo + i) * 64;
-      for (int q = tid; q < 64 * (S::kInPitch / 16); q += kGradThreads) {
-        const int row = q / (S::kInPitch / 16), c = q % (S::kInPitch / 16);
-        const uint32_t dst = st + swz<S::kInPitch>(row, c);
-        if (row < left) load_piece(dst, a.in + (size_t)g.perm[p + row] * a.K, col0 + 8 * c, a.K, vec);
-        else sts16(dst, make_uint4(0, 0, 0, 0));
-      }
-      const int pieces = r16 / 8;
+      constexpr int pieces = R / 8;
+#pragma unroll
       for (int q = tid; q < 64 * pieces; q += kGradThreads) {
         const int row = q / pieces, c = q % pieces;
+        if (8 * c >= r16) continue;
         const size_t at = (size_t)(p + min(row, left - 1)) * g.rp + 8 * c;
         const uint32_t dst = st + S::kInBytes + swz<S::kTPitch>(row, c);
         cp_async16(dst, a.hi + at, row < left ? 16 : 0);
@@ -825,7 +901,10 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
     }
     cp_async_commit();
   };
-  for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+  fetch(0);
+  for (int i = 0; i < S::kStages - 1; ++i) issue_in(i);
+  grid_dependency_wait();  // T is the call's own; the rest was there before the call
+  for (int i = 0; i < S::kStages - 1; ++i) issue_t(i);
   float sum[R / 16][2][4];
 #pragma unroll
   for (int t = 0; t < R / 16; ++t)
@@ -834,7 +913,8 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
   for (int i = 0; i < nt; ++i) {
     cp_async_wait<S::kStages - 2>();
     __syncthreads();
-    issue(i + S::kStages - 1);
+    issue_in(i + S::kStages - 1);
+    issue_t(i + S::kStages - 1);
     const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
     const float unit = a.unit[tile0 + t_lo + i];
     uint32_t bf[4][4];
@@ -931,14 +1011,6 @@ cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, size_t smem, cudaS
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
-template <int R>
-cudaError_t launch_rows(const RowsArgs& args, bool wide, int passes, int tiles, cudaStream_t stream) {
-  void* a[] = {(void*)&args};
-  const void* fn = wide ? (const void*)k_adapter_rows<R> : (const void*)k_adapter_few<R>;
-  return launch_pdl(fn, dim3((unsigned)tiles * kCluster, passes), dim3(kRowThreads), wide ? RowsShape<R>::smem : 0,
-                    stream, a, dim3(kCluster, 1, 1));
-}
-
 RowsArgs rows_args(const dictproj_adapters* a, const dictproj_rows* r, bool wide) {
   RowsArgs g = {};
   g.n_tiles = r->n_tiles + (wide ? 2 : 0);
@@ -948,6 +1020,8 @@ RowsArgs rows_args(const dictproj_adapters* a, const dictproj_rows* r, bool wide
   g.scale = a->scale;
   g.rp = a->rp;
   g.n_slots = a->n_slots;
+  g.rows = r->M;
+  g.cluster = kCluster;
   return g;
 }
 RowsPass rows_pass(const dictproj_adapters* a, bool forward, const __half* in, const __half* base, __half* out) {
@@ -965,12 +1039,44 @@ RowsPass rows_pass(const dictproj_adapters* a, bool forward, const __half* in, c
   p.ld_q = forward ? a->ld_b : a->d_in;
   return p;
 }
-cudaError_t launch_rows_any(const RowsArgs& g, bool wide, int passes, const dictproj_rows* r, cudaStream_t stream) {
-  const int tiles = adapter_tiles(r->M, r->n_slots, wide ? kWideRows : kFewRows);
-  if (g.rp <= 16) return launch_rows<16>(g, wide, passes, tiles, stream);
-  if (g.rp <= 32) return launch_rows<32>(g, wide, passes, tiles, stream);
-  if (g.rp <= 64) return launch_rows<64>(g, wide, passes, tiles, stream);
-  return launch_rows<128>(g, wide, passes, tiles, stream);
+// The kernel of the smallest template rank that holds rp ranks.
+#define DICTPROJ_BY_RANK(rp, call) \
+  ((rp) <= 16 ? call(16) : (rp) <= 32 ? call(32) : (rp) <= 64 ? call(64) : call(128))
+
+cudaError_t launch_few(const RowsArgs& g, const dictproj_rows* r, cudaStream_t stream) {
+  void* args[] = {(void*)&g};
+  const bool vec = ((g.pass[0].K | g.pass[0].N) & 7) == 0;
+#define FEW(R) (vec ? (const void*)k_adapter_few<R, true> : (const void*)k_adapter_few<R, false>)
+  return launch_pdl(DICTPROJ_BY_RANK(g.rp, FEW), dim3((unsigned)(adapter_tiles(r->M, r->n_slots, kFewRows) * kCluster)),
+                    dim3(kRowThreads), 0, stream, args, dim3(kCluster, 1, 1));
+#undef FEW
+}
+cudaError_t launch_contract(RowsArgs& g, int passes, const dictproj_rows* r, int n_sm, cudaStream_t stream) {
+  const int tiles = adapter_tiles(r->M, r->n_slots, kWideRows);
+  const int full = r->M / kWideRows * passes;  // tiles that do exist, about
+  g.cluster = 2;
+  while (g.cluster < 8 && full * g.cluster < 2 * n_sm) g.cluster *= 2;
+  void* args[] = {(void*)&g};
+#define FN(R) (const void*)k_adapter_contract<R>
+#define SMEM(R) ContractShape<R>::smem
+  return launch_pdl(DICTPROJ_BY_RANK(g.rp, FN), dim3((unsigned)(tiles * g.cluster), passes), dim3(kRowThreads),
+                    DICTPROJ_BY_RANK(g.rp, SMEM), stream, args, dim3(g.cluster, 1, 1));
+#undef FN
+#undef SMEM
+}
+cudaError_t launch_expand(const RowsArgs& g, const dictproj_rows* r, int n_sm, cudaStream_t stream) {
+  const int tiles = adapter_tiles(r->M, r->n_slots, kWideRows), blocks = (g.pass[0].N + 127) / 128;
+  const int full = std::max(1, r->M / kWideRows);  // tiles that do exist, about
+  // as many CTAs as run at once (two an SM above rank 32): 2048 rows of rank 32 took 22.3 us
+  // with three an SM, 24.1 with two, 26 with more than four
+  const int parts = std::min(blocks, std::max(1, (g.rp <= 32 ? 3 : 2) * n_sm / full));
+  void* args[] = {(void*)&g};
+#define FN(R) (const void*)k_adapter_expand<R>
+#define SMEM(R) ExpandShape<R>::smem
+  return launch_pdl(DICTPROJ_BY_RANK(g.rp, FN), dim3(parts, tiles), dim3(kRowThreads),
+                    DICTPROJ_BY_RANK(g.rp, SMEM), stream, args);
+#undef FN
+#undef SMEM
 }
 
 template <int R>
@@ -983,7 +1089,8 @@ cudaError_t launch_grad(const GradArgs& args, dim3 grid, cudaStream_t stream) {
 template <int R>
 cudaError_t allow_rank() {
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(k_adapter_rows<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsShape<R>::smem)))
+  if ((e = cudaFuncSetAttribute(k_adapter_contract<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, ContractShape<R>::smem)) ||
+      (e = cudaFuncSetAttribute(k_adapter_expand<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, ExpandShape<R>::smem)))
     return e;
   return cudaFuncSetAttribute(k_adapter_grad<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, GradShape<R>::smem);
 }
@@ -1017,12 +1124,23 @@ cudaError_t launch_rows_plan(const dictproj_rows* r, const int* ids, int M, cuda
                     ((size_t)kPlanWarps * (ns + 1) + 3 * (ns + 2)) * sizeof(int), stream, args);
 }
 
+static void set_parts(const dictproj_adapters* a, RowsArgs& g) {
+  for (int i = 0; i < 2; ++i) {
+    g.pass[i].hi = reinterpret_cast<__half*>(a->part[i][0]);
+    g.pass[i].lo = reinterpret_cast<__half*>(a->part[i][1]);
+    g.pass[i].unit = a->unit[i];
+  }
+}
+
 cudaError_t launch_adapter_forward(const dictproj_adapters* a, const dictproj_rows* r, const __half* X,
                                    const __half* base, __half* Y, cudaStream_t stream) {
   const bool wide = r->M >= 256 && r->M >= 32 * a->n_slots;
   RowsArgs g = rows_args(a, r, wide);
   g.pass[0] = rows_pass(a, true, X, base, Y);
-  return launch_rows_any(g, wide, 1, r, stream);
+  if (!wide) return launch_few(g, r, stream);
+  set_parts(a, g);
+  const cudaError_t e = launch_contract(g, 1, r, a->n_sm, stream);
+  return e == cudaSuccess ? launch_expand(g, r, a->n_sm, stream) : e;
 }
 
 cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_rows* r, const __half* X,
@@ -1031,13 +1149,9 @@ cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_r
   RowsArgs g = rows_args(a, r, true);
   g.pass[0] = rows_pass(a, false, dY, base, dX);
   g.pass[1] = rows_pass(a, true, X, nullptr, nullptr);
-  if (dA)
-    for (int i = 0; i < 2; ++i) {
-      g.pass[i].hi = reinterpret_cast<__half*>(a->part[i][0]);
-      g.pass[i].lo = reinterpret_cast<__half*>(a->part[i][1]);
-      g.pass[i].unit = a->unit[i];
-    }
-  cudaError_t e = launch_rows_any(g, true, dA ? 2 : 1, r, stream);
+  set_parts(a, g);
+  cudaError_t e = launch_contract(g, dA ? 2 : 1, r, a->n_sm, stream);
+  if (e == cudaSuccess && dX) e = launch_expand(g, r, a->n_sm, stream);
   if (e != cudaSuccess || !dA) return e;
   GradArgs w = {};
   for (int i = 0; i < 2; ++i) {
@@ -1056,6 +1170,7 @@ cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_r
   w.rp = a->rp;
   w.max_rank = a->max_rank;
   w.accumulate = accumulate;
+  w.n_rows = r->M;
   const int blocks = w.pass[0].blocks + w.pass[1].blocks;
   int split = 1;
   while (split < 8 && blocks * a->n_slots * split < 3 * a->n_sm && 64 * a->n_slots * split < r->M) split *= 2;
