@@ -18,6 +18,7 @@
 
 #include <algorithm>
 
+#include "adapter.cuh"
 #include "common.cuh"
 #include "dictproj_internal.h"
 #include "kernels.h"
@@ -30,14 +31,15 @@ namespace {
 // histogram (equal lanes found by match), a scan over (slot, warp) turns the counts
 // into positions, and the second pass over the ids scatters in row order, so the
 // result does not depend on timing. Bucket n_slots takes the rows without a slot.
-// Then the slots' rows are cut into tiles of kFewRows and of kWideRows.
+// Then the slots' rows are cut into tiles of kFewRows, kWideRows and kTallRows.
 constexpr int kPlanWarps = 32;
-constexpr int kFewRows = 4, kWideRows = 64;
 
 __device__ __forceinline__ int plan_bucket(const int* ids, int m, int n_slots) {
   const int id = ids[m];
   return id >= 0 && id < n_slots ? id : n_slots;
 }
+
+__device__ __forceinline__ int plan_rows(int q) { return q == 0 ? kFewRows : q == 1 ? kWideRows : kTallRows; }
 
 // Exclusive sum over the CTA's threads; *total gets the whole sum.
 __device__ __forceinline__ int block_exclusive_sum(int x, int* wsum, int* total) {
@@ -64,13 +66,13 @@ __device__ __forceinline__ int block_exclusive_sum(int x, int* wsum, int* total)
 __global__ void __launch_bounds__(kPlanWarps * 32)
     k_rows_plan(const int* __restrict__ ids, int M, int n_slots, int* __restrict__ perm, int* __restrict__ start,
                 int* __restrict__ n_tiles, int4* __restrict__ tiles4, int4* __restrict__ tiles64,
-                int* __restrict__ first64) {
+                int4* __restrict__ tiles128, int* __restrict__ first64) {
   extern __shared__ int plan_smem[];
   __shared__ int wsum[kPlanWarps];
   const int nb = n_slots + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* hist = plan_smem;                    // [kPlanWarps][nb]
   int* begin = hist + kPlanWarps * nb;      // [nb + 1] first position of each bucket
-  int* tfirst = begin + nb + 1;             // [2][nb + 1] first tile of each bucket
+  int* tfirst = begin + nb + 1;             // [3][nb + 1] first tile of each bucket
   grid_dependency_wait();
   for (int i = threadIdx.x; i < kPlanWarps * nb; i += blockDim.x) hist[i] = 0;
   __syncthreads();
@@ -112,20 +114,20 @@ __global__ void __launch_bounds__(kPlanWarps * 32)
       at += c;
     }
   }
-  int last[2];
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int T = q ? kWideRows : kFewRows;
-    const int f = block_exclusive_sum((count + T - 1) / T, wsum, &last[q]);
+#pragma unroll 1
+  for (int q = 0; q < 3; ++q) {
+    const int T = plan_rows(q);
+    int last;
+    const int f = block_exclusive_sum((count + T - 1) / T, wsum, &last);
     if (s < n_slots) {
       tfirst[q * (nb + 1) + s] = f;
-      if (q) first64[s] = f;
+      if (q == 1) first64[s] = f;
     }
     if (threadIdx.x == 0) {
-      const int all = last[q] + (M - live + T - 1) / T;
-      tfirst[q * (nb + 1) + n_slots] = last[q];
+      const int all = last + (M - live + T - 1) / T;
+      tfirst[q * (nb + 1) + n_slots] = last;
       tfirst[q * (nb + 1) + nb] = all;
-      n_tiles[2 * q] = last[q];
+      n_tiles[2 * q] = last;
       n_tiles[2 * q + 1] = all;
     }
   }
@@ -141,10 +143,11 @@ __global__ void __launch_bounds__(kPlanWarps * 32)
     __syncwarp();
   }
   __syncthreads();  // the tiles name row numbers of perm
-  for (int q = 0; q < 2; ++q) {
-    const int T = q ? kWideRows : kFewRows;
+#pragma unroll 1
+  for (int q = 0; q < 3; ++q) {
+    const int T = plan_rows(q);
     const int* tf = tfirst + q * (nb + 1);
-    int4* tiles = q ? tiles64 : tiles4;
+    int4* tiles = q == 0 ? tiles4 : q == 1 ? tiles64 : tiles128;
     for (int t = threadIdx.x; t < tf[nb]; t += blockDim.x) {
       int a = 0, z = n_slots;  // the last bucket whose first tile is <= t (an empty bucket owns none)
       while (a < z) {
@@ -153,7 +156,8 @@ __global__ void __launch_bounds__(kPlanWarps * 32)
         else z = mid - 1;
       }
       const int p = begin[a] + (t - tf[a]) * T;
-      tiles[t] = make_int4(a, p, min(T, begin[a + 1] - p), perm[p]);
+      const int w = q == 2 ? tfirst[nb + 1 + a] + 2 * (t - tf[a]) : perm[p];
+      tiles[t] = make_int4(a, p, min(T, begin[a + 1] - p), w);
     }
   }
 }
@@ -176,27 +180,6 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// ---- helpers ------------------------------------------------------------------------
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ uint32_t peer_smem(uint32_t local, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float4 ld_peer_v4f(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float ld_peer_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void st_peer_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
 // 16 bytes global -> shared, the last 16 - bytes of them zeros
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -215,11 +198,6 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-__device__ __forceinline__ uint32_t half2_bits(__half a, __half b) {
-  const __half2 h = __halves2half2(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // Byte offset of 16-byte piece p of row `row` in a tile of PITCH-byte rows whose
 // pieces are permuted so that 8 rows' pieces of one column lie in different banks.
 template <int PITCH>
@@ -277,50 +255,9 @@ __device__ __forceinline__ void write_piece(__half* row, int c, int n, bool vec,
     if (c + e < n) row[c + e] = __ushort_as_half((unsigned short)(w[e >> 1] >> (16 * (e & 1))));
 }
 
-// T in two fp16 parts: t * unit = high + low with |t * unit| < 2^14, so that the two
-// together keep 22 bits of it, or 2^-24 absolute (2^-38 of the tile's largest): the
-// MMA's fp16 operands then carry T as exactly as the fp32 sums that made it, whatever
-// its size. unit is a power of two.
-struct Split {
-  __half hi, lo;
-};
-__device__ __forceinline__ Split split_half(float t) {
-  Split s;
-  s.hi = __float2half_rn(t);
-  s.lo = __hisinf(s.hi) ? __float2half_rn(0.f) : __float2half_rn(t - __half2float(s.hi));
-  return s;
-}
-// 2^13 / 2^floor(log2 m), within fp32's normal range; 1 for m = 0.
-__device__ __forceinline__ float split_unit(float m) {
-  if (m == 0.f) return 1.f;
-  const int e = (int)((__float_as_uint(m) >> 23) & 255) - 127;  // -127 for a subnormal
-  return __uint_as_float((uint32_t)(min(13 - e, 126) + 127) << 23);
-}
-
 // ---- contraction and expansion -------------------------------------------------------------
 constexpr int kCluster = 8;
 constexpr int kRowThreads = 256;
-
-struct RowsPass {
-  const __half* in;
-  const __half* P;
-  const __half* Q;
-  const __half* base;
-  __half* out;
-  __half* hi;  // the two parts of scale * T (many rows)
-  __half* lo;
-  float* unit;
-  int K, N, ld_p, ld_q;
-};
-struct RowsArgs {
-  RowsPass pass[2];
-  const int* n_tiles;
-  const int4* tiles;
-  const int* perm;
-  const int* rank;
-  const float* scale;
-  int rp, n_slots, rows, cluster;
-};
 
 // ---- few rows of a slot: serving ----------------------------------------------------------
 // A cluster of kCluster CTAs takes one tile of up to four rows of one slot and walks the
@@ -650,7 +587,7 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_c
     for (int e = 0; e < 4; ++e)
       if (fabsf(v[e]) <= 3.0e38f) m = fmaxf(m, fabsf(v[e]));  // an infinity or NaN does not decide the others' digits
   }
-  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+  m = warp_max_bits(m);
   if (lane == 0) smax[warp] = m;
   __syncthreads();
   if (tid < cluster) {
@@ -666,10 +603,10 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_c
   if (rankc == 0 && tid == 0) a.unit[tile_no] = 1.f / unit;
   for (int i = 4 * tid; i < share * R; i += 4 * kRowThreads) {
     const int j = i % R, row = row_lo + i / R;
-    if (j >= r16 || row >= count) continue;
-    const float4 x = *reinterpret_cast<const float4*>(own + i);
+    if (j >= r16) continue;
+    const float4 x = row < count ? *reinterpret_cast<const float4*>(own + i) : make_float4(0.f, 0.f, 0.f, 0.f);
     const Split s0 = split_half(x.x * unit), s1 = split_half(x.y * unit), s2 = split_half(x.z * unit), s3 = split_half(x.w * unit);
-    const size_t at = (size_t)(tile.y + row) * g.rp + j;
+    const size_t at = (size_t)(tile_no * TM + row) * g.rp + j;
     *reinterpret_cast<uint2*>(a.hi + at) = make_uint2(half2_bits(s0.hi, s1.hi), half2_bits(s2.hi, s3.hi));
     *reinterpret_cast<uint2*>(a.lo + at) = make_uint2(half2_bits(s0.lo, s1.lo), half2_bits(s2.lo, s3.lo));
   }
@@ -748,9 +685,8 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_expand(const __grid_con
   for (int t = 0; t < R / 16; ++t)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int tr = g0 + 8 * (q & 1);
-      const size_t at = (size_t)(tile.y + tr) * g.rp + 16 * t + c0 + 8 * (q >> 1);
-      const bool in = tr < count && 16 * t < r16;
+      const size_t at = (size_t)(tile_no * TM + g0 + 8 * (q & 1)) * g.rp + 16 * t + c0 + 8 * (q >> 1);
+      const bool in = 16 * t < r16;
       thi[t][q] = in ? *reinterpret_cast<const uint32_t*>(a.hi + at) : 0u;
       tlo[t][q] = in ? *reinterpret_cast<const uint32_t*>(a.lo + at) : 0u;
     }
@@ -805,25 +741,7 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_expand(const __grid_con
 // order. Per tile the products of T's two parts are accumulated by the MMA and then
 // added, times the tile's unit, to fp32 sums: a long sum is rounded to nearest once a
 // tile, not truncated at each MMA.
-constexpr int kGradCols = 128;
 constexpr int kGradThreads = 256;
-
-struct GradPass {
-  const __half* in;
-  const __half* hi;
-  const __half* lo;
-  const float* unit;
-  float* g;
-  int K, blocks;
-};
-struct GradArgs {
-  GradPass pass[2];
-  const int* start;
-  const int* first64;
-  const int* perm;
-  const int* rank;
-  int rp, max_rank, accumulate, n_rows;
-};
 
 template <int R>
 struct GradShape {
@@ -887,16 +805,15 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
   auto issue_t = [&](int i) {
     if (i < nt) {
       const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
-      const int p = p0 + (t_lo + i) * 64, left = rows - (t_lo + i) * 64;
       constexpr int pieces = R / 8;
 #pragma unroll
       for (int q = tid; q < 64 * pieces; q += kGradThreads) {
         const int row = q / pieces, c = q % pieces;
         if (8 * c >= r16) continue;
-        const size_t at = (size_t)(p + min(row, left - 1)) * g.rp + 8 * c;
+        const size_t at = (size_t)((tile0 + t_lo + i) * kWideRows + row) * g.rp + 8 * c;
         const uint32_t dst = st + S::kInBytes + swz<S::kTPitch>(row, c);
-        cp_async16(dst, a.hi + at, row < left ? 16 : 0);
-        cp_async16(dst + S::kTBytes, a.lo + at, row < left ? 16 : 0);
+        cp_async16(dst, a.hi + at, 16);
+        cp_async16(dst + S::kTBytes, a.lo + at, 16);
       }
     }
     cp_async_commit();
@@ -1051,7 +968,9 @@ cudaError_t launch_few(const RowsArgs& g, const dictproj_rows* r, cudaStream_t s
                     dim3(kRowThreads), 0, stream, args, dim3(kCluster, 1, 1));
 #undef FEW
 }
-cudaError_t launch_contract(RowsArgs& g, int passes, const dictproj_rows* r, int n_sm, cudaStream_t stream) {
+cudaError_t launch_contract(RowsArgs& g, int passes, const dictproj_adapters* pool, const dictproj_rows* r, cudaStream_t stream) {
+  const int n_sm = pool->n_sm;
+  if (tall_serves(pool, r)) return launch_contract_tall(g, passes, pool, r, stream);
   const int tiles = adapter_tiles(r->M, r->n_slots, kWideRows);
   const int full = r->M / kWideRows * passes;  // tiles that do exist, about
   g.cluster = 2;
@@ -1102,7 +1021,7 @@ cudaError_t prepare_adapter_kernels(int device) {
   cudaError_t e;
   if ((e = allow_rank<16>()) || (e = allow_rank<32>()) || (e = allow_rank<64>()) || (e = allow_rank<128>())) return e;
   return cudaFuncSetAttribute(k_rows_plan, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (kPlanWarps + 3) * (DICTPROJ_MAX_SLOTS + 2) * (int)sizeof(int));
+                              (kPlanWarps + 4) * (DICTPROJ_MAX_SLOTS + 2) * (int)sizeof(int));
 }
 
 cudaError_t launch_adapter_set(const dictproj_adapters* a, int slot, int rank, float scale, const __half* A,
@@ -1119,9 +1038,9 @@ cudaError_t launch_adapter_set(const dictproj_adapters* a, int slot, int rank, f
 cudaError_t launch_rows_plan(const dictproj_rows* r, const int* ids, int M, cudaStream_t stream) {
   int ns = r->n_slots;
   void* args[] = {&ids, &M, &ns, (void*)&r->perm, (void*)&r->start, (void*)&r->n_tiles, (void*)&r->tiles[0],
-                  (void*)&r->tiles[1], (void*)&r->first64};
+                  (void*)&r->tiles[1], (void*)&r->tiles[2], (void*)&r->first64};
   return launch_pdl((const void*)k_rows_plan, dim3(1), dim3(kPlanWarps * 32),
-                    ((size_t)kPlanWarps * (ns + 1) + 3 * (ns + 2)) * sizeof(int), stream, args);
+                    ((size_t)kPlanWarps * (ns + 1) + 4 * (ns + 2)) * sizeof(int), stream, args);
 }
 
 static void set_parts(const dictproj_adapters* a, RowsArgs& g) {
@@ -1139,7 +1058,7 @@ cudaError_t launch_adapter_forward(const dictproj_adapters* a, const dictproj_ro
   g.pass[0] = rows_pass(a, true, X, base, Y);
   if (!wide) return launch_few(g, r, stream);
   set_parts(a, g);
-  const cudaError_t e = launch_contract(g, 1, r, a->n_sm, stream);
+  const cudaError_t e = launch_contract(g, 1, a, r, stream);
   return e == cudaSuccess ? launch_expand(g, r, a->n_sm, stream) : e;
 }
 
@@ -1150,7 +1069,7 @@ cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_r
   g.pass[0] = rows_pass(a, false, dY, base, dX);
   g.pass[1] = rows_pass(a, true, X, nullptr, nullptr);
   set_parts(a, g);
-  cudaError_t e = launch_contract(g, dA ? 2 : 1, r, a->n_sm, stream);
+  cudaError_t e = launch_contract(g, dA ? 2 : 1, a, r, stream);
   if (e == cudaSuccess && dX) e = launch_expand(g, r, a->n_sm, stream);
   if (e != cudaSuccess || !dA) return e;
   GradArgs w = {};
@@ -1171,6 +1090,7 @@ cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_r
   w.max_rank = a->max_rank;
   w.accumulate = accumulate;
   w.n_rows = r->M;
+  if (tall_serves(a, r)) return launch_grad_tall(w, a, r, stream);
   const int blocks = w.pass[0].blocks + w.pass[1].blocks;
   int split = 1;
   while (split < 8 && blocks * a->n_slots * split < 3 * a->n_sm && 64 * a->n_slots * split < r->M) split *= 2;

@@ -1,0 +1,587 @@
+// Adapters of many rows on the 5th-generation tensor cores: the contraction T = X A^T
+// and the weight gradients T^T X, for row lengths that TMA can read (multiples of 8).
+//
+// Both stream the activations once for few operations, so the aim is to move them with
+// as few instructions as can be: the rows of a tile arrive by TMA (128-byte swizzle) and
+// are multiplied by one thread's tcgen05.mma; the mma.sync kernels of adapter.cu, which
+// serve the other row lengths, spend 28 M warp instructions where these need 9 M (8192
+// rows of 4096, rank 64, both contractions). Rows that follow one another in the batch
+// (a sequence's) come as one box, others by gathers of four rows, which move about 6 bytes
+// a clock and SM: both contractions of 2048 rows (4096 + 11008 wide) took 38 us by gathers
+// alone. A slot's rows ascend in the plan, so they follow one another when the last is as
+// far from the first as there are rows between.
+//
+// Every spin-wait is bounded; a wait that gives up sets the file's device error word and
+// the kernel unwinds (frees its tensor memory) without hanging.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "adapter.cuh"
+#include "common.cuh"
+#include "dictproj_internal.h"
+#include "kernels.h"
+#include "tcgen05.cuh"
+
+namespace dictproj {
+namespace {
+
+constexpr int kTallThreads = 192;  // warp 0 TMA, warp 1 MMA + tensor memory, warps 2..5 epilogue
+constexpr int kCols = 64;          // columns of a stage (one 128-byte swizzle row)
+
+// First 1024-byte boundary (swizzled operand tiles start on one).
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) { return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u); }
+
+// A producer that gives up first waits (bounded) for the copies it has in flight, those of
+// the last stages before stage s.
+__device__ __forceinline__ void drain(uint64_t* full, int stages, int s) {
+  for (int q = max(0, s - stages); q < s; ++q) mbar_wait_bounded(&full[q % stages], (q / stages) & 1);
+}
+
+// ---- contraction -------------------------------------------------------------------------
+// A cluster splits the K columns of one tile of up to 128 rows of one slot. Per 64-column
+// stage 128 gathered rows of In (16 KB) and r rows of P_s; D = In P^T, rows x r, in tensor
+// memory. The CTAs' partial sums meet through distributed shared memory, in rank order;
+// each CTA writes its share of the rows as two fp16 parts, with a unit for each 64 rows.
+struct TallContractArgs {
+  CUtensorMap in[2], box[2], p[2];  // In by single rows and by 64, P by 16
+  RowsArgs g;
+};
+
+template <int R>
+struct TallContract {
+  static constexpr int kStages = R == 16 ? 5 : R <= 64 ? 4 : 3;
+  static constexpr int kInBytes = kTallRows * 128, kStageBytes = kInBytes + R * 128;
+  static constexpr int kPitch = R + 4;  // floats of a row of the partial sums
+  static constexpr int kRing = kStages * kStageBytes;
+  static_assert(kTallRows * kPitch * 4 <= kRing, "the partial sums lie over the drained ring");
+  static constexpr int smem = kRing + 1024 + 256;
+  static constexpr int kTmem = R < 32 ? 32 : R;
+};
+
+template <int R>
+__global__ void __launch_bounds__(kTallThreads) k_contract_tall(const __grid_constant__ TallContractArgs args) {
+  using S = TallContract<R>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kRing);
+  uint64_t* empty = full + S::kStages;
+  uint64_t* accf = empty + S::kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
+  __shared__ float smax[2][kTallThreads / 32], cmax[2][8];
+  const RowsArgs& g = args.g;
+  const RowsPass& a = g.pass[blockIdx.y];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cluster = g.cluster, rankc = blockIdx.x % cluster, tile_no = blockIdx.x / cluster;
+
+  grid_dependency_wait();
+  const int4 tile = g.tiles[tile_no];
+  if (tile_no >= g.n_tiles[0]) return;  // the whole cluster
+  const int count = tile.z, slot = tile.x, r = g.rank[slot], r16 = (r + 15) & ~15;
+  if (r == 0) return;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(accf, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, S::kTmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  trigger_dependents();  // not before the tensor memory is ours: a dependent may want all of it
+  const uint32_t tmem = *tmem_slot;
+  const float scale = g.scale[slot];
+  const int kc = (a.K + kCols - 1) / kCols, k_lo = kc * rankc / cluster, nk = kc * (rankc + 1) / cluster - k_lo;
+
+  if (warp == 0) {
+    // lane l gathers rows 4 l .. 4 l + 3 of the tile; past its end any row will do
+    int row[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) row[q] = g.perm[tile.y + min(4 * lane + q, count - 1)];
+    const int row_a = __shfl_sync(0xffffffffu, row[0], 0), row_z = __shfl_sync(0xffffffffu, row[3], 31);
+    const bool run = row_z - row_a == count - 1;
+    const int boxes = run ? (count + kWideRows - 1) / kWideRows : 0;
+    const uint32_t bytes = (run ? boxes * kWideRows * 128 : S::kInBytes) + r16 * 128;
+    bool ok = true;
+    for (int s = 0; s < nk && ok; ++s) {
+      const int slot_s = s % S::kStages, round = s / S::kStages;
+      if (lane == 0) {
+        if (s >= S::kStages) ok = mbar_wait_bounded(&empty[slot_s], (round - 1) & 1);
+        if (ok) mbar_arrive_expect_tx(&full[slot_s], bytes);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) {
+        drain(full, S::kStages, s);
+        break;
+      }
+      const uint32_t st = smem_u32(smem + slot_s * S::kStageBytes);
+      const int x = (k_lo + s) * kCols;
+      if (!run) tma_gather4(st + 512 * lane, &args.in[blockIdx.y], x, row[0], row[1], row[2], row[3], &full[slot_s]);
+      else if (lane < boxes) tma_load_2d(st + 8192 * lane, &args.box[blockIdx.y], x, row_a + kWideRows * lane, &full[slot_s]);
+      if (lane < r16 / 16)
+        tma_load_2d(st + S::kInBytes + 2048 * lane, &args.p[blockIdx.y], x, slot * g.rp + 16 * lane, &full[slot_s]);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // kind::f16, A and B fp16, D fp32, K-major, M = 128 rows, N = r16
+      const uint32_t idesc = (1u << 4) | ((uint32_t)(r16 >> 3) << 17) | ((uint32_t)(kTallRows >> 4) << 24);
+      for (int s = 0; s < nk; ++s) {
+        const int slot_s = s % S::kStages, round = s / S::kStages;
+        if (!mbar_wait_bounded(&full[slot_s], round & 1)) break;
+        tc_fence_after();
+        const uint32_t st = smem_u32(smem + slot_s * S::kStageBytes);
+#pragma unroll
+        for (int j = 0; j < kCols / 16; ++j)
+          mma_f16_ss(tmem, smem_desc_sw128(st + 32 * j), smem_desc_sw128(st + S::kInBytes + 32 * j), idesc, (s | j) != 0);
+        mma_commit(&empty[slot_s]);
+      }
+      mma_commit(accf);
+    }
+  }
+  __syncwarp();
+  float* part = reinterpret_cast<float*>(smem);  // [128][kPitch], over the drained ring
+  if (warp >= 2) {
+    const int q = warp & 3, row = 32 * q + lane;
+    const bool ok = mbar_wait_bounded(accf, 0);
+    tc_fence_after();
+#pragma unroll
+    for (int t = 0; t < R / 16; ++t) {
+      if (16 * t >= r16) break;
+      uint32_t v[16];
+      tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + 16 * t, v);
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<float4*>(part + row * S::kPitch + 16 * t + e) =
+            ok && nk > 0 ? make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]))
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  tc_fence_before();
+  cluster_arrive();
+  cluster_wait();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kTmem);
+  }
+  // the cluster's sum of this CTA's share of the rows, CTAs in order: scale * T, zero past
+  // the slot's rank and the tile's rows
+  const uint32_t pbase = smem_u32(part);
+  const int share = kTallRows / cluster, row_lo = rankc * share, quads = r16 / 4;
+  constexpr int kMine = (kTallRows / 2 * R / 4 + kTallThreads - 1) / kTallThreads;  // quads of a thread, cluster >= 2
+  float4 mine[kMine];
+  float m[2] = {0.f, 0.f};
+#pragma unroll
+  for (int q = 0; q < kMine; ++q) {
+    const int i = threadIdx.x + q * kTallThreads, row = row_lo + i / quads, j = 4 * (i % quads);
+    mine[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i >= share * quads || row >= count) continue;
+    const uint32_t at = pbase + 4 * (row * S::kPitch + j);
+    float4 x = ld_peer_v4f(peer_smem(at, 0));
+    for (int c = 1; c < cluster; ++c) {
+      const float4 y = ld_peer_v4f(peer_smem(at, c));
+      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    const float v[4] = {j < r ? x.x * scale : 0.f, j + 1 < r ? x.y * scale : 0.f, j + 2 < r ? x.z * scale : 0.f,
+                        j + 3 < r ? x.w * scale : 0.f};
+    mine[q] = make_float4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (fabsf(v[e]) <= 3.0e38f) {  // an infinity or NaN does not decide the others' digits
+        if (row < kWideRows) m[0] = fmaxf(m[0], fabsf(v[e]));
+        else m[1] = fmaxf(m[1], fabsf(v[e]));
+      }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    m[h] = warp_max_bits(m[h]);
+    if (lane == 0) smax[h][warp] = m[h];
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < cluster) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float x = smax[h][0];
+#pragma unroll
+      for (int w = 1; w < kTallThreads / 32; ++w) x = fmaxf(x, smax[h][w]);
+      st_peer_f32(peer_smem(smem_u32(&cmax[h][rankc]), threadIdx.x), x);
+    }
+  }
+  cluster_arrive();
+  cluster_wait();
+  float unit[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float x = 0.f;
+    for (int c = 0; c < cluster; ++c) x = fmaxf(x, cmax[h][c]);
+    unit[h] = split_unit(x);
+  }
+  const bool two = count > kWideRows;
+  if (rankc == 0 && (int)threadIdx.x < (two ? 2 : 1)) a.unit[tile.w + threadIdx.x] = 1.f / unit[threadIdx.x];
+#pragma unroll
+  for (int q = 0; q < kMine; ++q) {
+    const int i = threadIdx.x + q * kTallThreads, row = row_lo + i / quads, j = 4 * (i % quads);
+    if (i >= share * quads || (row >= kWideRows && !two)) continue;
+    const float u = row < kWideRows ? unit[0] : unit[1];
+    const Split s0 = split_half(mine[q].x * u), s1 = split_half(mine[q].y * u), s2 = split_half(mine[q].z * u), s3 = split_half(mine[q].w * u);
+    const size_t at = ((size_t)tile.w * kWideRows + row) * g.rp + j;
+    *reinterpret_cast<uint2*>(a.hi + at) = make_uint2(half2_bits(s0.hi, s1.hi), half2_bits(s2.hi, s3.hi));
+    *reinterpret_cast<uint2*>(a.lo + at) = make_uint2(half2_bits(s0.lo, s1.lo), half2_bits(s2.lo, s3.lo));
+  }
+}
+
+// ---- weight gradients ------------------------------------------------------------------------
+// G_s[j][i] (+)= sum over the slot's 64-row tiles of unit * (T parts)^T In, as G^T: 128
+// columns of In are the MMA's rows (A, gathered, MN-major), the ranks its columns (B, T's
+// parts, MN-major), 64 rows its reduction. Each tile gets an accumulator of its own in
+// tensor memory (two in turn), which the epilogue warps add, times the tile's unit, to
+// fp32 sums in registers (thread = column): a long sum is rounded to nearest once a tile.
+// A cluster splits the tiles and sums through distributed shared memory in rank order.
+struct TallGradArgs {
+  CUtensorMap in[2], box[2], part[2][2];
+  GradArgs g;
+};
+
+template <int R>
+struct TallGrad {
+  static constexpr int kInBytes = 2 * kWideRows * 128;  // two chunks of 64 columns
+  static constexpr int kTChunks = R > 64 ? 2 : 1, kTBytes = kTChunks * kWideRows * 128;
+  static constexpr int kStageBytes = kInBytes + 2 * kTBytes;
+  static constexpr int kStages = 3;
+  static constexpr int kRing = kStages * kStageBytes;
+  static_assert(R * kGradCols * 4 <= kRing, "the partial sums lie over the drained ring");
+  static constexpr int smem = kRing + 1024 + 256;
+  static constexpr int kTmem = 2 * R;
+};
+
+template <int R>
+__global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constant__ TallGradArgs args) {
+  using S = TallGrad<R>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kRing);
+  uint64_t* empty = full + S::kStages;
+  uint64_t* dfull = empty + S::kStages;
+  uint64_t* dempty = dfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dempty + 2);
+  const GradArgs& g = args.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = blockIdx.z, nsplit = gridDim.z, slot = blockIdx.y;
+  const int which = (int)blockIdx.x < g.pass[0].blocks ? 0 : 1;
+  const GradPass& a = g.pass[which];
+  const int col0 = ((int)blockIdx.x - (which ? g.pass[0].blocks : 0)) * kGradCols;
+  // The launch before is the expansion or the contraction of the same call: what was there
+  // before the call (plan, ranks, In) is complete and may be read before the wait.
+  const int p0 = g.start[slot], rows = g.start[slot + 1] - p0, tile0 = g.first64[slot];
+  const int r = rows ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
+  float* out = a.g + (size_t)slot * g.max_rank * a.K;
+  const int width = min(kGradCols, a.K - col0);
+  if (r == 0) {
+    trigger_dependents();
+    grid_dependency_wait();
+    if (!g.accumulate)
+      for (int i = split * kTallThreads + threadIdx.x; i < g.max_rank * width; i += nsplit * kTallThreads)
+        out[(size_t)(i / width) * a.K + col0 + i % width] = 0.f;
+    return;
+  }
+  const int nt_all = (rows + kWideRows - 1) / kWideRows, t_lo = (int)((long)nt_all * split / nsplit);
+  const int nt = (int)((long)nt_all * (split + 1) / nsplit) - t_lo;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&dfull[s], 1);
+      mbar_init(&dempty[s], 4);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, S::kTmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  trigger_dependents();  // not before the tensor memory is ours
+  const uint32_t tmem = *tmem_slot;
+  const int tch = r16 > 64 ? 2 : 1;  // 64-rank chunks of T
+
+  if (warp == 0) {
+    const uint32_t bytes = S::kInBytes + 2 * tch * kWideRows * 128;
+    const int chunk = lane >> 4, r4 = 4 * (lane & 15);  // this lane's chunk and first row of a tile
+    const int x = col0 + 64 * chunk < a.K ? col0 + 64 * chunk : col0;  // past the end any columns will do
+    // In's part of stage s: a whole tile of rows in a run as two boxes. Rows past the slot's
+    // end must not be others' (0 * inf): the ragged tile gathers, repeating its last row (T
+    // is zero there). A tile's first and last row numbers are loaded one stage ahead.
+    int row_a = 0, row_z = 0;
+    auto ends = [&](int s) {
+      const int at = p0 + (t_lo + s) * kWideRows;
+      row_a = s < nt ? g.perm[at] : 0;
+      row_z = s < nt ? g.perm[min(at + kWideRows, p0 + rows) - 1] : 0;
+    };
+    ends(0);
+    auto gather = [&](int s) {
+      const uint32_t st = smem_u32(smem + s % S::kStages * S::kStageBytes);
+      if (row_z - row_a == kWideRows - 1) {
+        if (lane < 2) tma_load_2d(st + 8192 * lane, &args.box[which], col0 + 64 * lane < a.K ? col0 + 64 * lane : col0, row_a, &full[s % S::kStages]);
+      } else {
+        int row[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) row[q] = g.perm[p0 + min((t_lo + s) * kWideRows + r4 + q, rows - 1)];
+        tma_gather4(st + 8192 * chunk + 128 * r4, &args.in[which], x, row[0], row[1], row[2], row[3], &full[s % S::kStages]);
+      }
+      ends(s + 1);
+    };
+    auto parts = [&](int s) {  // T's part: lane = (part, chunk)
+      if (lane < 2 * tch) {
+        const int pt = lane / tch, c = lane % tch;
+        tma_load_2d(smem_u32(smem + s % S::kStages * S::kStageBytes) + S::kInBytes + pt * S::kTBytes + 8192 * c,
+                    &args.part[which][pt], 64 * c, (tile0 + t_lo + s) * kWideRows, &full[s % S::kStages]);
+      }
+    };
+    const int first = min(nt, S::kStages);
+    for (int s = 0; s < first; ++s) {
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
+      __syncwarp();
+      gather(s);
+    }
+    grid_dependency_wait();
+    for (int s = 0; s < first; ++s) parts(s);
+    for (int s = first; s < nt; ++s) {
+      bool ok = true;
+      if (lane == 0) {
+        ok = mbar_wait_bounded(&empty[s % S::kStages], (s / S::kStages - 1) & 1);
+        if (ok) mbar_arrive_expect_tx(&full[s % S::kStages], bytes);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) {
+        drain(full, S::kStages, s);
+        break;
+      }
+      gather(s);
+      parts(s);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // kind::f16, A and B fp16 and MN-major, D fp32, M = 128 columns, N = r16
+      const uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(r16 >> 3) << 17) | ((uint32_t)(kGradCols >> 4) << 24);
+      for (int s = 0; s < nt; ++s) {
+        const int st_no = s % S::kStages, d = s & 1;
+        if (s >= 2 && !mbar_wait_bounded(&dempty[d], (s / 2 - 1) & 1)) break;
+        if (!mbar_wait_bounded(&full[st_no], (s / S::kStages) & 1)) break;
+        tc_fence_after();
+        const uint32_t st = smem_u32(smem + st_no * S::kStageBytes), tp = st + S::kInBytes;
+#pragma unroll
+        for (int pt = 1; pt >= 0; --pt)  // the low part first
+#pragma unroll
+          for (int j = 0; j < kWideRows / 16; ++j)
+            mma_f16_ss(tmem + d * R, smem_desc_mn_sw128(st + 2048 * j), smem_desc_mn_sw128(tp + pt * S::kTBytes + 2048 * j), idesc,
+                       pt == 0 || j != 0);
+        mma_commit(&empty[st_no]);
+        mma_commit(&dfull[d]);
+      }
+    }
+  }
+  __syncwarp();
+  float* part = reinterpret_cast<float*>(smem);  // [R][128], over the drained ring
+  if (warp >= 2) {
+    grid_dependency_wait();  // the units are the contraction's
+    const int q = warp & 3;
+    float sum[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) sum[j] = 0.f;
+    for (int s = 0; s < nt; ++s) {
+      const float unit = a.unit[tile0 + t_lo + s];
+      if (!mbar_wait_bounded(&dfull[s & 1], (s / 2) & 1)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int t = 0; t < R / 16; ++t) {
+        if (16 * t >= r16) break;
+        uint32_t v[16];
+        tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + (s & 1) * R + 16 * t, v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum[16 * t + e] = fmaf(__uint_as_float(v[e]), unit, sum[16 * t + e]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dempty[s & 1]);
+    }
+    // every MMA of the last tile has completed (its accumulator was read), so that no
+    // operand of the ring is in use any more
+#pragma unroll
+    for (int j = 0; j < R; ++j) part[j * kGradCols + 32 * q + lane] = sum[j];
+  } else {
+    grid_dependency_wait();
+  }
+  tc_fence_before();
+  if (nsplit > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kTmem);
+  }
+  // this CTA's share of the gradient's rows; rows past the rank are zero
+  const uint32_t pbase = smem_u32(part);
+  for (int i = split * kTallThreads + threadIdx.x; i < g.max_rank * (kGradCols / 4); i += nsplit * kTallThreads) {
+    const int j = i / (kGradCols / 4), c = 4 * (i % (kGradCols / 4));
+    if (c >= width) continue;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (j < r)
+      for (int s = 0; s < nsplit; ++s) {
+        const float4 y = nsplit > 1 ? ld_peer_v4f(peer_smem(pbase + 4 * (j * kGradCols + c), s))
+                                    : *reinterpret_cast<const float4*>(part + j * kGradCols + c);
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      }
+    float* dst = out + (size_t)j * a.K + col0 + c;  // K % 8 == 0: 16-byte aligned, c + 4 <= width
+    if (g.accumulate) {
+      const float4 y = *reinterpret_cast<const float4*>(dst);
+      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    *reinterpret_cast<float4*>(dst) = x;
+  }
+  if (nsplit > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+
+// Self-test of this file's bounded-wait error path (its own device error word): one warp
+// waits on an mbarrier that expects two arrivals and receives one.
+__global__ void k_wait_probe_tall(long long cycles) {
+  __shared__ __align__(8) uint64_t bar;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 2);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if (threadIdx.x == 0) {
+    mbar_arrive(&bar);
+    mbar_wait_bounded(&bar, 0, cycles);
+  }
+  __syncwarp();
+}
+
+cudaError_t launch_pdl_cluster(const void* fn, dim3 grid, size_t smem, cudaStream_t stream, void** args, dim3 cluster) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kTallThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster.x;
+  attr[1].val.clusterDim.y = cluster.y;
+  attr[1].val.clusterDim.z = cluster.z;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster.x * cluster.z > 1 ? 2 : 1;
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+// Rows of an activation array: boxes of 64 columns by one row (gathers) and by 64 rows.
+cudaError_t encode_rows(CUtensorMap* single, CUtensorMap* box, const __half* x, int K, int M) {
+  const cudaError_t e = encode_tiled_2d(single, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2,
+                                        kCols, 1, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  return encode_tiled_2d(box, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2, kCols, kWideRows,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int R>
+cudaError_t allow_tall() {
+  const cudaError_t e = cudaFuncSetAttribute(k_contract_tall<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, TallContract<R>::smem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(k_grad_tall<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, TallGrad<R>::smem);
+}
+
+}  // namespace
+
+cudaError_t prepare_tall_kernels(int device) {
+  (void)device;
+  cudaError_t e;
+  if ((e = allow_tall<16>()) || (e = allow_tall<32>()) || (e = allow_tall<64>())) return e;
+  return allow_tall<128>();
+}
+
+cudaError_t encode_adapter_maps(dictproj_adapters* a) {
+  cudaError_t e;
+  const uint64_t ranks = (uint64_t)a->n_slots * a->rp, rows = (uint64_t)adapter_tiles(a->max_tokens, a->n_slots, kWideRows) * kWideRows;
+  if ((e = encode_tiled_2d(&a->a_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a->A, (uint64_t)a->d_in, ranks, (uint64_t)a->d_in * 2,
+                           kCols, 16, CU_TENSOR_MAP_SWIZZLE_128B)) ||
+      (e = encode_tiled_2d(&a->b_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a->B, (uint64_t)a->ld_b, ranks, (uint64_t)a->ld_b * 2,
+                           kCols, 16, CU_TENSOR_MAP_SWIZZLE_128B)))
+    return e;
+  for (int i = 0; i < 2; ++i)
+    for (int p = 0; p < 2; ++p)
+      if ((e = encode_tiled_2d(&a->part_map[i][p], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a->part[i][p], (uint64_t)a->rp, rows,
+                               (uint64_t)a->rp * 2, 64, kWideRows, CU_TENSOR_MAP_SWIZZLE_128B)))
+        return e;
+  return cudaSuccess;
+}
+
+// Rows that TMA can read, and enough of them to fill 128-row tiles.
+bool tall_serves(const dictproj_adapters* a, const dictproj_rows* r) { return a->d_out % 8 == 0 && r->M >= 256; }
+
+#define DICTPROJ_TALL(rp, kernel, shape)                                             \
+  ((rp) <= 16 ? std::make_pair((const void*)kernel<16>, (int)shape<16>::smem)        \
+   : (rp) <= 32 ? std::make_pair((const void*)kernel<32>, (int)shape<32>::smem)      \
+   : (rp) <= 64 ? std::make_pair((const void*)kernel<64>, (int)shape<64>::smem)      \
+                : std::make_pair((const void*)kernel<128>, (int)shape<128>::smem))
+
+cudaError_t launch_contract_tall(RowsArgs& g, int passes, const dictproj_adapters* a, const dictproj_rows* r,
+                                 cudaStream_t stream) {
+  TallContractArgs args;
+  cudaError_t e;
+  for (int i = 0; i < passes; ++i) {
+    if ((e = encode_rows(&args.in[i], &args.box[i], g.pass[i].in, g.pass[i].K, r->M)) != cudaSuccess) return e;
+    args.p[i] = reinterpret_cast<const uint16_t*>(g.pass[i].P) == a->A ? a->a_map : a->b_map;
+  }
+  args.g = g;
+  args.g.tiles = r->tiles[2];
+  args.g.n_tiles = r->n_tiles + 4;
+  const int full = std::max(1, r->M / kTallRows) * passes;  // tiles that do exist, about
+  args.g.cluster = 2;
+  while (args.g.cluster < 8 && full * args.g.cluster < 2 * a->n_sm) args.g.cluster *= 2;
+  const auto k = DICTPROJ_TALL(g.rp, k_contract_tall, TallContract);
+  void* p[] = {(void*)&args};
+  return launch_pdl_cluster(k.first, dim3((unsigned)(adapter_tiles(r->M, r->n_slots, kTallRows) * args.g.cluster), passes), k.second,
+                            stream, p, dim3(args.g.cluster, 1, 1));
+}
+
+cudaError_t launch_grad_tall(const GradArgs& w, const dictproj_adapters* a, const dictproj_rows* r, cudaStream_t stream) {
+  TallGradArgs args;
+  cudaError_t e;
+  for (int i = 0; i < 2; ++i) {
+    if ((e = encode_rows(&args.in[i], &args.box[i], w.pass[i].in, w.pass[i].K, r->M)) != cudaSuccess) return e;
+    for (int p = 0; p < 2; ++p) args.part[i][p] = a->part_map[i][p];
+  }
+  args.g = w;
+  const int blocks = w.pass[0].blocks + w.pass[1].blocks;
+  int split = 1;
+  while (split < 8 && blocks * a->n_slots * split < 2 * a->n_sm && kWideRows * a->n_slots * split < r->M) split *= 2;
+  const auto k = DICTPROJ_TALL(w.rp, k_grad_tall, TallGrad);
+  void* p[] = {(void*)&args};
+  return launch_pdl_cluster(k.first, dim3(blocks, a->n_slots, split), k.second, stream, p, dim3(1, 1, split));
+}
+
+cudaError_t launch_wait_probe_tall(long long cycles, cudaStream_t stream) {
+  k_wait_probe_tall<<<1, 32, 0, stream>>>(cycles);
+  return cudaGetLastError();
+}
+
+cudaError_t take_tall_error(unsigned int* out) {
+  unsigned int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_dictproj_error, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_dictproj_error, &zero, sizeof(unsigned int));
+}
+
+}  // namespace dictproj

@@ -117,10 +117,12 @@ struct dictproj_adapters {
   uint16_t* B;             // fp16 [n_slots][rp][ld_b]
   int* rank;               // [n_slots], 0 = empty
   float* scale;            // [n_slots]
-  // backward pass: scale * U (index 0) and scale * T (1) of the planned rows, in plan
-  // order, as two fp16 parts times a power of two per 64-row tile (adapter.cu)
-  uint16_t* part[2][2];    // [pass][high, low] fp16 [max_tokens][rp]
+  // batches of many rows: scale * T (forward), or scale * U (index 0) and scale * T (1) of
+  // the backward pass, as two fp16 parts times a power of two per 64-row tile (adapter.cuh)
+  uint16_t* part[2][2];    // [pass][high, low] fp16 [adapter_tiles(64)][64][rp]
   float* unit[2];          // [pass] what a tile's parts are multiplied with, [adapter_tiles(64)]
+  CUtensorMap a_map, b_map;      // A and B as [n_slots * rp] rows, box 64 columns x 16 rows
+  CUtensorMap part_map[2][2];    // the parts as rows of rp, box 64 columns x 64 rows
 };
 
 // Most tiles of `rows` rows that M rows over n_slots slots (and no slot) can form.
@@ -136,10 +138,10 @@ struct dictproj_rows {
   int M;                   // rows of the last dictproj_rows_set (0: none yet)
   int* perm;               // [max_rows] row numbers by slot, rows without an adapter last
   int* start;              // [n_slots + 2] first position of each slot, of the rows without one, M
-  // tiles of up to 4 (index 0) and 64 (1) rows of one slot, in plan order; those of
-  // rows without an adapter (slot n_slots) come last
-  int* n_tiles;            // [2][2] tiles of the slots, all tiles
-  int4* tiles[2];          // {slot, first position, rows, row number of the first}
+  // tiles of up to 4 (index 0), 64 (1) and 128 (2) rows of one slot, in plan order; those
+  // of rows without an adapter (slot n_slots) come last
+  int* n_tiles;            // [3][2] tiles of the slots, all tiles
+  int4* tiles[3];          // {slot, first position, rows, row number of the first (2: its first 64-row tile)}
   int* first64;            // [n_slots] first 64-row tile of each slot
 };
 

@@ -126,6 +126,19 @@ cudaError_t launch_gemm_nn(const __half* A, const __half* B, int M, int N, int K
 
 // adapters (adapter.cu)
 cudaError_t prepare_adapter_kernels(int device);
+cudaError_t prepare_tall_kernels(int device);
+// Tensor maps of the pool's arrays (contractions and gradients on tcgen05).
+cudaError_t encode_adapter_maps(dictproj_adapters* a);
+// Whether the tcgen05 kernels (adapter_tall.cu) serve a batch of many rows.
+bool tall_serves(const dictproj_adapters* a, const dictproj_rows* r);
+struct RowsArgs;
+struct GradArgs;
+cudaError_t launch_contract_tall(RowsArgs& g, int passes, const dictproj_adapters* a, const dictproj_rows* r,
+                                 cudaStream_t stream);
+cudaError_t launch_grad_tall(const GradArgs& w, const dictproj_adapters* a, const dictproj_rows* r,
+                             cudaStream_t stream);
+cudaError_t take_tall_error(unsigned int* out);
+cudaError_t launch_wait_probe_tall(long long cycles, cudaStream_t stream);
 cudaError_t launch_adapter_set(const dictproj_adapters* a, int slot, int rank, float scale, const __half* A,
                                const __half* B, cudaStream_t stream);
 cudaError_t launch_rows_plan(const dictproj_rows* r, const int* ids, int M, cudaStream_t stream);

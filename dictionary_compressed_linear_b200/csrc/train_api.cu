@@ -102,7 +102,7 @@ int dictproj_adapters_create(int d_in, int d_out, int max_rank, int n_slots, int
     return cuda_fail(e, "adapters_create: SM count");
   }
   const size_t ab = (size_t)n_slots * a->rp * d_in * 2, bb = (size_t)n_slots * a->rp * a->ld_b * 2;
-  const size_t pb = (size_t)max_tokens * a->rp * 2, ub = (size_t)adapter_tiles(max_tokens, n_slots, 64) * sizeof(float);
+  const size_t t64 = (size_t)adapter_tiles(max_tokens, n_slots, 64), pb = t64 * 64 * a->rp * 2, ub = t64 * sizeof(float);
   if ((e = dmalloc((void**)&a->A, ab)) || (e = dmalloc((void**)&a->B, bb)) ||
       (e = dmalloc((void**)&a->rank, (size_t)n_slots * 4)) || (e = dmalloc((void**)&a->scale, (size_t)n_slots * 4)) ||
       (e = dmalloc((void**)&a->part[0][0], pb)) || (e = dmalloc((void**)&a->part[0][1], pb)) ||
@@ -118,6 +118,10 @@ int dictproj_adapters_create(int d_in, int d_out, int max_rank, int n_slots, int
     dictproj_free_adapters(a);
     cudaGetLastError();
     return cuda_fail(e, "adapters_create: empty slots");
+  }
+  if ((e = encode_adapter_maps(a)) != cudaSuccess) {
+    dictproj_free_adapters(a);
+    return cuda_fail(e, "adapters_create: tensor maps");
   }
   *out = a;
   return DICTPROJ_OK;
@@ -183,9 +187,10 @@ int dictproj_rows_create(int max_rows, int n_slots, dictproj_rows** out) {
   r->n_slots = n_slots;
   cudaError_t e;
   if ((e = dmalloc((void**)&r->perm, (size_t)max_rows * 4)) || (e = dmalloc((void**)&r->start, (size_t)(n_slots + 2) * 4)) ||
-      (e = dmalloc((void**)&r->n_tiles, 4 * sizeof(int))) || (e = dmalloc((void**)&r->first64, (size_t)n_slots * 4)) ||
+      (e = dmalloc((void**)&r->n_tiles, 6 * sizeof(int))) || (e = dmalloc((void**)&r->first64, (size_t)n_slots * 4)) ||
       (e = dmalloc((void**)&r->tiles[0], (size_t)adapter_tiles(max_rows, n_slots, 4) * sizeof(int4))) ||
-      (e = dmalloc((void**)&r->tiles[1], (size_t)adapter_tiles(max_rows, n_slots, 64) * sizeof(int4)))) {
+      (e = dmalloc((void**)&r->tiles[1], (size_t)adapter_tiles(max_rows, n_slots, 64) * sizeof(int4))) ||
+      (e = dmalloc((void**)&r->tiles[2], (size_t)adapter_tiles(max_rows, n_slots, 128) * sizeof(int4)))) {
     dictproj_free_rows(r);
     cudaGetLastError();
     return fail(DICTPROJ_ERR_OOM, "rows_create: device allocation failed (%s)", cudaGetErrorName(e));
@@ -202,6 +207,7 @@ void dictproj_free_rows(dictproj_rows* r) {
   cudaFree(r->first64);
   cudaFree(r->tiles[0]);
   cudaFree(r->tiles[1]);
+  cudaFree(r->tiles[2]);
   delete r;
 }
 
