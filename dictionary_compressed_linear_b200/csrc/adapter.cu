@@ -66,7 +66,8 @@ __device__ __forceinline__ int block_exclusive_sum(int x, int* wsum, int* total)
 __global__ void __launch_bounds__(kPlanWarps * 32)
     k_rows_plan(const int* __restrict__ ids, int M, int n_slots, int* __restrict__ perm, int* __restrict__ start,
                 int* __restrict__ n_tiles, int4* __restrict__ tiles4, int4* __restrict__ tiles64,
-                int4* __restrict__ tiles128, int* __restrict__ first64) {
+                int4* __restrict__ tiles128, int* __restrict__ runs64, int* __restrict__ runs128,
+                int* __restrict__ first64) {
   extern __shared__ int plan_smem[];
   __shared__ int wsum[kPlanWarps];
   const int nb = n_slots + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -155,9 +156,10 @@ __global__ void __launch_bounds__(kPlanWarps * 32)
         if (tf[mid] <= t) a = mid;
         else z = mid - 1;
       }
-      const int p = begin[a] + (t - tf[a]) * T;
-      const int w = q == 2 ? tfirst[nb + 1 + a] + 2 * (t - tf[a]) : perm[p];
-      tiles[t] = make_int4(a, p, min(T, begin[a + 1] - p), w);
+      const int p = begin[a] + (t - tf[a]) * T, n = min(T, begin[a + 1] - p), row = perm[p];
+      tiles[t] = make_int4(a, p, n, q == 2 ? tfirst[nb + 1 + a] + 2 * (t - tf[a]) : row);
+      // a bucket's rows ascend: they follow one another when the last is n - 1 further
+      if (q) (q == 1 ? runs64 : runs128)[t] = perm[p + n - 1] - row == n - 1 ? row : -1;
     }
   }
 }
@@ -204,55 +206,6 @@ template <int PITCH>
 __device__ __forceinline__ uint32_t swz(int row, int p) {
   constexpr int per = PITCH / 16, shift = PITCH >= 128 ? 0 : PITCH == 64 ? 1 : 2, mask = per >= 8 ? 7 : per - 1;
   return (uint32_t)(row * PITCH + 16 * (p ^ ((row >> shift) & mask)));
-}
-
-// 8 elements from column c of a row of n elements, zeros past the end. Rows of an odd
-// length start at any even byte: two aligned 16-byte loads and a shift, as long as both
-// lie inside the array (which ends at `end`), single elements otherwise.
-__device__ __forceinline__ uint4 read_piece(const __half* row, int c, int n, bool vec, const __half* end) {
-  if (vec) return c < n ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
-  const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
-  const uint4* q = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
-  if (c + 8 <= n && reinterpret_cast<uintptr_t>(q + 2) <= reinterpret_cast<uintptr_t>(end)) {
-    const uint4 a = q[0], b = q[1];
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    const uint32_t words = (uint32_t)(at >> 2) & 3u, shift = 8u * ((uint32_t)at & 2u);
-    if (words & 2) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = w[6], w[5] = w[7];
-    if (words & 1) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
-    return make_uint4(__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift),
-                      __funnelshift_r(w[2], w[3], shift), __funnelshift_r(w[3], w[4], shift));
-  }
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const unsigned short a = c + 2 * i < n ? __half_as_ushort(row[c + 2 * i]) : 0;
-    const unsigned short b = c + 2 * i + 1 < n ? __half_as_ushort(row[c + 2 * i + 1]) : 0;
-    w[i] = (uint32_t)a | ((uint32_t)b << 16);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void write_piece(__half* row, int c, int n, bool vec, const uint4& v) {
-  if (vec) {
-    if (c < n) *reinterpret_cast<uint4*>(row + c) = v;
-    return;
-  }
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  if (c + 8 <= n) {
-    unsigned short* h = reinterpret_cast<unsigned short*>(row + c);
-    if ((reinterpret_cast<uintptr_t>(h) & 2) == 0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(h)[i] = w[i];
-    } else {
-      h[0] = (unsigned short)w[0];
-#pragma unroll
-      for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t*>(h + 1 + 2 * i) = __funnelshift_r(w[i], w[i + 1], 16);
-      h[7] = (unsigned short)(w[3] >> 16);
-    }
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (c + e < n) row[c + e] = __ushort_as_half((unsigned short)(w[e >> 1] >> (16 * (e & 1))));
 }
 
 // ---- contraction and expansion -------------------------------------------------------------
@@ -403,17 +356,6 @@ __device__ __forceinline__ void few_rows(const RowsPass& a, int n_rows, const Fe
   cluster_wait();
 }
 
-// base alone, for rows without an adapter: pieces [lo, hi) of the columns
-__device__ __forceinline__ void copy_rows(const RowsPass& a, int n_rows, const int* rows, int count, int lo, int hi) {
-  const bool vec = (a.N & 7) == 0;
-  const int n = hi - lo;
-  for (int i = threadIdx.x; i < count * n; i += kRowThreads) {
-    const size_t at = (size_t)rows[i / n] * a.N;
-    const int c = 8 * (lo + i % n);
-    write_piece(a.out + at, c, a.N, vec, a.base ? read_piece(a.base + at, c, a.N, vec, a.base + (size_t)n_rows * a.N) : make_uint4(0, 0, 0, 0));
-  }
-}
-
 // VEC: K and N are multiples of 8, every row 16-byte aligned.
 template <int R, bool VEC>
 __global__ void __launch_bounds__(kRowThreads, R <= 32 ? 4 : 2) k_adapter_few(const __grid_constant__ RowsArgs g) {
@@ -493,7 +435,7 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_c
   if (r == 0) return;
   if (tid < TM) srow[tid] = tid < count ? g.perm[tile.y + tid] : tile.w;
   const bool vec = (a.K & 7) == 0;
-  const int kc = (a.K + CW - 1) / CW, k_lo = kc * rankc / cluster, nk = kc * (rankc + 1) / cluster - k_lo;
+  const int kc = (a.K + CW - 1) / CW, nk = (kc - rankc + cluster - 1) / cluster;  // blocks in turn
   const float scale = g.scale[slot];
   __syncthreads();
   // this thread's 16-byte column and rows of a stage
@@ -506,7 +448,7 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_c
   auto issue = [&](int i) {
     if (i < nk) {
       const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes + spot;
-      const int col = (k_lo + i) * CW, c = col + 8 * piece;
+      const int col = (i * cluster + rankc) * CW, c = col + 8 * piece;
 #pragma unroll
       for (int q = 0; q < TM / STEP; ++q) {
         const bool in = row0 + STEP * q < count && c < a.K;
@@ -575,11 +517,7 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_c
     const int j = i % R, row = row_lo + i / R;
     if (j >= r16 || row >= count) continue;
     const uint32_t at = pbase + 4 * (row * R + j);
-    float4 x = ld_peer_v4f(peer_smem(at, 0));
-    for (int c = 1; c < cluster; ++c) {
-      const float4 y = ld_peer_v4f(peer_smem(at, c));
-      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-    }
+    const float4 x = sum_peers(at, cluster);
     const float v[4] = {j < r ? x.x * scale : 0.f, j + 1 < r ? x.y * scale : 0.f, j + 2 < r ? x.z * scale : 0.f,
                         j + 3 < r ? x.w * scale : 0.f};
     *reinterpret_cast<float4*>(own + i) = make_float4(v[0], v[1], v[2], v[3]);
@@ -606,13 +544,13 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_c
     if (j >= r16) continue;
     const float4 x = row < count ? *reinterpret_cast<const float4*>(own + i) : make_float4(0.f, 0.f, 0.f, 0.f);
     const Split s0 = split_half(x.x * unit), s1 = split_half(x.y * unit), s2 = split_half(x.z * unit), s3 = split_half(x.w * unit);
-    const size_t at = (size_t)(tile_no * TM + row) * g.rp + j;
-    *reinterpret_cast<uint2*>(a.hi + at) = make_uint2(half2_bits(s0.hi, s1.hi), half2_bits(s2.hi, s3.hi));
-    *reinterpret_cast<uint2*>(a.lo + at) = make_uint2(half2_bits(s0.lo, s1.lo), half2_bits(s2.lo, s3.lo));
+    __half* at = a.parts + (size_t)(tile_no * TM + row) * (2 * g.pp) + j;
+    *reinterpret_cast<uint2*>(at) = make_uint2(half2_bits(s0.hi, s1.hi), half2_bits(s2.hi, s3.hi));
+    *reinterpret_cast<uint2*>(at + g.pp) = make_uint2(half2_bits(s0.lo, s1.lo), half2_bits(s2.lo, s3.lo));
   }
 }
 
-// Expansion: a CTA takes a range of 128-column blocks of one tile; T's parts sit in MMA
+// Expansion: a CTA takes some 128-column blocks of one tile; T's parts sit in MMA
 // fragments throughout, the base tile and r rows of Q of the next blocks arrive (cp.async)
 // while one is computed. The launch before is the contraction of the same call, which lets
 // this one start only after its own dependency wait: all that was written before the call
@@ -621,7 +559,7 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_c
 template <int R>
 struct ExpandShape {
   static constexpr int TM = kWideRows, CW = 128, kPitch = 2 * CW;
-  static constexpr int kStages = R <= 32 ? 3 : 2, kStageBytes = (TM + R) * kPitch;
+  static constexpr int kStages = R <= 64 ? 3 : 2, kStageBytes = (TM + R) * kPitch;
   static constexpr int smem = kStages * kStageBytes;
 };
 
@@ -644,12 +582,14 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_expand(const __grid_con
   const int count = tile.z, slot = tile.x;
   const int r = slot < g.n_slots ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
   const bool vec = (a.N & 7) == 0;
-  const int blocks = (a.N + CW - 1) / CW, b_lo = blocks * blockIdx.x / gridDim.x;
-  const int nb = blocks * (blockIdx.x + 1) / gridDim.x - b_lo;
+  // the CTAs of a tile take its column blocks in turn, so that they read and write
+  // neighbouring parts of the rows at the same time
+  const int blocks = (a.N + CW - 1) / CW, b0 = blockIdx.x, parts = gridDim.x, nb = (blocks - b0 + parts - 1) / parts;
   if (r == 0) {  // base alone
     grid_dependency_wait();
     if (!in_place)
-      copy_rows(a, g.rows, g.perm + tile.y, count, b_lo * (CW / 8), min((b_lo + nb) * (CW / 8), (a.N + 7) / 8));
+      for (int b = b0; b < blocks; b += parts)
+        copy_rows(a, g.rows, g.perm + tile.y, count, b * (CW / 8), min((b + 1) * (CW / 8), (a.N + 7) / 8));
     return;
   }
   const int piece = tid & 15, row0 = tid >> 4;
@@ -661,7 +601,7 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_expand(const __grid_con
   auto issue = [&](int i) {
     if (i < nb) {
       const uint32_t dst = spot + (uint32_t)(i % S::kStages) * S::kStageBytes;
-      const int c = (b_lo + i) * CW + 8 * piece;
+      const int c = (b0 + i * parts) * CW + 8 * piece;
       const bool inq = c < a.ld_q;
 #pragma unroll
       for (int j = 0; j < R / 16; ++j)
@@ -685,10 +625,10 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_expand(const __grid_con
   for (int t = 0; t < R / 16; ++t)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const size_t at = (size_t)(tile_no * TM + g0 + 8 * (q & 1)) * g.rp + 16 * t + c0 + 8 * (q >> 1);
+      const __half* at = a.parts + (size_t)(tile_no * TM + g0 + 8 * (q & 1)) * (2 * g.pp) + 16 * t + c0 + 8 * (q >> 1);
       const bool in = 16 * t < r16;
-      thi[t][q] = in ? *reinterpret_cast<const uint32_t*>(a.hi + at) : 0u;
-      tlo[t][q] = in ? *reinterpret_cast<const uint32_t*>(a.lo + at) : 0u;
+      thi[t][q] = in ? *reinterpret_cast<const uint32_t*>(at) : 0u;
+      tlo[t][q] = in ? *reinterpret_cast<const uint32_t*>(at + g.pp) : 0u;
     }
   const float back = a.unit[tile_no];
   constexpr int NT = CW / 16;  // 8-column tiles of a warp
@@ -726,7 +666,7 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_expand(const __grid_con
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(*reinterpret_cast<const uint32_t*>(&o)) : "memory");
       }
     __syncthreads();
-    const int c = (b_lo + i) * CW + 8 * piece;
+    const int c = (b0 + i * parts) * CW + 8 * piece;
 #pragma unroll
     for (int q = 0; q < TM / 16; ++q)
       if (row[q] >= 0) write_piece(a.out + (size_t)row[q] * a.N, c, a.N, vec, lds_u32x4(spot + off + 16 * q * PITCH));
@@ -810,10 +750,10 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
       for (int q = tid; q < 64 * pieces; q += kGradThreads) {
         const int row = q / pieces, c = q % pieces;
         if (8 * c >= r16) continue;
-        const size_t at = (size_t)((tile0 + t_lo + i) * kWideRows + row) * g.rp + 8 * c;
+        const __half* at = a.parts + (size_t)((tile0 + t_lo + i) * kWideRows + row) * (2 * g.pp) + 8 * c;
         const uint32_t dst = st + S::kInBytes + swz<S::kTPitch>(row, c);
-        cp_async16(dst, a.hi + at, 16);
-        cp_async16(dst + S::kTBytes, a.lo + at, 16);
+        cp_async16(dst, at, 16);
+        cp_async16(dst + S::kTBytes, at + g.pp, 16);
       }
     }
     cp_async_commit();
@@ -936,6 +876,7 @@ RowsArgs rows_args(const dictproj_adapters* a, const dictproj_rows* r, bool wide
   g.rank = a->rank;
   g.scale = a->scale;
   g.rp = a->rp;
+  g.pp = a->pp;
   g.n_slots = a->n_slots;
   g.rows = r->M;
   g.cluster = kCluster;
@@ -983,7 +924,9 @@ cudaError_t launch_contract(RowsArgs& g, int passes, const dictproj_adapters* po
 #undef FN
 #undef SMEM
 }
-cudaError_t launch_expand(const RowsArgs& g, const dictproj_rows* r, int n_sm, cudaStream_t stream) {
+cudaError_t launch_expand(const RowsArgs& g, const dictproj_adapters* pool, const dictproj_rows* r, cudaStream_t stream) {
+  if (tall_serves(pool, r)) return launch_expand_tall(g, pool, r, stream);
+  const int n_sm = pool->n_sm;
   const int tiles = adapter_tiles(r->M, r->n_slots, kWideRows), blocks = (g.pass[0].N + 127) / 128;
   const int full = std::max(1, r->M / kWideRows);  // tiles that do exist, about
   // as many CTAs as run at once (two an SM above rank 32): 2048 rows of rank 32 took 22.3 us
@@ -1038,15 +981,15 @@ cudaError_t launch_adapter_set(const dictproj_adapters* a, int slot, int rank, f
 cudaError_t launch_rows_plan(const dictproj_rows* r, const int* ids, int M, cudaStream_t stream) {
   int ns = r->n_slots;
   void* args[] = {&ids, &M, &ns, (void*)&r->perm, (void*)&r->start, (void*)&r->n_tiles, (void*)&r->tiles[0],
-                  (void*)&r->tiles[1], (void*)&r->tiles[2], (void*)&r->first64};
+                  (void*)&r->tiles[1], (void*)&r->tiles[2], (void*)&r->runs[0], (void*)&r->runs[1],
+                  (void*)&r->first64};
   return launch_pdl((const void*)k_rows_plan, dim3(1), dim3(kPlanWarps * 32),
                     ((size_t)kPlanWarps * (ns + 1) + 4 * (ns + 2)) * sizeof(int), stream, args);
 }
 
 static void set_parts(const dictproj_adapters* a, RowsArgs& g) {
   for (int i = 0; i < 2; ++i) {
-    g.pass[i].hi = reinterpret_cast<__half*>(a->part[i][0]);
-    g.pass[i].lo = reinterpret_cast<__half*>(a->part[i][1]);
+    g.pass[i].parts = reinterpret_cast<__half*>(a->parts[i]);
     g.pass[i].unit = a->unit[i];
   }
 }
@@ -1059,7 +1002,7 @@ cudaError_t launch_adapter_forward(const dictproj_adapters* a, const dictproj_ro
   if (!wide) return launch_few(g, r, stream);
   set_parts(a, g);
   const cudaError_t e = launch_contract(g, 1, a, r, stream);
-  return e == cudaSuccess ? launch_expand(g, r, a->n_sm, stream) : e;
+  return e == cudaSuccess ? launch_expand(g, a, r, stream) : e;
 }
 
 cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_rows* r, const __half* X,
@@ -1070,13 +1013,12 @@ cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_r
   g.pass[1] = rows_pass(a, true, X, nullptr, nullptr);
   set_parts(a, g);
   cudaError_t e = launch_contract(g, dA ? 2 : 1, a, r, stream);
-  if (e == cudaSuccess && dX) e = launch_expand(g, r, a->n_sm, stream);
+  if (e == cudaSuccess && dX) e = launch_expand(g, a, r, stream);
   if (e != cudaSuccess || !dA) return e;
   GradArgs w = {};
   for (int i = 0; i < 2; ++i) {
     w.pass[i].in = i ? dY : X;
-    w.pass[i].hi = g.pass[i].hi;
-    w.pass[i].lo = g.pass[i].lo;
+    w.pass[i].parts = g.pass[i].parts;
     w.pass[i].unit = a->unit[i];
     w.pass[i].g = i ? dB : dA;
     w.pass[i].K = i ? a->d_out : a->d_in;
@@ -1084,9 +1026,11 @@ cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_r
   }
   w.start = r->start;
   w.first64 = r->first64;
+  w.runs = r->runs[0];
   w.perm = r->perm;
   w.rank = a->rank;
   w.rp = a->rp;
+  w.pp = a->pp;
   w.max_rank = a->max_rank;
   w.accumulate = accumulate;
   w.n_rows = r->M;

@@ -17,10 +17,9 @@ struct RowsPass {
   const __half* Q;
   const __half* base;
   __half* out;
-  // many rows: the two parts of scale * T, [tile][kWideRows][rp], zeros past a tile's
-  // rows, and what the parts of a tile are multiplied with
-  __half* hi;
-  __half* lo;
+  // many rows: the two parts of scale * T, [tile][kWideRows][high pp | low pp], zeros past
+  // a tile's rows, and what the parts of a tile are multiplied with
+  __half* parts;
   float* unit;
   int K, N, ld_p, ld_q;
 };
@@ -28,16 +27,16 @@ struct RowsArgs {
   RowsPass pass[2];
   const int* n_tiles;
   const int4* tiles;
+  const int* runs;  // 128-row tiles: the first row of a tile whose rows follow one another, else -1
   const int* perm;
   const int* rank;
   const float* scale;
-  int rp, n_slots, rows, cluster;
+  int rp, pp, n_slots, rows, cluster;
 };
 
 struct GradPass {
   const __half* in;
-  const __half* hi;
-  const __half* lo;
+  const __half* parts;
   const float* unit;
   float* g;
   int K, blocks;
@@ -46,9 +45,10 @@ struct GradArgs {
   GradPass pass[2];
   const int* start;
   const int* first64;
+  const int* runs;  // of the 64-row tiles
   const int* perm;
   const int* rank;
-  int rp, max_rank, accumulate, n_rows;
+  int rp, pp, max_rank, accumulate, n_rows;
 };
 
 // ---- clusters and distributed shared memory
@@ -68,6 +68,17 @@ __device__ __forceinline__ float ld_peer_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
+}
+// Four floats of every CTA of the cluster, summed in rank order (the loads go out together).
+__device__ __forceinline__ float4 sum_peers(uint32_t local, int cluster) {
+  float4 v[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    if (c < cluster) v[c] = ld_peer_v4f(peer_smem(local, c));
+#pragma unroll
+  for (int c = 1; c < 8; ++c)
+    if (c < cluster) v[0].x += v[c].x, v[0].y += v[c].y, v[0].z += v[c].z, v[0].w += v[c].w;
+  return v[0];
 }
 __device__ __forceinline__ void st_peer_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -95,6 +106,66 @@ __device__ __forceinline__ float split_unit(float m) {
   if (m == 0.f) return 1.f;
   const int e = (int)((__float_as_uint(m) >> 23) & 255) - 127;  // -127 for a subnormal
   return __uint_as_float((uint32_t)(min(13 - e, 126) + 127) << 23);
+}
+
+// 8 elements from column c of a row of n elements, zeros past the end. Rows of an odd
+// length start at any even byte: two aligned 16-byte loads and a shift, as long as both
+// lie inside the array (which ends at `end`), single elements otherwise.
+__device__ __forceinline__ uint4 read_piece(const __half* row, int c, int n, bool vec, const __half* end) {
+  if (vec) return c < n ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+  const uint4* q = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
+  if (c + 8 <= n && reinterpret_cast<uintptr_t>(q + 2) <= reinterpret_cast<uintptr_t>(end)) {
+    const uint4 a = q[0], b = q[1];
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const uint32_t words = (uint32_t)(at >> 2) & 3u, shift = 8u * ((uint32_t)at & 2u);
+    if (words & 2) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = w[6], w[5] = w[7];
+    if (words & 1) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
+    return make_uint4(__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift),
+                      __funnelshift_r(w[2], w[3], shift), __funnelshift_r(w[3], w[4], shift));
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned short a = c + 2 * i < n ? __half_as_ushort(row[c + 2 * i]) : 0;
+    const unsigned short b = c + 2 * i + 1 < n ? __half_as_ushort(row[c + 2 * i + 1]) : 0;
+    w[i] = (uint32_t)a | ((uint32_t)b << 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void write_piece(__half* row, int c, int n, bool vec, const uint4& v) {
+  if (vec) {
+    if (c < n) *reinterpret_cast<uint4*>(row + c) = v;
+    return;
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (c + 8 <= n) {
+    unsigned short* h = reinterpret_cast<unsigned short*>(row + c);
+    if ((reinterpret_cast<uintptr_t>(h) & 2) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(h)[i] = w[i];
+    } else {
+      h[0] = (unsigned short)w[0];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t*>(h + 1 + 2 * i) = __funnelshift_r(w[i], w[i + 1], 16);
+      h[7] = (unsigned short)(w[3] >> 16);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c + e < n) row[c + e] = __ushort_as_half((unsigned short)(w[e >> 1] >> (16 * (e & 1))));
+}
+
+// base alone, for rows without an adapter: pieces [lo, hi) of the columns
+__device__ __forceinline__ void copy_rows(const RowsPass& a, int n_rows, const int* rows, int count, int lo, int hi) {
+  const bool vec = (a.N & 7) == 0;
+  const int n = hi - lo;
+  for (int i = threadIdx.x; i < count * n; i += blockDim.x) {
+    const size_t at = (size_t)rows[i / n] * a.N;
+    const int c = 8 * (lo + i % n);
+    write_piece(a.out + at, c, a.N, vec, a.base ? read_piece(a.base + at, c, a.N, vec, a.base + (size_t)n_rows * a.N) : make_uint4(0, 0, 0, 0));
+  }
 }
 
 // Largest of the warp's finite non-negative values.

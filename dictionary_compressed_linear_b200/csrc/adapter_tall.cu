@@ -1,7 +1,8 @@
-// Adapters of many rows on the 5th-generation tensor cores: the contraction T = X A^T
-// and the weight gradients T^T X, for row lengths that TMA can read (multiples of 8).
+// Adapters of many rows on the 5th-generation tensor cores: the contraction T = X A^T, the
+// expansion base + T B and the weight gradients T^T X, for row lengths that TMA can read
+// (multiples of 8).
 //
-// Both stream the activations once for few operations, so the aim is to move them with
+// All three stream the activations once for few operations, so the aim is to move them with
 // as few instructions as can be: the rows of a tile arrive by TMA (128-byte swizzle) and
 // are multiplied by one thread's tcgen05.mma; the mma.sync kernels of adapter.cu, which
 // serve the other row lengths, spend 28 M warp instructions where these need 9 M (8192
@@ -18,6 +19,8 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
+#include <utility>
 
 #include "adapter.cuh"
 #include "common.cuh"
@@ -48,16 +51,16 @@ __device__ __forceinline__ void drain(uint64_t* full, int stages, int s) {
 struct TallContractArgs {
   CUtensorMap in[2], box[2], p[2];  // In by single rows and by 64, P by 16
   RowsArgs g;
+  int stages;
 };
+
+constexpr int kMaxStages = 12;
 
 template <int R>
 struct TallContract {
-  static constexpr int kStages = R == 16 ? 5 : R <= 64 ? 4 : 3;
   static constexpr int kInBytes = kTallRows * 128, kStageBytes = kInBytes + R * 128;
-  static constexpr int kPitch = R + 4;  // floats of a row of the partial sums
-  static constexpr int kRing = kStages * kStageBytes;
-  static_assert(kTallRows * kPitch * 4 <= kRing, "the partial sums lie over the drained ring");
-  static constexpr int smem = kRing + 1024 + 256;
+  static constexpr int kPitch = R + 4;  // floats of a row of the partial sums, which lie over the drained ring
+  static constexpr int kPart = kTallRows * kPitch * 4;
   static constexpr int kTmem = R < 32 ? 32 : R;
 };
 
@@ -66,88 +69,112 @@ __global__ void __launch_bounds__(kTallThreads) k_contract_tall(const __grid_con
   using S = TallContract<R>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kRing);
-  uint64_t* empty = full + S::kStages;
-  uint64_t* accf = empty + S::kStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], accf;
+  __shared__ uint32_t tmem_slot;
   __shared__ float smax[2][kTallThreads / 32], cmax[2][8];
   const RowsArgs& g = args.g;
   const RowsPass& a = g.pass[blockIdx.y];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, stages = args.stages;
   const int cluster = g.cluster, rankc = blockIdx.x % cluster, tile_no = blockIdx.x / cluster;
 
-  grid_dependency_wait();
-  const int4 tile = g.tiles[tile_no];
-  if (tile_no >= g.n_tiles[0]) return;  // the whole cluster
-  const int count = tile.z, slot = tile.x, r = g.rank[slot], r16 = (r + 15) & ~15;
-  if (r == 0) return;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(&full[s], 1);
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 2);  // In's bytes and P's are announced apart
       mbar_init(&empty[s], 1);
     }
-    mbar_init(accf, 1);
+    mbar_init(&accf, 1);
     fence_mbar_init();
+    tma_prefetch_map(&args.box[blockIdx.y]);
+    tma_prefetch_map(&args.p[blockIdx.y]);
   }
-  if (warp == 1) tmem_alloc(tmem_slot, S::kTmem);
+  if (warp == 1) tmem_alloc(&tmem_slot, S::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  grid_dependency_wait();
   trigger_dependents();  // not before the tensor memory is ours: a dependent may want all of it
-  const uint32_t tmem = *tmem_slot;
+  const int4 tile = g.tiles[tile_no];
+  const int run_row = g.runs[tile_no];
+  const bool live = tile_no < g.n_tiles[0];
+  const int count = tile.z, slot = tile.x;
+  // the cluster's CTAs take the column blocks in turn, so that they read neighbouring parts
+  // of the rows at the same time
+  const int kc = (a.K + kCols - 1) / kCols, nk = (kc - rankc + cluster - 1) / cluster;
+  // In's first stages are on their way before the rank is known
+  const bool run = run_row >= 0;
+  const int boxes = run ? (count + kWideRows - 1) / kWideRows : 0, first = min(stages, nk);
+  int row[4] = {0, 0, 0, 0};
+  auto load_in = [&](int s) {
+    const uint32_t st = smem_u32(smem + s % stages * S::kStageBytes);
+    const int x = (s * cluster + rankc) * kCols;
+    uint64_t* bar = &full[s % stages];
+    if (lane == 0) mbar_arrive_expect_tx(bar, run ? boxes * kWideRows * 128 : S::kInBytes);
+    __syncwarp();
+    if (!run) tma_gather4(st + 512 * lane, &args.in[blockIdx.y], x, row[0], row[1], row[2], row[3], bar);
+    else if (lane < boxes) tma_load_2d(st + 8192 * lane, &args.box[blockIdx.y], x, run_row + kWideRows * lane, bar);
+  };
+  if (warp == 0 && live) {
+    if (!run)  // lane l gathers rows 4 l .. 4 l + 3 of the tile; past its end any row will do
+#pragma unroll
+      for (int q = 0; q < 4; ++q) row[q] = g.perm[tile.y + min(4 * lane + q, count - 1)];
+    for (int s = 0; s < first; ++s) load_in(s);
+  }
+  const int r = live ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
+  if (r == 0) {  // no tile, or an empty slot's (the whole cluster): what was asked for has to land
+    if (warp == 0 && live && lane == 0)
+      for (int s = 0; s < first; ++s) {
+        mbar_arrive(&full[s]);
+        mbar_wait_bounded(&full[s], 0);
+      }
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, S::kTmem);
+    return;
+  }
   const float scale = g.scale[slot];
-  const int kc = (a.K + kCols - 1) / kCols, k_lo = kc * rankc / cluster, nk = kc * (rankc + 1) / cluster - k_lo;
 
   if (warp == 0) {
-    // lane l gathers rows 4 l .. 4 l + 3 of the tile; past its end any row will do
-    int row[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) row[q] = g.perm[tile.y + min(4 * lane + q, count - 1)];
-    const int row_a = __shfl_sync(0xffffffffu, row[0], 0), row_z = __shfl_sync(0xffffffffu, row[3], 31);
-    const bool run = row_z - row_a == count - 1;
-    const int boxes = run ? (count + kWideRows - 1) / kWideRows : 0;
-    const uint32_t bytes = (run ? boxes * kWideRows * 128 : S::kInBytes) + r16 * 128;
-    bool ok = true;
-    for (int s = 0; s < nk && ok; ++s) {
-      const int slot_s = s % S::kStages, round = s / S::kStages;
-      if (lane == 0) {
-        if (s >= S::kStages) ok = mbar_wait_bounded(&empty[slot_s], (round - 1) & 1);
-        if (ok) mbar_arrive_expect_tx(&full[slot_s], bytes);
-      }
+    auto load_p = [&](int s) {
+      uint64_t* bar = &full[s % stages];
+      if (lane == 0) mbar_arrive_expect_tx(bar, r16 * 128);
+      __syncwarp();
+      if (lane < r16 / 16)
+        tma_load_2d(smem_u32(smem + s % stages * S::kStageBytes) + S::kInBytes + 2048 * lane, &args.p[blockIdx.y],
+                    (s * cluster + rankc) * kCols, slot * g.rp + 16 * lane, bar);
+    };
+    for (int s = 0; s < first; ++s) load_p(s);
+    for (int s = first; s < nk; ++s) {
+      bool ok = true;
+      if (lane == 0) ok = mbar_wait_bounded(&empty[s % stages], (s / stages - 1) & 1);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) {
-        drain(full, S::kStages, s);
+        drain(full, stages, s);
         break;
       }
-      const uint32_t st = smem_u32(smem + slot_s * S::kStageBytes);
-      const int x = (k_lo + s) * kCols;
-      if (!run) tma_gather4(st + 512 * lane, &args.in[blockIdx.y], x, row[0], row[1], row[2], row[3], &full[slot_s]);
-      else if (lane < boxes) tma_load_2d(st + 8192 * lane, &args.box[blockIdx.y], x, row_a + kWideRows * lane, &full[slot_s]);
-      if (lane < r16 / 16)
-        tma_load_2d(st + S::kInBytes + 2048 * lane, &args.p[blockIdx.y], x, slot * g.rp + 16 * lane, &full[slot_s]);
+      load_in(s);
+      load_p(s);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       // kind::f16, A and B fp16, D fp32, K-major, M = 128 rows, N = r16
       const uint32_t idesc = (1u << 4) | ((uint32_t)(r16 >> 3) << 17) | ((uint32_t)(kTallRows >> 4) << 24);
       for (int s = 0; s < nk; ++s) {
-        const int slot_s = s % S::kStages, round = s / S::kStages;
-        if (!mbar_wait_bounded(&full[slot_s], round & 1)) break;
+        if (!mbar_wait_bounded(&full[s % stages], (s / stages) & 1)) break;
         tc_fence_after();
-        const uint32_t st = smem_u32(smem + slot_s * S::kStageBytes);
+        const uint32_t st = smem_u32(smem + s % stages * S::kStageBytes);
 #pragma unroll
         for (int j = 0; j < kCols / 16; ++j)
           mma_f16_ss(tmem, smem_desc_sw128(st + 32 * j), smem_desc_sw128(st + S::kInBytes + 32 * j), idesc, (s | j) != 0);
-        mma_commit(&empty[slot_s]);
+        mma_commit(&empty[s % stages]);
       }
-      mma_commit(accf);
+      mma_commit(&accf);
     }
   }
   __syncwarp();
   float* part = reinterpret_cast<float*>(smem);  // [128][kPitch], over the drained ring
   if (warp >= 2) {
-    const int q = warp & 3, row = 32 * q + lane;
-    const bool ok = mbar_wait_bounded(accf, 0);
+    const int q = warp & 3, tr = 32 * q + lane;
+    const bool ok = mbar_wait_bounded(&accf, 0);
     tc_fence_after();
 #pragma unroll
     for (int t = 0; t < R / 16; ++t) {
@@ -156,7 +183,7 @@ __global__ void __launch_bounds__(kTallThreads) k_contract_tall(const __grid_con
       tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + 16 * t, v);
 #pragma unroll
       for (int e = 0; e < 16; e += 4)
-        *reinterpret_cast<float4*>(part + row * S::kPitch + 16 * t + e) =
+        *reinterpret_cast<float4*>(part + tr * S::kPitch + 16 * t + e) =
             ok && nk > 0 ? make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]))
                          : make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -181,11 +208,7 @@ __global__ void __launch_bounds__(kTallThreads) k_contract_tall(const __grid_con
     mine[q] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (i >= share * quads || row >= count) continue;
     const uint32_t at = pbase + 4 * (row * S::kPitch + j);
-    float4 x = ld_peer_v4f(peer_smem(at, 0));
-    for (int c = 1; c < cluster; ++c) {
-      const float4 y = ld_peer_v4f(peer_smem(at, c));
-      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-    }
+    const float4 x = sum_peers(at, cluster);
     const float v[4] = {j < r ? x.x * scale : 0.f, j + 1 < r ? x.y * scale : 0.f, j + 2 < r ? x.z * scale : 0.f,
                         j + 3 < r ? x.w * scale : 0.f};
     mine[q] = make_float4(v[0], v[1], v[2], v[3]);
@@ -228,9 +251,200 @@ __global__ void __launch_bounds__(kTallThreads) k_contract_tall(const __grid_con
     if (i >= share * quads || (row >= kWideRows && !two)) continue;
     const float u = row < kWideRows ? unit[0] : unit[1];
     const Split s0 = split_half(mine[q].x * u), s1 = split_half(mine[q].y * u), s2 = split_half(mine[q].z * u), s3 = split_half(mine[q].w * u);
-    const size_t at = ((size_t)tile.w * kWideRows + row) * g.rp + j;
-    *reinterpret_cast<uint2*>(a.hi + at) = make_uint2(half2_bits(s0.hi, s1.hi), half2_bits(s2.hi, s3.hi));
-    *reinterpret_cast<uint2*>(a.lo + at) = make_uint2(half2_bits(s0.lo, s1.lo), half2_bits(s2.lo, s3.lo));
+    __half* at = a.parts + ((size_t)tile.w * kWideRows + row) * (2 * g.pp) + j;
+    *reinterpret_cast<uint2*>(at) = make_uint2(half2_bits(s0.hi, s1.hi), half2_bits(s2.hi, s3.hi));
+    *reinterpret_cast<uint2*>(at + g.pp) = make_uint2(half2_bits(s0.lo, s1.lo), half2_bits(s2.lo, s3.lo));
+  }
+}
+
+// ---- expansion -------------------------------------------------------------------------------
+// A CTA takes some 64-column blocks of one tile of up to 128 rows. T's parts, side by side
+// as one row of 2 R elements, are the MMA's A operand for all of them; per block r rows of
+// Q (B, MN-major, used by both parts) and the base tile (16 KB) arrive by TMA, D = T Q gets
+// one of two accumulators, and four epilogue warps (thread = row) add base, round once and
+// write the rows out by 128-byte lines. Started as the mma.sync expansion is: what was
+// there before the call is read before the wait on the contraction.
+struct TallExpandArgs {
+  CUtensorMap in, box, q, parts;  // base by single rows and by 64, Q by 16
+  RowsArgs g;
+  int stages;
+};
+
+template <int R>
+struct TallExpand {
+  static constexpr int kTChunks = R <= 32 ? 1 : R / 32, kTBytes = kTChunks * kTallRows * 128;
+  static constexpr int kBaseBytes = kTallRows * 128, kStageBytes = kBaseBytes + R * 128;
+  static constexpr int kPart = 0;
+  static constexpr int kTmem = 2 * kCols;
+};
+
+template <int R>
+__global__ void __launch_bounds__(kTallThreads) k_expand_tall(const __grid_constant__ TallExpandArgs args) {
+  using S = TallExpand<R>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* ring = smem + S::kTBytes;
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tfull, dfull[2], dempty[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int srow[kTallRows];
+  const RowsArgs& g = args.g;
+  const RowsPass& a = g.pass[0];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, stages = args.stages;
+  const int tile_no = blockIdx.y, parts = gridDim.x, b0 = blockIdx.x;
+  const bool in_place = a.base == a.out;
+  const int4 tile = g.tiles[tile_no];
+  const int run_row = g.runs[tile_no];
+  const bool live = tile_no < g.n_tiles[in_place ? 0 : 1];
+  const int count = tile.z, slot = tile.x;
+  const int r = live && slot < g.n_slots ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
+  const int blocks = (a.N + kCols - 1) / kCols, nb = (blocks - b0 + parts - 1) / parts;
+  if (r == 0) {  // no tile, or base alone
+    trigger_dependents();
+    grid_dependency_wait();
+    if (live && !in_place)
+      for (int b = b0; b < blocks; b += parts)
+        copy_rows(a, g.rows, g.perm + tile.y, count, b * (kCols / 8), min((b + 1) * (kCols / 8), a.N / 8));
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 5);  // the MMA and the four epilogue warps
+    }
+    mbar_init(&tfull, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&dfull[s], 1);
+      mbar_init(&dempty[s], 4);
+    }
+    fence_mbar_init();
+    tma_prefetch_map(&args.box);
+    tma_prefetch_map(&args.q);
+    tma_prefetch_map(&args.parts);
+  }
+  if (warp == 1) tmem_alloc(&tmem_slot, S::kTmem);
+  for (int i = threadIdx.x; i < kTallRows; i += kTallThreads) srow[i] = g.perm[tile.y + min(i, count - 1)];
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  trigger_dependents();  // not before the tensor memory is ours
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 0) {
+    const bool run = run_row >= 0;
+    const int boxes = run ? (count + kWideRows - 1) / kWideRows : 0;
+    const uint32_t base_bytes = a.base == nullptr ? 0 : run ? boxes * kWideRows * 128 : S::kBaseBytes;
+    auto load = [&](int i) {
+      const uint32_t st = smem_u32(ring + i % stages * S::kStageBytes);
+      const int x = (b0 + i * parts) * kCols;
+      uint64_t* bar = &full[i % stages];
+      if (lane == 0) mbar_arrive_expect_tx(bar, base_bytes + r16 * 128);
+      __syncwarp();
+      if (lane < r16 / 16) tma_load_2d(st + S::kBaseBytes + 2048 * lane, &args.q, x, slot * g.rp + 16 * lane, bar);
+      if (a.base) {
+        if (!run) tma_gather4(st + 512 * lane, &args.in, x, srow[4 * lane], srow[4 * lane + 1], srow[4 * lane + 2], srow[4 * lane + 3], bar);
+        else if (lane < boxes) tma_load_2d(st + 8192 * lane, &args.box, x, run_row + kWideRows * lane, bar);
+      }
+    };
+    const int first = min(stages, nb);
+    for (int i = 0; i < first; ++i) load(i);
+    grid_dependency_wait();
+    {  // T: chunks of 64 of a row's 2 R elements, 64 rows a box; past the tile's rows whatever is there
+      const int half = S::kTChunks / 2, used = R <= 64 ? S::kTChunks : r16 > 64 ? 4 : 2;
+      if (lane == 0) mbar_arrive_expect_tx(&tfull, used * kTallRows * 128);
+      __syncwarp();
+      if (lane < 2 * used) {
+        const int u = lane >> 1, c = R > 64 && used == 2 ? u * half : u;
+        tma_load_2d(smem_u32(smem) + 16384 * c + 8192 * (lane & 1), &args.parts, 64 * c, (tile.w + (lane & 1)) * kWideRows, &tfull);
+      }
+    }
+    for (int i = first; i < nb; ++i) {
+      bool ok = true;
+      if (lane == 0) ok = mbar_wait_bounded(&empty[i % stages], (i / stages - 1) & 1);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) {
+        drain(full, stages, i);
+        break;
+      }
+      load(i);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // kind::f16, A (K-major) and B (MN-major) fp16, D fp32, M = 128 rows, N = 64 columns
+      const uint32_t idesc = (1u << 4) | (1u << 16) | ((uint32_t)(kCols >> 3) << 17) | ((uint32_t)(kTallRows >> 4) << 24);
+      const uint32_t ta = smem_u32(smem);
+      const bool there = mbar_wait_bounded(&tfull, 0);
+      for (int i = 0; i < nb && there; ++i) {
+        const int st_no = i % stages, d = i & 1;
+        if (i >= 2 && !mbar_wait_bounded(&dempty[d], (i / 2 - 1) & 1)) break;
+        if (!mbar_wait_bounded(&full[st_no], (i / stages) & 1)) break;
+        tc_fence_after();
+        const uint32_t q = smem_u32(ring + st_no * S::kStageBytes) + S::kBaseBytes;
+#pragma unroll
+        for (int pt = 1; pt >= 0; --pt)  // the low part first
+#pragma unroll
+          for (int j = 0; j < R / 16; ++j) {
+            if (16 * j >= r16) break;
+            const int e = pt * R + 16 * j;  // first of the 16 elements of T's row
+            mma_f16_ss(tmem + d * kCols, smem_desc_sw128(ta + e / 64 * 16384 + e % 64 * 2), smem_desc_mn_sw128(q + 2048 * j), idesc,
+                       pt == 0 || j != 0);
+          }
+        mma_commit(&empty[st_no]);
+        mma_commit(&dfull[d]);
+      }
+    }
+  }
+  __syncwarp();
+  if (warp >= 2) {
+    grid_dependency_wait();  // the units are the contraction's, and it may still read what out replaces
+    const int q = warp & 3, tr = 32 * q + lane;
+    const float back = a.unit[tile.w + (tr >= kWideRows && count > kWideRows ? 1 : 0)];
+    for (int i = 0; i < nb; ++i) {
+      const int st_no = i % stages;
+      const uint32_t st = smem_u32(ring + st_no * S::kStageBytes);
+      if (!mbar_wait_bounded(&full[st_no], (i / stages) & 1) || !mbar_wait_bounded(&dfull[i & 1], (i / 2) & 1)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t v[32];
+        tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (i & 1) * kCols + 32 * h, v);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t at = st + tr * 128 + 16 * ((4 * h + c) ^ (tr & 7));
+          const uint4 b = a.base ? lds_u32x4(at) : make_uint4(0, 0, 0, 0);
+          const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&bw[e]));
+            const __half2 x = __floats2half2_rn(fmaf(__uint_as_float(v[8 * c + 2 * e]), back, f.x), fmaf(__uint_as_float(v[8 * c + 2 * e + 1]), back, f.y));
+            o[e] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          sts_v4(at, o[0], o[1], o[2], o[3]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dempty[i & 1]);
+      // the warp's own 32 rows, eight lanes a line
+      const int c = (b0 + i * parts) * kCols + 8 * (lane & 7);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int row = 32 * q + 4 * k + (lane >> 3);
+        if (row < count && c < a.N)
+          *reinterpret_cast<uint4*>(a.out + (size_t)srow[row] * a.N + c) = lds_u32x4(st + row * 128 + 16 * ((lane & 7) ^ (row & 7)));
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before TMA writes the stage again
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st_no]);
+    }
+  } else {
+    grid_dependency_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kTmem);
   }
 }
 
@@ -242,19 +456,19 @@ __global__ void __launch_bounds__(kTallThreads) k_contract_tall(const __grid_con
 // fp32 sums in registers (thread = column): a long sum is rounded to nearest once a tile.
 // A cluster splits the tiles and sums through distributed shared memory in rank order.
 struct TallGradArgs {
-  CUtensorMap in[2], box[2], part[2][2];
+  CUtensorMap in[2], box[2], parts[2];
   GradArgs g;
+  int stages;
 };
 
 template <int R>
 struct TallGrad {
   static constexpr int kInBytes = 2 * kWideRows * 128;  // two chunks of 64 columns
-  static constexpr int kTChunks = R > 64 ? 2 : 1, kTBytes = kTChunks * kWideRows * 128;
-  static constexpr int kStageBytes = kInBytes + 2 * kTBytes;
-  static constexpr int kStages = 3;
-  static constexpr int kRing = kStages * kStageBytes;
-  static_assert(R * kGradCols * 4 <= kRing, "the partial sums lie over the drained ring");
-  static constexpr int smem = kRing + 1024 + 256;
+  // 64-element chunks of T's rows [high R | low R]: both parts in one, or one or two each
+  static constexpr int kTChunks = R <= 32 ? 1 : R / 32, kTBytes = kTChunks * kWideRows * 128;
+  static constexpr int kLow = R <= 32 ? 2 * R : kTBytes / 2;  // bytes from the high part to the low
+  static constexpr int kStageBytes = kInBytes + kTBytes;
+  static constexpr int kPart = R * kGradCols * 4;  // the partial sums lie over the drained ring
   static constexpr int kTmem = 2 * R;
 };
 
@@ -263,13 +477,10 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
   using S = TallGrad<R>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kRing);
-  uint64_t* empty = full + S::kStages;
-  uint64_t* dfull = empty + S::kStages;
-  uint64_t* dempty = dfull + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dempty + 2);
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], dfull[2], dempty[2];
+  __shared__ uint32_t tmem_slot;
   const GradArgs& g = args.g;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, stages = args.stages;
   const int split = blockIdx.z, nsplit = gridDim.z, slot = blockIdx.y;
   const int which = (int)blockIdx.x < g.pass[0].blocks ? 0 : 1;
   const GradPass& a = g.pass[which];
@@ -291,7 +502,7 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
   const int nt_all = (rows + kWideRows - 1) / kWideRows, t_lo = (int)((long)nt_all * split / nsplit);
   const int nt = (int)((long)nt_all * (split + 1) / nsplit) - t_lo;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::kStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -300,49 +511,46 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
       mbar_init(&dempty[s], 4);
     }
     fence_mbar_init();
+    tma_prefetch_map(&args.box[which]);
+    tma_prefetch_map(&args.parts[which]);
   }
-  if (warp == 1) tmem_alloc(tmem_slot, S::kTmem);
+  if (warp == 1) tmem_alloc(&tmem_slot, S::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   trigger_dependents();  // not before the tensor memory is ours
-  const uint32_t tmem = *tmem_slot;
-  const int tch = r16 > 64 ? 2 : 1;  // 64-rank chunks of T
+  const uint32_t tmem = tmem_slot;
 
   if (warp == 0) {
-    const uint32_t bytes = S::kInBytes + 2 * tch * kWideRows * 128;
+    const int half = S::kTChunks / 2, used = R <= 64 ? S::kTChunks : r16 > 64 ? 4 : 2;  // chunks with ranks in them
+    const uint32_t bytes = S::kInBytes + used * kWideRows * 128;
     const int chunk = lane >> 4, r4 = 4 * (lane & 15);  // this lane's chunk and first row of a tile
     const int x = col0 + 64 * chunk < a.K ? col0 + 64 * chunk : col0;  // past the end any columns will do
     // In's part of stage s: a whole tile of rows in a run as two boxes. Rows past the slot's
     // end must not be others' (0 * inf): the ragged tile gathers, repeating its last row (T
-    // is zero there). A tile's first and last row numbers are loaded one stage ahead.
-    int row_a = 0, row_z = 0;
-    auto ends = [&](int s) {
-      const int at = p0 + (t_lo + s) * kWideRows;
-      row_a = s < nt ? g.perm[at] : 0;
-      row_z = s < nt ? g.perm[min(at + kWideRows, p0 + rows) - 1] : 0;
-    };
-    ends(0);
+    // is zero there). Whether a tile is a run is loaded one stage ahead.
+    int next = nt > 0 ? g.runs[tile0 + t_lo] : -1;
     auto gather = [&](int s) {
-      const uint32_t st = smem_u32(smem + s % S::kStages * S::kStageBytes);
-      if (row_z - row_a == kWideRows - 1) {
-        if (lane < 2) tma_load_2d(st + 8192 * lane, &args.box[which], col0 + 64 * lane < a.K ? col0 + 64 * lane : col0, row_a, &full[s % S::kStages]);
+      const uint32_t st = smem_u32(smem + s % stages * S::kStageBytes);
+      const int row_a = next;
+      if (row_a >= 0 && rows - (t_lo + s) * kWideRows >= kWideRows) {
+        if (lane < 2) tma_load_2d(st + 8192 * lane, &args.box[which], col0 + 64 * lane < a.K ? col0 + 64 * lane : col0, row_a, &full[s % stages]);
       } else {
         int row[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) row[q] = g.perm[p0 + min((t_lo + s) * kWideRows + r4 + q, rows - 1)];
-        tma_gather4(st + 8192 * chunk + 128 * r4, &args.in[which], x, row[0], row[1], row[2], row[3], &full[s % S::kStages]);
+        tma_gather4(st + 8192 * chunk + 128 * r4, &args.in[which], x, row[0], row[1], row[2], row[3], &full[s % stages]);
       }
-      ends(s + 1);
+      next = s + 1 < nt ? g.runs[tile0 + t_lo + s + 1] : -1;
     };
-    auto parts = [&](int s) {  // T's part: lane = (part, chunk)
-      if (lane < 2 * tch) {
-        const int pt = lane / tch, c = lane % tch;
-        tma_load_2d(smem_u32(smem + s % S::kStages * S::kStageBytes) + S::kInBytes + pt * S::kTBytes + 8192 * c,
-                    &args.part[which][pt], 64 * c, (tile0 + t_lo + s) * kWideRows, &full[s % S::kStages]);
+    auto parts = [&](int s) {
+      if (lane < used) {
+        const int c = R > 64 && used == 2 ? lane * half : lane;  // the first chunk of each part, or all
+        tma_load_2d(smem_u32(smem + s % stages * S::kStageBytes) + S::kInBytes + 8192 * c, &args.parts[which], 64 * c,
+                    (tile0 + t_lo + s) * kWideRows, &full[s % stages]);
       }
     };
-    const int first = min(nt, S::kStages);
+    const int first = min(nt, stages);
     for (int s = 0; s < first; ++s) {
       if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
       __syncwarp();
@@ -353,12 +561,12 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
     for (int s = first; s < nt; ++s) {
       bool ok = true;
       if (lane == 0) {
-        ok = mbar_wait_bounded(&empty[s % S::kStages], (s / S::kStages - 1) & 1);
-        if (ok) mbar_arrive_expect_tx(&full[s % S::kStages], bytes);
+        ok = mbar_wait_bounded(&empty[s % stages], (s / stages - 1) & 1);
+        if (ok) mbar_arrive_expect_tx(&full[s % stages], bytes);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) {
-        drain(full, S::kStages, s);
+        drain(full, stages, s);
         break;
       }
       gather(s);
@@ -369,16 +577,16 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
       // kind::f16, A and B fp16 and MN-major, D fp32, M = 128 columns, N = r16
       const uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(r16 >> 3) << 17) | ((uint32_t)(kGradCols >> 4) << 24);
       for (int s = 0; s < nt; ++s) {
-        const int st_no = s % S::kStages, d = s & 1;
+        const int st_no = s % stages, d = s & 1;
         if (s >= 2 && !mbar_wait_bounded(&dempty[d], (s / 2 - 1) & 1)) break;
-        if (!mbar_wait_bounded(&full[st_no], (s / S::kStages) & 1)) break;
+        if (!mbar_wait_bounded(&full[st_no], (s / stages) & 1)) break;
         tc_fence_after();
         const uint32_t st = smem_u32(smem + st_no * S::kStageBytes), tp = st + S::kInBytes;
 #pragma unroll
         for (int pt = 1; pt >= 0; --pt)  // the low part first
 #pragma unroll
           for (int j = 0; j < kWideRows / 16; ++j)
-            mma_f16_ss(tmem + d * R, smem_desc_mn_sw128(st + 2048 * j), smem_desc_mn_sw128(tp + pt * S::kTBytes + 2048 * j), idesc,
+            mma_f16_ss(tmem + d * R, smem_desc_mn_sw128(st + 2048 * j), smem_desc_mn_sw128(tp + pt * S::kLow + 2048 * j), idesc,
                        pt == 0 || j != 0);
         mma_commit(&empty[st_no]);
         mma_commit(&dfull[d]);
@@ -393,8 +601,10 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
     float sum[R];
 #pragma unroll
     for (int j = 0; j < R; ++j) sum[j] = 0.f;
+    float next = nt > 0 ? a.unit[tile0 + t_lo] : 0.f;
     for (int s = 0; s < nt; ++s) {
-      const float unit = a.unit[tile0 + t_lo + s];
+      const float unit = next;
+      if (s + 1 < nt) next = a.unit[tile0 + t_lo + s + 1];
       if (!mbar_wait_bounded(&dfull[s & 1], (s / 2) & 1)) break;
       tc_fence_after();
 #pragma unroll
@@ -495,11 +705,32 @@ cudaError_t encode_rows(CUtensorMap* single, CUtensorMap* box, const __half* x, 
                          CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Stages of a ring, and the shared memory it takes: what an SM holds, shared by the CTAs
+// that run on it, since a load takes some 2 us and every stage in flight counts; no more
+// than there is work for, no less than the partial sums need.
+constexpr int kSmPerSm = 216 * 1024, kTallSlack = 1024 + 1024;  // alignment, static shared memory
+struct Ring {
+  int stages, smem;
+};
+Ring plan_ring(int stage_bytes, int part_bytes, int fixed_bytes, int work, int share) {
+  Ring r;
+  const int room = (kSmPerSm / share - kTallSlack - fixed_bytes) / stage_bytes;
+  r.stages = std::min({kMaxStages, std::max(1, work), std::max(2, room)});
+  r.stages = std::max(r.stages, (part_bytes + stage_bytes - 1) / stage_bytes);
+  r.smem = r.stages * stage_bytes + fixed_bytes + 1024;
+  return r;
+}
+// CTAs of an SM: two (clusters of eight with one an SM leave SMs idle: 16 of them fit a
+// GPU of 148), or three where there are more than two anyway.
+int sm_share(long ctas, int n_sm) { return ctas > 2l * n_sm ? 3 : 2; }
+
 template <int R>
 cudaError_t allow_tall() {
-  const cudaError_t e = cudaFuncSetAttribute(k_contract_tall<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, TallContract<R>::smem);
+  const int most = kSmPerSm - 1024;
+  cudaError_t e = cudaFuncSetAttribute(k_contract_tall<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(k_grad_tall<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, TallGrad<R>::smem);
+  if ((e = cudaFuncSetAttribute(k_expand_tall<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, most))) return e;
+  return cudaFuncSetAttribute(k_grad_tall<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
 }
 
 }  // namespace
@@ -520,21 +751,25 @@ cudaError_t encode_adapter_maps(dictproj_adapters* a) {
                            kCols, 16, CU_TENSOR_MAP_SWIZZLE_128B)))
     return e;
   for (int i = 0; i < 2; ++i)
-    for (int p = 0; p < 2; ++p)
-      if ((e = encode_tiled_2d(&a->part_map[i][p], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a->part[i][p], (uint64_t)a->rp, rows,
-                               (uint64_t)a->rp * 2, 64, kWideRows, CU_TENSOR_MAP_SWIZZLE_128B)))
-        return e;
+    if ((e = encode_tiled_2d(&a->part_map[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a->parts[i], (uint64_t)2 * a->pp, rows,
+                             (uint64_t)4 * a->pp, 64, kWideRows, CU_TENSOR_MAP_SWIZZLE_128B)))
+      return e;
   return cudaSuccess;
 }
 
 // Rows that TMA can read, and enough of them to fill 128-row tiles.
 bool tall_serves(const dictproj_adapters* a, const dictproj_rows* r) { return a->d_out % 8 == 0 && r->M >= 256; }
 
-#define DICTPROJ_TALL(rp, kernel, shape)                                             \
-  ((rp) <= 16 ? std::make_pair((const void*)kernel<16>, (int)shape<16>::smem)        \
-   : (rp) <= 32 ? std::make_pair((const void*)kernel<32>, (int)shape<32>::smem)      \
-   : (rp) <= 64 ? std::make_pair((const void*)kernel<64>, (int)shape<64>::smem)      \
-                : std::make_pair((const void*)kernel<128>, (int)shape<128>::smem))
+struct TallKernel {
+  const void* fn;
+  int stage_bytes, part_bytes;
+};
+#define DICTPROJ_TALL_R(kernel, shape, R) TallKernel{(const void*)kernel<R>, shape<R>::kStageBytes, shape<R>::kPart}
+#define DICTPROJ_TALL(rp, kernel, shape)                  \
+  ((rp) <= 16   ? DICTPROJ_TALL_R(kernel, shape, 16)      \
+   : (rp) <= 32 ? DICTPROJ_TALL_R(kernel, shape, 32)      \
+   : (rp) <= 64 ? DICTPROJ_TALL_R(kernel, shape, 64)      \
+                : DICTPROJ_TALL_R(kernel, shape, 128))
 
 cudaError_t launch_contract_tall(RowsArgs& g, int passes, const dictproj_adapters* a, const dictproj_rows* r,
                                  cudaStream_t stream) {
@@ -547,13 +782,53 @@ cudaError_t launch_contract_tall(RowsArgs& g, int passes, const dictproj_adapter
   args.g = g;
   args.g.tiles = r->tiles[2];
   args.g.n_tiles = r->n_tiles + 4;
+  args.g.runs = r->runs[1];
   const int full = std::max(1, r->M / kTallRows) * passes;  // tiles that do exist, about
   args.g.cluster = 2;
-  while (args.g.cluster < 8 && full * args.g.cluster < 2 * a->n_sm) args.g.cluster *= 2;
-  const auto k = DICTPROJ_TALL(g.rp, k_contract_tall, TallContract);
+  while (args.g.cluster < 8 && full * args.g.cluster < 3 * a->n_sm / 2) args.g.cluster *= 2;
+  const TallKernel k = DICTPROJ_TALL(g.rp, k_contract_tall, TallContract);
+  const int kc = (std::max(g.pass[0].K, g.pass[passes - 1].K) + kCols - 1) / kCols;
+  const Ring ring = plan_ring(k.stage_bytes, k.part_bytes, 0, (kc + args.g.cluster - 1) / args.g.cluster,
+                              sm_share((long)full * args.g.cluster, a->n_sm));
+  args.stages = ring.stages;
   void* p[] = {(void*)&args};
-  return launch_pdl_cluster(k.first, dim3((unsigned)(adapter_tiles(r->M, r->n_slots, kTallRows) * args.g.cluster), passes), k.second,
+  return launch_pdl_cluster(k.fn, dim3((unsigned)(adapter_tiles(r->M, r->n_slots, kTallRows) * args.g.cluster), passes), ring.smem,
                             stream, p, dim3(args.g.cluster, 1, 1));
+}
+
+cudaError_t launch_expand_tall(const RowsArgs& g, const dictproj_adapters* a, const dictproj_rows* r, cudaStream_t stream) {
+  TallExpandArgs args;
+  const RowsPass& p = g.pass[0];
+  // without a base its maps are not used; out stands in for them
+  cudaError_t e = encode_rows(&args.in, &args.box, p.base ? p.base : p.out, p.N, r->M);
+  if (e != cudaSuccess) return e;
+  args.q = reinterpret_cast<const uint16_t*>(p.Q) == a->A ? a->a_map : a->b_map;
+  args.parts = a->part_map[0];
+  args.g = g;
+  args.g.tiles = r->tiles[2];
+  args.g.n_tiles = r->n_tiles + 4;
+  args.g.runs = r->runs[1];
+  const TallKernel k = DICTPROJ_TALL(g.rp, k_expand_tall, TallExpand);
+  const int fixed = (g.rp <= 32 ? 1 : a->pp / 32) * kTallRows * 128, blocks = (p.N + kCols - 1) / kCols;
+  const int share = g.rp <= 64 ? 2 : 1, full = std::max(1, r->M / kTallRows);  // tiles that do exist, about
+  const int parts = std::min(blocks, std::max(1, share * a->n_sm / full));  // as many CTAs as run at once
+  const Ring ring = plan_ring(k.stage_bytes, 0, fixed, (blocks + parts - 1) / parts, share);
+  args.stages = ring.stages;
+  void* pp[] = {(void*)&args};
+  return launch_pdl_cluster(k.fn, dim3(parts, adapter_tiles(r->M, r->n_slots, kTallRows)), ring.smem, stream, pp, dim3(1, 1, 1));
+}
+
+// CTAs that the tiles of a gradient are split over: with `at_once` CTAs running, each is as
+// long as its tiles and a fixed part (set-up, first loads, cluster sum) worth about eight.
+static int grad_split(int blocks, int tiles, int at_once) {
+  int best = 1;
+  double cost = 1e30;
+  for (int s = 1; s <= 8 && (s == 1 || s <= tiles); s *= 2) {
+    const double w = (double)blocks * s / at_once;  // between whole waves and none
+    const double c = std::max(1.0, 0.5 * (w + std::ceil(w))) * ((tiles + s - 1) / s + 8);
+    if (c < cost) cost = c, best = s;
+  }
+  return best;
 }
 
 cudaError_t launch_grad_tall(const GradArgs& w, const dictproj_adapters* a, const dictproj_rows* r, cudaStream_t stream) {
@@ -561,15 +836,17 @@ cudaError_t launch_grad_tall(const GradArgs& w, const dictproj_adapters* a, cons
   cudaError_t e;
   for (int i = 0; i < 2; ++i) {
     if ((e = encode_rows(&args.in[i], &args.box[i], w.pass[i].in, w.pass[i].K, r->M)) != cudaSuccess) return e;
-    for (int p = 0; p < 2; ++p) args.part[i][p] = a->part_map[i][p];
+    args.parts[i] = a->part_map[i];
   }
   args.g = w;
   const int blocks = w.pass[0].blocks + w.pass[1].blocks;
-  int split = 1;
-  while (split < 8 && blocks * a->n_slots * split < 2 * a->n_sm && kWideRows * a->n_slots * split < r->M) split *= 2;
-  const auto k = DICTPROJ_TALL(w.rp, k_grad_tall, TallGrad);
+  const int split = grad_split(blocks * a->n_slots, r->M / (kWideRows * a->n_slots), a->n_sm * (w.rp <= 32 ? 3 : w.rp <= 64 ? 2 : 1));
+  const TallKernel k = DICTPROJ_TALL(w.rp, k_grad_tall, TallGrad);
+  const int tiles = (r->M / (kWideRows * a->n_slots) + split) / split;
+  const Ring ring = plan_ring(k.stage_bytes, k.part_bytes, 0, tiles, sm_share((long)blocks * a->n_slots * split, a->n_sm));
+  args.stages = ring.stages;
   void* p[] = {(void*)&args};
-  return launch_pdl_cluster(k.first, dim3(blocks, a->n_slots, split), k.second, stream, p, dim3(1, 1, split));
+  return launch_pdl_cluster(k.fn, dim3(blocks, a->n_slots, split), ring.smem, stream, p, dim3(1, 1, split));
 }
 
 cudaError_t launch_wait_probe_tall(long long cycles, cudaStream_t stream) {

@@ -119,10 +119,11 @@ struct dictproj_adapters {
   float* scale;            // [n_slots]
   // batches of many rows: scale * T (forward), or scale * U (index 0) and scale * T (1) of
   // the backward pass, as two fp16 parts times a power of two per 64-row tile (adapter.cuh)
-  uint16_t* part[2][2];    // [pass][high, low] fp16 [adapter_tiles(64)][64][rp]
+  int pp;                  // ranks of a part's row: rp rounded up to 16, 32, 64 or 128
+  uint16_t* parts[2];      // [pass] fp16 [adapter_tiles(64)][64][high pp | low pp]
   float* unit[2];          // [pass] what a tile's parts are multiplied with, [adapter_tiles(64)]
   CUtensorMap a_map, b_map;      // A and B as [n_slots * rp] rows, box 64 columns x 16 rows
-  CUtensorMap part_map[2][2];    // the parts as rows of rp, box 64 columns x 64 rows
+  CUtensorMap part_map[2];       // the parts, box 64 columns x 64 rows
 };
 
 // Most tiles of `rows` rows that M rows over n_slots slots (and no slot) can form.
@@ -142,6 +143,7 @@ struct dictproj_rows {
   // of rows without an adapter (slot n_slots) come last
   int* n_tiles;            // [3][2] tiles of the slots, all tiles
   int4* tiles[3];          // {slot, first position, rows, row number of the first (2: its first 64-row tile)}
+  int* runs[2];            // of the 64- and 128-row tiles: the first row where a tile's rows follow one another, else -1
   int* first64;            // [n_slots] first 64-row tile of each slot
 };
 

@@ -135,6 +135,8 @@ struct RowsArgs;
 struct GradArgs;
 cudaError_t launch_contract_tall(RowsArgs& g, int passes, const dictproj_adapters* a, const dictproj_rows* r,
                                  cudaStream_t stream);
+cudaError_t launch_expand_tall(const RowsArgs& g, const dictproj_adapters* a, const dictproj_rows* r,
+                               cudaStream_t stream);
 cudaError_t launch_grad_tall(const GradArgs& w, const dictproj_adapters* a, const dictproj_rows* r,
                              cudaStream_t stream);
 cudaError_t take_tall_error(unsigned int* out);

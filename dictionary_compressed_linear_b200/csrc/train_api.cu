@@ -95,6 +95,7 @@ int dictproj_adapters_create(int d_in, int d_out, int max_rank, int n_slots, int
   a->n_slots = n_slots;
   a->max_tokens = max_tokens;
   a->rp = (max_rank + 15) / 16 * 16;
+  a->pp = a->rp <= 16 ? 16 : a->rp <= 32 ? 32 : a->rp <= 64 ? 64 : 128;
   a->ld_b = (d_out + 7) / 8 * 8;
   cudaError_t e = cudaDeviceGetAttribute(&a->n_sm, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) {
@@ -102,11 +103,10 @@ int dictproj_adapters_create(int d_in, int d_out, int max_rank, int n_slots, int
     return cuda_fail(e, "adapters_create: SM count");
   }
   const size_t ab = (size_t)n_slots * a->rp * d_in * 2, bb = (size_t)n_slots * a->rp * a->ld_b * 2;
-  const size_t t64 = (size_t)adapter_tiles(max_tokens, n_slots, 64), pb = t64 * 64 * a->rp * 2, ub = t64 * sizeof(float);
+  const size_t t64 = (size_t)adapter_tiles(max_tokens, n_slots, 64), pb = t64 * 64 * a->pp * 4, ub = t64 * sizeof(float);
   if ((e = dmalloc((void**)&a->A, ab)) || (e = dmalloc((void**)&a->B, bb)) ||
       (e = dmalloc((void**)&a->rank, (size_t)n_slots * 4)) || (e = dmalloc((void**)&a->scale, (size_t)n_slots * 4)) ||
-      (e = dmalloc((void**)&a->part[0][0], pb)) || (e = dmalloc((void**)&a->part[0][1], pb)) ||
-      (e = dmalloc((void**)&a->part[1][0], pb)) || (e = dmalloc((void**)&a->part[1][1], pb)) ||
+      (e = dmalloc((void**)&a->parts[0], pb)) || (e = dmalloc((void**)&a->parts[1], pb)) ||
       (e = dmalloc((void**)&a->unit[0], ub)) || (e = dmalloc((void**)&a->unit[1], ub))) {
     dictproj_free_adapters(a);
     cudaGetLastError();
@@ -134,8 +134,7 @@ void dictproj_free_adapters(dictproj_adapters* a) {
   cudaFree(a->rank);
   cudaFree(a->scale);
   for (int i = 0; i < 2; ++i) {
-    cudaFree(a->part[i][0]);
-    cudaFree(a->part[i][1]);
+    cudaFree(a->parts[i]);
     cudaFree(a->unit[i]);
   }
   delete a;
@@ -190,6 +189,8 @@ int dictproj_rows_create(int max_rows, int n_slots, dictproj_rows** out) {
       (e = dmalloc((void**)&r->n_tiles, 6 * sizeof(int))) || (e = dmalloc((void**)&r->first64, (size_t)n_slots * 4)) ||
       (e = dmalloc((void**)&r->tiles[0], (size_t)adapter_tiles(max_rows, n_slots, 4) * sizeof(int4))) ||
       (e = dmalloc((void**)&r->tiles[1], (size_t)adapter_tiles(max_rows, n_slots, 64) * sizeof(int4))) ||
+      (e = dmalloc((void**)&r->runs[0], (size_t)adapter_tiles(max_rows, n_slots, 64) * sizeof(int))) ||
+      (e = dmalloc((void**)&r->runs[1], (size_t)adapter_tiles(max_rows, n_slots, 128) * sizeof(int))) ||
       (e = dmalloc((void**)&r->tiles[2], (size_t)adapter_tiles(max_rows, n_slots, 128) * sizeof(int4)))) {
     dictproj_free_rows(r);
     cudaGetLastError();
@@ -208,6 +209,8 @@ void dictproj_free_rows(dictproj_rows* r) {
   cudaFree(r->tiles[0]);
   cudaFree(r->tiles[1]);
   cudaFree(r->tiles[2]);
+  cudaFree(r->runs[0]);
+  cudaFree(r->runs[1]);
   delete r;
 }
 
