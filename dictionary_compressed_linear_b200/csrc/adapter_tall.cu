@@ -32,10 +32,24 @@ namespace dictproj {
 namespace {
 
 constexpr int kTallThreads = 192;  // warp 0 TMA, warp 1 MMA + tensor memory, warps 2..5 epilogue
+constexpr int kExpandThreads = 320;  // the expansion: eight epilogue warps, 2..9
 constexpr int kCols = 64;          // columns of a stage (one 128-byte swizzle row)
 
 // First 1024-byte boundary (swizzled operand tiles start on one).
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) { return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u); }
+
+// A ring position that advances without a division (the MMA thread's own instructions are
+// what a stage of few columns takes: descriptors built anew for each MMA and s % stages
+// took 1100 of 1440 cycles of a gradient's tile).
+struct RingPos {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++slot == stages) slot = 0, phase ^= 1;
+  }
+};
+// Operand descriptors hold the address / 16 in their low bits: a step of `bytes` on.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 
 // A producer that gives up first waits (bounded) for the copies it has in flight, those of
 // the last stages before stage s.
@@ -158,14 +172,17 @@ __global__ void __launch_bounds__(kTallThreads) k_contract_tall(const __grid_con
     if (lane == 0) {
       // kind::f16, A and B fp16, D fp32, K-major, M = 128 rows, N = r16
       const uint32_t idesc = (1u << 4) | ((uint32_t)(r16 >> 3) << 17) | ((uint32_t)(kTallRows >> 4) << 24);
-      for (int s = 0; s < nk; ++s) {
-        if (!mbar_wait_bounded(&full[s % stages], (s / stages) & 1)) break;
+      const uint64_t in0 = smem_desc_sw128(smem_u32(smem)), p0 = smem_desc_sw128(smem_u32(smem) + S::kInBytes);
+      RingPos at;
+      for (int s = 0; s < nk; ++s, at.next(stages)) {
+        if (!mbar_wait_bounded(&full[at.slot], at.phase)) break;
         tc_fence_after();
-        const uint32_t st = smem_u32(smem + s % stages * S::kStageBytes);
+        const uint32_t off = at.slot * S::kStageBytes;
+        const uint64_t in = desc_at(in0, off), pd = desc_at(p0, off);
 #pragma unroll
         for (int j = 0; j < kCols / 16; ++j)
-          mma_f16_ss(tmem, smem_desc_sw128(st + 32 * j), smem_desc_sw128(st + S::kInBytes + 32 * j), idesc, (s | j) != 0);
-        mma_commit(&empty[s % stages]);
+          mma_f16_ss(tmem, desc_at(in, 32 * j), desc_at(pd, 32 * j), idesc, (s | j) != 0);
+        mma_commit(&empty[at.slot]);
       }
       mma_commit(&accf);
     }
@@ -261,8 +278,9 @@ __global__ void __launch_bounds__(kTallThreads) k_contract_tall(const __grid_con
 // A CTA takes some 64-column blocks of one tile of up to 128 rows. T's parts, side by side
 // as one row of 2 R elements, are the MMA's A operand for all of them; per block r rows of
 // Q (B, MN-major, used by both parts) and the base tile (16 KB) arrive by TMA, D = T Q gets
-// one of two accumulators, and four epilogue warps (thread = row) add base, round once and
-// write the rows out by 128-byte lines. Started as the mma.sync expansion is: what was
+// one of two accumulators, and eight epilogue warps (thread = 32 columns of a row) add base,
+// round once and write the rows out. (Four warps took 1 us a block and were what 2048 rows
+// waited for.) Started as the mma.sync expansion is: what was
 // there before the call is read before the wait on the contraction.
 struct TallExpandArgs {
   CUtensorMap in, box, q, parts;  // base by single rows and by 64, Q by 16
@@ -274,16 +292,16 @@ template <int R>
 struct TallExpand {
   static constexpr int kTChunks = R <= 32 ? 1 : R / 32, kTBytes = kTChunks * kTallRows * 128;
   static constexpr int kBaseBytes = kTallRows * 128, kStageBytes = kBaseBytes + R * 128;
-  static constexpr int kPart = 0;
+  static constexpr int kPart = 0, kOutBytes = 8 * 2048;  // a warp's 32 rows of 32 columns on their way out
   static constexpr int kTmem = 2 * kCols;
 };
 
 template <int R>
-__global__ void __launch_bounds__(kTallThreads) k_expand_tall(const __grid_constant__ TallExpandArgs args) {
+__global__ void __launch_bounds__(kExpandThreads) k_expand_tall(const __grid_constant__ TallExpandArgs args) {
   using S = TallExpand<R>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  uint8_t* ring = smem + S::kTBytes;
+  uint8_t* ring = smem + S::kTBytes + S::kOutBytes;
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tfull, dfull[2], dempty[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int srow[kTallRows];
@@ -309,12 +327,12 @@ __global__ void __launch_bounds__(kTallThreads) k_expand_tall(const __grid_const
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 5);  // the MMA and the four epilogue warps
+      mbar_init(&empty[s], 9);  // the MMA and the eight epilogue warps
     }
     mbar_init(&tfull, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&dfull[s], 1);
-      mbar_init(&dempty[s], 4);
+      mbar_init(&dempty[s], 8);
     }
     fence_mbar_init();
     tma_prefetch_map(&args.box);
@@ -322,7 +340,7 @@ __global__ void __launch_bounds__(kTallThreads) k_expand_tall(const __grid_const
     tma_prefetch_map(&args.parts);
   }
   if (warp == 1) tmem_alloc(&tmem_slot, S::kTmem);
-  for (int i = threadIdx.x; i < kTallRows; i += kTallThreads) srow[i] = g.perm[tile.y + min(i, count - 1)];
+  for (int i = threadIdx.x; i < kTallRows; i += kExpandThreads) srow[i] = g.perm[tile.y + min(i, count - 1)];
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -371,24 +389,24 @@ __global__ void __launch_bounds__(kTallThreads) k_expand_tall(const __grid_const
     if (lane == 0) {
       // kind::f16, A (K-major) and B (MN-major) fp16, D fp32, M = 128 rows, N = 64 columns
       const uint32_t idesc = (1u << 4) | (1u << 16) | ((uint32_t)(kCols >> 3) << 17) | ((uint32_t)(kTallRows >> 4) << 24);
-      const uint32_t ta = smem_u32(smem);
+      const uint64_t ta = smem_desc_sw128(smem_u32(smem)), q0 = smem_desc_mn_sw128(smem_u32(ring) + S::kBaseBytes);
       const bool there = mbar_wait_bounded(&tfull, 0);
-      for (int i = 0; i < nb && there; ++i) {
-        const int st_no = i % stages, d = i & 1;
+      RingPos at;
+      for (int i = 0; i < nb && there; ++i, at.next(stages)) {
+        const int d = i & 1;
         if (i >= 2 && !mbar_wait_bounded(&dempty[d], (i / 2 - 1) & 1)) break;
-        if (!mbar_wait_bounded(&full[st_no], (i / stages) & 1)) break;
+        if (!mbar_wait_bounded(&full[at.slot], at.phase)) break;
         tc_fence_after();
-        const uint32_t q = smem_u32(ring + st_no * S::kStageBytes) + S::kBaseBytes;
+        const uint64_t q = desc_at(q0, at.slot * S::kStageBytes);
 #pragma unroll
         for (int pt = 1; pt >= 0; --pt)  // the low part first
 #pragma unroll
           for (int j = 0; j < R / 16; ++j) {
             if (16 * j >= r16) break;
             const int e = pt * R + 16 * j;  // first of the 16 elements of T's row
-            mma_f16_ss(tmem + d * kCols, smem_desc_sw128(ta + e / 64 * 16384 + e % 64 * 2), smem_desc_mn_sw128(q + 2048 * j), idesc,
-                       pt == 0 || j != 0);
+            mma_f16_ss(tmem + d * kCols, desc_at(ta, e / 64 * 16384 + e % 64 * 2), desc_at(q, 2048 * j), idesc, pt == 0 || j != 0);
           }
-        mma_commit(&empty[st_no]);
+        mma_commit(&empty[at.slot]);
         mma_commit(&dfull[d]);
       }
     }
@@ -396,46 +414,44 @@ __global__ void __launch_bounds__(kTallThreads) k_expand_tall(const __grid_const
   __syncwarp();
   if (warp >= 2) {
     grid_dependency_wait();  // the units are the contraction's, and it may still read what out replaces
-    const int q = warp & 3, tr = 32 * q + lane;
+    const int q = warp & 3, h = (warp - 2) >> 2, tr = 32 * q + lane;
+    const uint32_t mine = smem_u32(smem + S::kTBytes) + (warp - 2) * 2048;
     const float back = a.unit[tile.w + (tr >= kWideRows && count > kWideRows ? 1 : 0)];
-    for (int i = 0; i < nb; ++i) {
-      const int st_no = i % stages;
-      const uint32_t st = smem_u32(ring + st_no * S::kStageBytes);
-      if (!mbar_wait_bounded(&full[st_no], (i / stages) & 1) || !mbar_wait_bounded(&dfull[i & 1], (i / 2) & 1)) break;
+    RingPos at;
+    for (int i = 0; i < nb; ++i, at.next(stages)) {
+      const uint32_t st = smem_u32(ring + at.slot * S::kStageBytes);
+      if (!mbar_wait_bounded(&full[at.slot], at.phase) || !mbar_wait_bounded(&dfull[i & 1], (i / 2) & 1)) break;
       tc_fence_after();
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t v[32];
-        tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (i & 1) * kCols + 32 * h, v);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t at = st + tr * 128 + 16 * ((4 * h + c) ^ (tr & 7));
-          const uint4 b = a.base ? lds_u32x4(at) : make_uint4(0, 0, 0, 0);
-          const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&bw[e]));
-            const __half2 x = __floats2half2_rn(fmaf(__uint_as_float(v[8 * c + 2 * e]), back, f.x), fmaf(__uint_as_float(v[8 * c + 2 * e + 1]), back, f.y));
-            o[e] = *reinterpret_cast<const uint32_t*>(&x);
-          }
-          sts_v4(at, o[0], o[1], o[2], o[3]);
-        }
-      }
+      uint32_t v[32];
+      tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (i & 1) * kCols + 32 * h, v);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&dempty[i & 1]);
-      // the warp's own 32 rows, eight lanes a line
-      const int c = (b0 + i * parts) * kCols + 8 * (lane & 7);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int row = 32 * q + 4 * k + (lane >> 3);
-        if (row < count && c < a.N)
-          *reinterpret_cast<uint4*>(a.out + (size_t)srow[row] * a.N + c) = lds_u32x4(st + row * 128 + 16 * ((lane & 7) ^ (row & 7)));
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t spot = st + tr * 128 + 16 * ((4 * h + c) ^ (tr & 7));
+        const uint4 b = a.base ? lds_u32x4(spot) : make_uint4(0, 0, 0, 0);
+        const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&bw[e]));
+          const __half2 x = __floats2half2_rn(fmaf(__uint_as_float(v[8 * c + 2 * e]), back, f.x), fmaf(__uint_as_float(v[8 * c + 2 * e + 1]), back, f.y));
+          o[e] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+        sts_v4(mine + lane * 64 + 16 * (c ^ ((lane >> 1) & 3)), o[0], o[1], o[2], o[3]);
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before TMA writes the stage again
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st_no]);
+      if (lane == 0) mbar_arrive(&empty[at.slot]);
+      // the warp's own 32 rows of 32 columns, four lanes a row
+      const int c = (b0 + i * parts) * kCols + 32 * h + 8 * (lane & 3);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int wr = 8 * k + (lane >> 2), row = 32 * q + wr;
+        if (row < count && c < a.N)
+          *reinterpret_cast<uint4*>(a.out + (size_t)srow[row] * a.N + c) = lds_u32x4(mine + wr * 64 + 16 * ((lane & 3) ^ ((wr >> 1) & 3)));
+      }
+      __syncwarp();
     }
   } else {
     grid_dependency_wait();
@@ -469,7 +485,10 @@ struct TallGrad {
   static constexpr int kLow = R <= 32 ? 2 * R : kTBytes / 2;  // bytes from the high part to the low
   static constexpr int kStageBytes = kInBytes + kTBytes;
   static constexpr int kPart = R * kGradCols * 4;  // the partial sums lie over the drained ring
-  static constexpr int kTmem = 2 * R;
+  // up to rank 32 both parts are one operand of 2 R columns, so that In is read once
+  static constexpr bool kBoth = R <= 32;
+  static constexpr int kD = kBoth ? 2 * R : R;  // columns of an accumulator
+  static constexpr int kTmem = 2 * kD;
 };
 
 template <int R>
@@ -575,20 +594,23 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
   } else if (warp == 1) {
     if (lane == 0) {
       // kind::f16, A and B fp16 and MN-major, D fp32, M = 128 columns, N = r16
-      const uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(r16 >> 3) << 17) | ((uint32_t)(kGradCols >> 4) << 24);
-      for (int s = 0; s < nt; ++s) {
-        const int st_no = s % stages, d = s & 1;
+      const uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)((S::kBoth ? 2 * R : r16) >> 3) << 17) | ((uint32_t)(kGradCols >> 4) << 24);
+      const uint64_t in0 = smem_desc_mn_sw128(smem_u32(smem)), t0 = smem_desc_mn_sw128(smem_u32(smem) + S::kInBytes);
+      RingPos at;
+      for (int s = 0; s < nt; ++s, at.next(stages)) {
+        const int d = s & 1;
         if (s >= 2 && !mbar_wait_bounded(&dempty[d], (s / 2 - 1) & 1)) break;
-        if (!mbar_wait_bounded(&full[st_no], (s / stages) & 1)) break;
+        if (!mbar_wait_bounded(&full[at.slot], at.phase)) break;
         tc_fence_after();
-        const uint32_t st = smem_u32(smem + st_no * S::kStageBytes), tp = st + S::kInBytes;
+        const uint32_t off = at.slot * S::kStageBytes;
+        const uint64_t in = desc_at(in0, off), tp = desc_at(t0, off);
 #pragma unroll
-        for (int pt = 1; pt >= 0; --pt)  // the low part first
+        for (int pt = S::kBoth ? 0 : 1; pt >= 0; --pt)  // the low part first
 #pragma unroll
           for (int j = 0; j < kWideRows / 16; ++j)
-            mma_f16_ss(tmem + d * R, smem_desc_mn_sw128(st + 2048 * j), smem_desc_mn_sw128(tp + pt * S::kLow + 2048 * j), idesc,
-                       pt == 0 || j != 0);
-        mma_commit(&empty[st_no]);
+            mma_f16_ss(tmem + d * S::kD, desc_at(in, 2048 * j), desc_at(tp, pt * S::kLow + 2048 * j), idesc,
+                       (!S::kBoth && pt == 0) || j != 0);
+        mma_commit(&empty[at.slot]);
         mma_commit(&dfull[d]);
       }
     }
@@ -611,9 +633,17 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
       for (int t = 0; t < R / 16; ++t) {
         if (16 * t >= r16) break;
         uint32_t v[16];
-        tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + (s & 1) * R + 16 * t, v);
+        const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (s & 1) * S::kD + 16 * t;
+        tmem_ld16(at, v);
+        if constexpr (S::kBoth) {
+          uint32_t w[16];
+          tmem_ld16(at + R, w);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sum[16 * t + e] = fmaf(__uint_as_float(v[e]), unit, sum[16 * t + e]);
+          for (int e = 0; e < 16; ++e) sum[16 * t + e] = fmaf(__uint_as_float(v[e]) + __uint_as_float(w[e]), unit, sum[16 * t + e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sum[16 * t + e] = fmaf(__uint_as_float(v[e]), unit, sum[16 * t + e]);
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -678,10 +708,11 @@ __global__ void k_wait_probe_tall(long long cycles) {
   __syncwarp();
 }
 
-cudaError_t launch_pdl_cluster(const void* fn, dim3 grid, size_t smem, cudaStream_t stream, void** args, dim3 cluster) {
+cudaError_t launch_pdl_cluster(const void* fn, dim3 grid, size_t smem, cudaStream_t stream, void** args, dim3 cluster,
+                               int threads = kTallThreads) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kTallThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -809,13 +840,15 @@ cudaError_t launch_expand_tall(const RowsArgs& g, const dictproj_adapters* a, co
   args.g.n_tiles = r->n_tiles + 4;
   args.g.runs = r->runs[1];
   const TallKernel k = DICTPROJ_TALL(g.rp, k_expand_tall, TallExpand);
-  const int fixed = (g.rp <= 32 ? 1 : a->pp / 32) * kTallRows * 128, blocks = (p.N + kCols - 1) / kCols;
+  const int fixed = (g.rp <= 32 ? 1 : a->pp / 32) * kTallRows * 128 + 8 * 2048, blocks = (p.N + kCols - 1) / kCols;
   const int share = g.rp <= 64 ? 2 : 1, full = std::max(1, r->M / kTallRows);  // tiles that do exist, about
-  const int parts = std::min(blocks, std::max(1, share * a->n_sm / full));  // as many CTAs as run at once
+  const int ragged = std::min(a->n_slots, full) / 2;  // and those that end a slot's rows
+  const int parts = std::min(blocks, std::max(1, share * a->n_sm / (full + ragged)));  // as many CTAs as run at once
   const Ring ring = plan_ring(k.stage_bytes, 0, fixed, (blocks + parts - 1) / parts, share);
   args.stages = ring.stages;
   void* pp[] = {(void*)&args};
-  return launch_pdl_cluster(k.fn, dim3(parts, adapter_tiles(r->M, r->n_slots, kTallRows)), ring.smem, stream, pp, dim3(1, 1, 1));
+  return launch_pdl_cluster(k.fn, dim3(parts, adapter_tiles(r->M, r->n_slots, kTallRows)), ring.smem, stream, pp, dim3(1, 1, 1),
+                            kExpandThreads);
 }
 
 // CTAs that the tiles of a gradient are split over: with `at_once` CTAs running, each is as
