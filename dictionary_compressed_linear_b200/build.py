@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdictproj.so")
 
-SOURCES = ["adamw.cu", "adapter.cu", "adapter_tall.cu", "api.cu", "decode.cu", "fused.cu", "indexfmt.cu", "noalloc.cu", "prefill.cu", "train_api.cu", "pack.cpp", "packfile.cpp"]
+SOURCES = ["adamw.cu", "adapter.cu", "adapter_tall.cu", "api.cu", "backward.cu", "decode.cu", "fused.cu", "indexfmt.cu", "noalloc.cu", "prefill.cu", "train_api.cu", "pack.cpp", "packfile.cpp"]
 HEADERS = ["adapter.cuh", "common.cuh", "dictproj_internal.h", "kernels.h", "tcgen05.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

@@ -92,6 +92,7 @@ int ensure_device(int* dev_out) {
     if ((e = prepare_fused_kernels(dev)) != cudaSuccess) return cuda_fail(e, "fused kernel set-up");
     if ((e = prepare_index_kernels(dev)) != cudaSuccess) return cuda_fail(e, "index-format kernel set-up");
     if ((e = prepare_adapter_kernels(dev)) != cudaSuccess) return cuda_fail(e, "adapter kernel set-up");
+    if ((e = prepare_backward_kernels(dev)) != cudaSuccess) return cuda_fail(e, "input-gradient kernel set-up");
     if ((e = prepare_tall_kernels(dev)) != cudaSuccess) return cuda_fail(e, "adapter tensor-core kernel set-up");
     g_dev_ready[dev] = 1;
   }
@@ -1136,6 +1137,7 @@ int dictproj_selftest_wait_timeout(long long cycles, void* stream) {
   if (e == cudaSuccess) e = launch_wait_probe_prefill(cycles, (cudaStream_t)stream);
   if (e == cudaSuccess) e = launch_wait_probe_fused(cycles, (cudaStream_t)stream);
   if (e == cudaSuccess) e = launch_wait_probe_tall(cycles, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = launch_wait_probe_backward(cycles, (cudaStream_t)stream);
   return e == cudaSuccess ? DICTPROJ_OK : cuda_fail(e, "selftest_wait_timeout: launch");
 }
 
@@ -1171,6 +1173,8 @@ int dictproj_check(void* stream) {
   if ((e = take_fused_error(&word2)) != cudaSuccess) return cuda_fail(e, "check: read error word");
   word |= word2;
   if ((e = take_tall_error(&word2)) != cudaSuccess) return cuda_fail(e, "check: read error word");
+  word |= word2;
+  if ((e = take_backward_error(&word2)) != cudaSuccess) return cuda_fail(e, "check: read error word");
   word |= word2;
   if (word) return fail(DICTPROJ_ERR_TIMEOUT, "check: a bounded device wait gave up (error word 0x%x)", word);
   return DICTPROJ_OK;

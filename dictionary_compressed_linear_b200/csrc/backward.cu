@@ -1,0 +1,323 @@
+// Input gradient of the frozen projection: dZ = s_C dY C^T and dX = s_D dZ D^T as tcgen05
+// GEMMs on densified factors.
+//
+// The forward's factors are stored along the reductions of the forward: Cd[d_out][k],
+// D codes [k][d_in]. The gradients contract over the row index instead, so each product is
+// A[M][K] B[K][N] with B row-major: a stage's B tile is bn / 64 boxes of 64 columns x 64
+// reduction rows (128-byte rows, 128-byte swizzle), which the tensor cores read as an
+// MN-major operand. No transposed copy of a factor exists.
+//
+// At 2048 rows the dense products (127 GFLOP for 4096 <- 2048 <- 11008) are what the time
+// goes to; with few rows it is the chain of stages, which a cluster then splits.
+//
+// Every spin-wait is bounded; a wait that gives up sets the file's device error word and
+// the kernel unwinds (frees its tensor memory) without hanging.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "adapter.cuh"
+#include "common.cuh"
+#include "dictproj_internal.h"
+#include "kernels.h"
+#include "tcgen05.cuh"
+
+namespace dictproj {
+namespace {
+
+// Dense fp16 copy of D^ (Dd[j][i], E2M1 x E4M3 exact in fp16, without s_D): one
+// thread per 16-value block, 8 + 1 bytes in, 32 bytes out.
+__global__ void __launch_bounds__(256)
+    k_densify_dict(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, long n_blocks,
+                   __half* __restrict__ dd) {
+  grid_dependency_wait();  // Dd may still be read by the previous input-gradient GEMM
+  trigger_dependents();
+  const long b = (long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (b >= n_blocks) return;
+  const uint2 c = ld_stream_v2(codes + 8 * b);
+  const uint32_t sv = dup_lo(e4m3x2_to_f16x2(scales[b]));
+  uint32_t v[8];
+  e2m1x8_to_f16x2x4(c.x, *reinterpret_cast<uint32_t(*)[4]>(v));
+  e2m1x8_to_f16x2x4(c.y, *reinterpret_cast<uint32_t(*)[4]>(v + 4));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = hmul2_u32(v[i], sv);
+  uint4* dst = reinterpret_cast<uint4*>(dd + 16 * b);
+  dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
+  dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
+}
+
+constexpr int kNnM = 128, kNnK = 64, kNnMaxN = 256, kNnStages = 4;
+constexpr int kNnThreads = 320;  // warp 0 TMA, warp 1 MMA + tensor memory, warps 2..9 epilogue
+constexpr int kNnABytes = kNnM * kNnK * 2, kNnBBytes = kNnMaxN * kNnK * 2;
+constexpr size_t kNnSmem = (size_t)kNnStages * (kNnABytes + kNnBBytes) + 1024 + 256;
+constexpr int kNnSplitN = 128;  // widest tile of a split product: its fp32 sums fit the ring
+static_assert(kNnM * (kNnSplitN + 4) * 4 <= kNnStages * (kNnABytes + kNnBBytes), "partial sums");
+
+// One 128 x bn tile (bn a multiple of 64) of out = scale A B. With gridDim.z = S > 1 the S
+// CTAs of a cluster (1, 1, S) take consecutive ranges of the reduction's stages; the fp32
+// partial tiles meet through distributed shared memory, in rank order, each CTA writing its
+// share of the rows.
+__global__ void __launch_bounds__(kNnThreads, 1)
+    k_gemm_nn(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, int M, int N, int K,
+              int bn, float scale, __half* __restrict__ out) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* sb = smem + kNnStages * kNnABytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sb + kNnStages * kNnBBytes);
+  uint64_t* empty = full + kNnStages;
+  uint64_t* accf = empty + kNnStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n0 = blockIdx.x * bn, m0 = blockIdx.y * kNnM, split = blockIdx.z, nsplit = gridDim.z;
+  const int nk_all = (K + kNnK - 1) / kNnK, s_lo = (int)((long)nk_all * split / nsplit);
+  const int nk = (int)((long)nk_all * (split + 1) / nsplit) - s_lo;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kNnStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(accf, 1);
+    fence_mbar_init();
+    tma_prefetch_map(&tm_a);
+    tma_prefetch_map(&tm_b);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, kNnMaxN);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();  // A and B may be the previous kernels' output
+  trigger_dependents();    // after the tensor memory is ours
+
+  if (warp == 0) {
+    if (lane == 0) {
+      RingPos at;
+      for (int s = 0; s < nk; ++s, at.next(kNnStages)) {
+        if (s >= kNnStages && !mbar_wait_bounded(&empty[at.slot], at.phase ^ 1)) {
+          drain(full, kNnStages, s);
+          break;
+        }
+        mbar_arrive_expect_tx(&full[at.slot], kNnABytes + bn * kNnK * 2);
+        tma_load_2d(smem_u32(smem + at.slot * kNnABytes), &tm_a, (s_lo + s) * kNnK, m0, &full[at.slot]);
+        for (int c = 0; c < bn / 64; ++c)
+          tma_load_2d(smem_u32(sb + at.slot * kNnBBytes + c * kMnChunk), &tm_b, n0 + 64 * c, (s_lo + s) * kNnK, &full[at.slot]);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // kind::f16, A (K-major) and B (MN-major) fp16, D fp32, M = 128, N = bn
+      const uint32_t idesc = (1u << 4) | (1u << 16) | ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(kNnM >> 4) << 24);
+      const uint64_t a0 = smem_desc_sw128(smem_u32(smem)), b0 = smem_desc_mn_sw128(smem_u32(sb));
+      RingPos at;
+      for (int s = 0; s < nk; ++s, at.next(kNnStages)) {
+        if (!mbar_wait_bounded(&full[at.slot], at.phase)) break;
+        tc_fence_after();
+        const uint64_t a = desc_at(a0, at.slot * kNnABytes), b = desc_at(b0, at.slot * kNnBBytes);
+#pragma unroll
+        for (int j = 0; j < kNnK / 16; ++j)
+          mma_f16_ss(tmem, desc_at(a, 32 * j), desc_at(b, 2048 * j), idesc, (s | j) != 0);
+        mma_commit(&empty[at.slot]);
+      }
+      mma_commit(accf);
+    }
+  }
+  __syncwarp();
+  const int pitch = bn + 4;  // floats of a row of the partial sums, over the drained ring
+  float* part = reinterpret_cast<float*>(smem);
+  if (warp >= 2) {
+    const int q = warp & 3, half = (warp - 2) >> 2, row = 32 * q + lane;
+    const bool ok = mbar_wait_bounded(accf, 0);
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = half; 32 * c < bn; c += 2) {
+      uint32_t v[32];
+      tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + 32 * c, v);
+      if (nsplit > 1) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<float4*>(part + row * pitch + 32 * c + e) = make_float4(
+              __uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+        continue;
+      }
+      if (!ok || m0 + row >= M) continue;
+      __half* orow = out + (size_t)(m0 + row) * N;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int gc = n0 + 32 * c + 8 * j;
+        if (gc >= N) break;  // N % 8 == 0
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2 h = __floats2half2_rn(__uint_as_float(v[8 * j + 2 * e]) * scale, __uint_as_float(v[8 * j + 2 * e + 1]) * scale);
+          o[e] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(orow + gc) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+  tc_fence_before();
+  if (nsplit > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kNnMaxN);
+  }
+  if (nsplit > 1) {
+    const uint32_t pbase = smem_u32(part);
+    const int pieces = bn / 8, rows = kNnM / nsplit;
+    for (int i = threadIdx.x; i < rows * pieces; i += kNnThreads) {
+      const int row = split * rows + i / pieces, c = 8 * (i % pieces);
+      if (m0 + row >= M || n0 + c >= N) continue;
+      const uint32_t at = pbase + 4 * (row * pitch + c);
+      const float4 x = sum_peers(at, nsplit), y = sum_peers(at + 16, nsplit);
+      const __half2 h[4] = {__floats2half2_rn(x.x * scale, x.y * scale), __floats2half2_rn(x.z * scale, x.w * scale),
+                            __floats2half2_rn(y.x * scale, y.y * scale), __floats2half2_rn(y.z * scale, y.w * scale)};
+      *reinterpret_cast<uint4*>(out + (size_t)(m0 + row) * N + n0 + c) = *reinterpret_cast<const uint4*>(h);
+    }
+    cluster_arrive();  // no CTA leaves while its sums are read
+    cluster_wait();
+  }
+}
+
+// Self-test of this file's bounded-wait error path (its own device error word).
+__global__ void k_wait_probe_backward(long long cycles) {
+  __shared__ __align__(8) uint64_t bar;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 2);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if (threadIdx.x == 0) {
+    mbar_arrive(&bar);
+    mbar_wait_bounded(&bar, 0, cycles);
+  }
+  __syncwarp();
+}
+
+void set_pdl(cudaLaunchAttribute& a) {
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+}
+void set_cluster_z(cudaLaunchAttribute& a, int s) {
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = 1;
+  a.val.clusterDim.y = 1;
+  a.val.clusterDim.z = (unsigned)s;
+}
+
+// Clusters of S CTAs of k_gemm_nn (one CTA an SM) that the device holds at once; cached.
+int nn_clusters_that_fit(int S, int n_sm) {
+  static std::mutex mu;
+  static int cache[16][9];
+  if (S == 1) return n_sm;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16 || S > 8) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  if (cache[dev][S]) return cache[dev][S] - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1, 1, S);
+  cfg.blockDim = dim3(kNnThreads);
+  cfg.dynamicSmemBytes = kNnSmem;
+  cudaLaunchAttribute attr[1];
+  set_cluster_z(attr[0], S);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, (const void*)k_gemm_nn, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  cache[dev][S] = n + 1;
+  return n;
+}
+
+// Tile width and split of one product, by a model of its time in us: waves of tiles, each a
+// fixed part, its stages (0.1 + 0.0014 per column each) and, split, the sum over the cluster.
+struct NnPlan {
+  int bn, split;
+};
+NnPlan nn_plan(int M, int N, int K, int n_sm) {
+  const int nk = (K + kNnK - 1) / kNnK, rows = (M + kNnM - 1) / kNnM;
+  NnPlan best = {256, 1};
+  double cost = 1e30;
+  for (int bn = 64; bn <= kNnMaxN; bn += 64) {
+    const long tiles = (long)rows * ((N + bn - 1) / bn);
+    for (int S = 1; S <= 8 && (S == 1 || (bn <= kNnSplitN && nk / S >= 2)); S *= 2) {
+      const int fit = nn_clusters_that_fit(S, n_sm);
+      if (fit < 1) continue;
+      const double t = (double)((tiles + fit - 1) / fit) * (3.0 + (double)((nk + S - 1) / S) * (0.1 + 0.0014 * bn) + (S > 1 ? 2.5 : 0.0));
+      if (t < cost) cost = t, best = {bn, S};
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
+cudaError_t prepare_backward_kernels(int device) {
+  (void)device;
+  return cudaFuncSetAttribute(k_gemm_nn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNnSmem);
+}
+
+cudaError_t launch_gemm_nn(const __half* A, const __half* B, int M, int N, int K, float scale, __half* out, int n_sm,
+                           cudaStream_t stream) {
+  CUtensorMap ta, tb;
+  cudaError_t e = encode_tiled_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, A, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2, kNnK, kNnM,
+                                  CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  e = encode_tiled_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, B, (uint64_t)N, (uint64_t)K, (uint64_t)N * 2, 64, kNnK,
+                      CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  const NnPlan plan = nn_plan(M, N, K, n_sm);
+  int bn = plan.bn;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((N + bn - 1) / bn, (M + kNnM - 1) / kNnM, plan.split);
+  cfg.blockDim = dim3(kNnThreads);
+  cfg.dynamicSmemBytes = kNnSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  set_pdl(attr[0]);
+  set_cluster_z(attr[1], plan.split);
+  cfg.attrs = attr;
+  cfg.numAttrs = plan.split > 1 ? 2 : 1;
+  void* args[] = {(void*)&ta, (void*)&tb, &M, &N, &K, &bn, &scale, (void*)&out};
+  return cudaLaunchKernelExC(&cfg, (const void*)k_gemm_nn, args);
+}
+
+cudaError_t launch_densify_dict(const dictproj_group* g, __half* Dd, cudaStream_t stream) {
+  const long blocks = (long)g->k * (g->d_in / 16);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((blocks + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  set_pdl(attr[0]);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  long n = blocks;
+  void* args[] = {(void*)&g->codes, (void*)&g->scales, &n, (void*)&Dd};
+  return cudaLaunchKernelExC(&cfg, (const void*)k_densify_dict, args);
+}
+
+cudaError_t launch_wait_probe_backward(long long cycles, cudaStream_t stream) {
+  k_wait_probe_backward<<<1, 32, 0, stream>>>(cycles);
+  return cudaGetLastError();
+}
+
+cudaError_t take_backward_error(unsigned int* out) {
+  unsigned int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_dictproj_error, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_dictproj_error, &zero, sizeof(unsigned int));
+}
+
+}  // namespace dictproj

@@ -121,8 +121,11 @@ cudaError_t take_prefill_error(unsigned int* out);
 // Input gradient: Dd[j][i] = D^ densified to fp16, [k][d_in]
 cudaError_t launch_densify_dict(const dictproj_group* g, __half* Dd, cudaStream_t stream);
 // out[M][N] = scale A[M][K] B[K][N] (fp16 row-major operands, fp32 accumulation)
-cudaError_t launch_gemm_nn(const __half* A, const __half* B, int M, int N, int K, float scale, __half* out,
+cudaError_t launch_gemm_nn(const __half* A, const __half* B, int M, int N, int K, float scale, __half* out, int n_sm,
                            cudaStream_t stream);
+cudaError_t prepare_backward_kernels(int device);
+cudaError_t take_backward_error(unsigned int* out);
+cudaError_t launch_wait_probe_backward(long long cycles, cudaStream_t stream);
 
 // adapters (adapter.cu)
 cudaError_t prepare_adapter_kernels(int device);

@@ -62,11 +62,6 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
 // (N x K) fp16 K-major, both brought by TMA with 128-byte swizzle; one thread
 // issues tcgen05.mma (M=128, N=256, K=16) into a fp32 accumulator in tensor
 // memory; eight warps run the epilogue.
-// kNN: out = scale · A · B with B (K x N) row-major, for the input gradient
-// (dY C^T and dZ D^T contract over the row index of the densified factors). A
-// stage's B tile is then bn / 64 boxes of 64 columns x 64 reduction rows (128-byte
-// rows, 128-byte swizzle), read as an MN-major operand: no transposed copy exists.
-template <bool kNN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_gemm_tma(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, int M, int N,
                int K, int bn, float scale, __half* __restrict__ out) {
@@ -85,8 +80,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int n0 = blockIdx.x * bn, m0 = blockIdx.y * BM;
   const int nk = (K + BK - 1) / BK;
   // kind::f16, A and B fp16, D fp32, K-major, M = 128, N = bn
-  // (kNN: B is MN-major, bit 16)
-  const uint32_t idesc = (1u << 4) | (kNN ? 1u << 16 : 0u) | ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+  const uint32_t idesc = (1u << 4) | ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -112,12 +106,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (s >= STAGES && !mbar_wait_bounded(&empty[slot], (round - 1) & 1)) break;
         mbar_arrive_expect_tx(&full[slot], A_BYTES + bn * BK * 2);
         tma_load_2d(smem_u32(sa + slot * A_BYTES), &tm_a, s * BK, m0, &full[slot]);
-        if constexpr (kNN) {
-          for (int c = 0; c < bn / 64; ++c)
-            tma_load_2d(smem_u32(sb + slot * B_BYTES + c * kMnChunk), &tm_b, n0 + 64 * c, s * BK, &full[slot]);
-        } else {
-          tma_load_2d(smem_u32(sb + slot * B_BYTES), &tm_b, s * BK, n0, &full[slot]);
-        }
+        tma_load_2d(smem_u32(sb + slot * B_BYTES), &tm_b, s * BK, n0, &full[slot]);
       }
     }
   } else if (warp == 1) {
@@ -129,8 +118,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const uint32_t a = smem_u32(sa + slot * A_BYTES), b = smem_u32(sb + slot * B_BYTES);
 #pragma unroll
         for (int j = 0; j < BK / 16; ++j)
-          mma_f16_ss(tmem, smem_desc_sw128(a + 32 * j), kNN ? smem_desc_mn_sw128(b + 2048 * j) : smem_desc_sw128(b + 32 * j),
-                     idesc, (s | j) != 0);
+          mma_f16_ss(tmem, smem_desc_sw128(a + 32 * j), smem_desc_sw128(b + 32 * j), idesc, (s | j) != 0);
         mma_commit(&empty[slot]);
       }
       mma_commit(accf);
@@ -484,26 +472,6 @@ __global__ void __launch_bounds__(256)
   for (int c = lane; c < k / 8; c += 32) dst[c] = lds_u32x4(rbase + 16 * c);
 }
 
-// Dense fp16 copy of D^ (Dd[j][i], E2M1 x E4M3 exact in fp16, without s_D): one
-// thread per 16-value block, 8 + 1 bytes in, 32 bytes out.
-__global__ void __launch_bounds__(256)
-    k_densify_dict(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, long n_blocks,
-                   __half* __restrict__ dd) {
-  grid_dependency_wait();  // Dd may still be read by the previous input-gradient GEMM
-  const long b = (long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (b >= n_blocks) return;
-  const uint2 c = ld_stream_v2(codes + 8 * b);
-  const uint32_t sv = dup_lo(e4m3x2_to_f16x2(scales[b]));
-  uint32_t v[8];
-  e2m1x8_to_f16x2x4(c.x, *reinterpret_cast<uint32_t(*)[4]>(v));
-  e2m1x8_to_f16x2x4(c.y, *reinterpret_cast<uint32_t(*)[4]>(v + 4));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = hmul2_u32(v[i], sv);
-  uint4* dst = reinterpret_cast<uint4*>(dd + 16 * b);
-  dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
-  dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
-}
-
 // ---- host side ---------------------------------------------------------------------------
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -563,8 +531,7 @@ static cudaLaunchAttribute pdl_attr() {
 cudaError_t prepare_prefill_kernels(int device) {
   (void)device;
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(k_gemm_tma<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem)) ||
-      (e = cudaFuncSetAttribute(k_gemm_tma<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem)) ||
+  if ((e = cudaFuncSetAttribute(k_gemm_tma, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem)) ||
       (e = cudaFuncSetAttribute(k_dict_prefill, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)DictTile::smem)))
     return e;
@@ -769,43 +736,7 @@ cudaError_t launch_coeff_prefill(const dictproj_layer* l, const __half* Z, const
   int N = l->d_out, K = l->k;
   float s = l->s;
   void* args[] = {(void*)&ta, (void*)&tb, &M, &N, &K, &bn, &s, (void*)&Y};
-  return cudaLaunchKernelExC(&cfg, (const void*)k_gemm_tma<false>, args);
-}
-
-cudaError_t launch_gemm_nn(const __half* A, const __half* B, int M, int N, int K, float scale, __half* out,
-                           cudaStream_t stream) {
-  CUtensorMap ta, tb;
-  cudaError_t e = encode_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, A, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2, BK, BM,
-                            CU_TENSOR_MAP_SWIZZLE_128B);
-  if (e != cudaSuccess) return e;
-  e = encode_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, B, (uint64_t)N, (uint64_t)K, (uint64_t)N * 2, 64, BK,
-                CU_TENSOR_MAP_SWIZZLE_128B);
-  if (e != cudaSuccess) return e;
-  int bn = std::min(256, (prefill_tile_width(N, (M + BM - 1) / BM, 148) + 63) / 64 * 64);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((N + bn - 1) / bn, (M + BM - 1) / BM);
-  cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = kGemmSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1] = {pdl_attr()};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  void* args[] = {(void*)&ta, (void*)&tb, &M, &N, &K, &bn, &scale, (void*)&out};
-  return cudaLaunchKernelExC(&cfg, (const void*)k_gemm_tma<true>, args);
-}
-
-cudaError_t launch_densify_dict(const dictproj_group* g, __half* Dd, cudaStream_t stream) {
-  const long blocks = (long)g->k * (g->d_in / 16);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((blocks + 255) / 256));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1] = {pdl_attr()};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  long n = blocks;
-  void* args[] = {(void*)&g->codes, (void*)&g->scales, &n, (void*)&Dd};
-  return cudaLaunchKernelExC(&cfg, (const void*)k_densify_dict, args);
+  return cudaLaunchKernelExC(&cfg, (const void*)k_gemm_tma, args);
 }
 
 }  // namespace dictproj

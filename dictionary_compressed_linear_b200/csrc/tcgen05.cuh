@@ -137,4 +137,26 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// First 1024-byte boundary (swizzled operand tiles start on one).
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) { return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u); }
+
+// A ring position that advances without a division (the MMA thread's own instructions are
+// what a stage of few columns takes: descriptors built anew for each MMA and s % stages
+// took 1100 of 1440 cycles of a gradient's tile).
+struct RingPos {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++slot == stages) slot = 0, phase ^= 1;
+  }
+};
+// Operand descriptors hold the address / 16 in their low bits: a step of `bytes` on.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
+
+// A producer that gives up first waits (bounded) for the copies it has in flight, those of
+// the last stages before stage s.
+__device__ __forceinline__ void drain(uint64_t* full, int stages, int s) {
+  for (int q = max(0, s - stages); q < s; ++q) mbar_wait_bounded(&full[q % stages], (q / stages) & 1);
+}
+
 }  // namespace dictproj

@@ -1,6 +1,6 @@
 // C ABI of the adapters: pools, row plans, forward and backward calls, and the
-// AdamW step (validation and handles; the kernels are in adapter.cu, prefill.cu
-// and adamw.cu).
+// AdamW step (validation and handles; the kernels are in adapter.cu,
+// adapter_tall.cu, backward.cu and adamw.cu).
 #include <algorithm>
 #include <cmath>
 #include <new>
@@ -331,9 +331,9 @@ int dictproj_backward_input(const void* dY, int M, const dictproj_layer* layer, 
     return cuda_fail(e, "backward_input: coefficient densify launch");
   if ((e = launch_densify_dict(group, dd, s)) != cudaSuccess)
     return cuda_fail(e, "backward_input: dictionary densify launch");
-  if ((e = launch_gemm_nn(static_cast<const __half*>(dY), cd, M, group->k, layer->d_out, layer->s, z, s)) != cudaSuccess)
+  if ((e = launch_gemm_nn(static_cast<const __half*>(dY), cd, M, group->k, layer->d_out, layer->s, z, group->n_sm, s)) != cudaSuccess)
     return cuda_fail(e, "backward_input: coefficient stage launch");
-  if ((e = launch_gemm_nn(z, dd, M, group->d_in, group->k, group->s, static_cast<__half*>(dX), s)) != cudaSuccess)
+  if ((e = launch_gemm_nn(z, dd, M, group->d_in, group->k, group->s, static_cast<__half*>(dX), group->n_sm, s)) != cudaSuccess)
     return cuda_fail(e, "backward_input: dictionary stage launch");
   return DICTPROJ_OK;
 }
