@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(kPlanWarps * 32)
         else z = mid - 1;
       }
       const int p = begin[a] + (t - tf[a]) * T, n = min(T, begin[a + 1] - p), row = perm[p];
-      tiles[t] = make_int4(a, p, n, q == 2 ? tfirst[nb + 1 + a] + 2 * (t - tf[a]) : row);
+      const int crowd = a < n_slots && begin[a + 1] - begin[a] > kCrowd ? kCrowdTile : 0;
+      tiles[t] = make_int4(a, p, n | crowd, q == 2 ? tfirst[nb + 1 + a] + 2 * (t - tf[a]) : row);
       // a bucket's rows ascend: they follow one another when the last is n - 1 further
       if (q) (q == 1 ? runs64 : runs128)[t] = perm[p + n - 1] - row == n - 1 ? row : -1;
     }
@@ -366,9 +367,9 @@ __global__ void __launch_bounds__(kRowThreads, R <= 32 ? 4 : 2) k_adapter_few(co
   trigger_dependents();
   const bool in_place = a.out == nullptr || a.base == a.out;
   const int4 tile = g.tiles[tile_no];
-  if (tile_no >= g.n_tiles[in_place ? 0 : 1]) return;  // the whole cluster
+  if (!takes_tile(g, tile_no, tile, in_place)) return;  // the whole cluster
   FewTile f;
-  f.count = tile.z;
+  f.count = tile.z & (kCrowdTile - 1);
   f.rankc = blockIdx.x % kCluster;
   if (tile.x < g.n_slots) {
     f.P = a.P + (size_t)tile.x * g.rp * a.ld_p;
@@ -430,8 +431,8 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_c
   grid_dependency_wait();
   trigger_dependents();
   const int4 tile = g.tiles[tile_no];
-  if (tile_no >= g.n_tiles[0]) return;  // the whole cluster
-  const int count = tile.z, slot = tile.x, r = g.rank[slot], r16 = (r + 15) & ~15;
+  if (!takes_tile(g, tile_no, tile, true)) return;  // the whole cluster
+  const int count = tile.z & (kCrowdTile - 1), slot = tile.x, r = g.rank[slot], r16 = (r + 15) & ~15;
   if (r == 0) return;
   if (tid < TM) srow[tid] = tid < count ? g.perm[tile.y + tid] : tile.w;
   const bool vec = (a.K & 7) == 0;
@@ -575,11 +576,11 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_expand(const __grid_con
   const int tile_no = blockIdx.y;
   const bool in_place = a.base == a.out;
   const int4 tile = g.tiles[tile_no];
-  if (tile_no >= g.n_tiles[in_place ? 0 : 1]) {
+  if (!takes_tile(g, tile_no, tile, in_place)) {
     grid_dependency_wait();
     return;
   }
-  const int count = tile.z, slot = tile.x;
+  const int count = tile.z & (kCrowdTile - 1), slot = tile.x;
   const int r = slot < g.n_slots ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
   const bool vec = (a.N & 7) == 0;
   // the CTAs of a tile take its column blocks in turn, so that they read and write
@@ -708,9 +709,7 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
   const int width = min(kGradCols, a.K - col0);
   if (r == 0) {
     grid_dependency_wait();
-    if (!g.accumulate)
-      for (int i = split * kGradThreads + tid; i < g.max_rank * width; i += nsplit * kGradThreads)
-        out[(size_t)(i / width) * a.K + col0 + i % width] = 0.f;
+    if (!g.accumulate) zero_columns(out + col0, a.K, width, g.max_rank, split, nsplit);
     return;
   }
   const int nt_all = (rows + 63) / 64, t_lo = (int)((long)nt_all * split / nsplit);
@@ -879,6 +878,7 @@ RowsArgs rows_args(const dictproj_adapters* a, const dictproj_rows* r, bool wide
   g.pp = a->pp;
   g.n_slots = a->n_slots;
   g.rows = r->M;
+  g.only = -1;
   g.cluster = kCluster;
   return g;
 }
@@ -996,12 +996,29 @@ static void set_parts(const dictproj_adapters* a, RowsArgs& g) {
 
 cudaError_t launch_adapter_forward(const dictproj_adapters* a, const dictproj_rows* r, const __half* X,
                                    const __half* base, __half* Y, cudaStream_t stream) {
-  const bool wide = r->M >= 256 && r->M >= 32 * a->n_slots;
-  RowsArgs g = rows_args(a, r, wide);
+  // A slot's rows go to the kernels of few rows up to kCrowd of them, to those of many rows
+  // above. The host knows how many rows there are, not how they fall on the slots. From
+  // kCrowd rows a slot on average the second kind takes every slot (4096 -> 4096, one slot
+  // of rank 64: 192 rows 22.4 us by the first kind, 12.3 by the second; 128 rows 12.5 and
+  // 12.2; rank 16: 256 rows 10.0 and 9.1, 384 rows 16.4 and 9.3). With fewer on average,
+  // both kinds run and each takes its slots, which their launches have to be worth: 16 slots
+  // of rank 64 took 32 us by the first kind alone at 256 rows and 39 by both, at 512 rows 64
+  // and 24.
+  const int many_rows = a->rp <= 16 ? 256 : 192;
+  const bool all = r->M >= many_rows && r->M >= kCrowd * a->n_slots, many = all || r->M >= 512;
+  cudaError_t e = cudaSuccess;
+  if (!all) {
+    RowsArgs g = rows_args(a, r, false);
+    g.pass[0] = rows_pass(a, true, X, base, Y);
+    if (many) g.only = 0;
+    e = launch_few(g, r, stream);
+  }
+  if (e != cudaSuccess || !many) return e;
+  RowsArgs g = rows_args(a, r, true);
   g.pass[0] = rows_pass(a, true, X, base, Y);
-  if (!wide) return launch_few(g, r, stream);
+  if (!all) g.only = 1;
   set_parts(a, g);
-  const cudaError_t e = launch_contract(g, 1, a, r, stream);
+  e = launch_contract(g, 1, a, r, stream);
   return e == cudaSuccess ? launch_expand(g, a, r, stream) : e;
 }
 

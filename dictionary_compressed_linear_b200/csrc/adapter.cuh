@@ -9,6 +9,8 @@
 namespace dictproj {
 
 constexpr int kFewRows = 4, kWideRows = 64, kTallRows = 128;  // rows of a tile
+constexpr int kCrowd = 32;  // a slot of more rows is a crowd: its tiles carry kCrowdTile with their row count
+constexpr int kCrowdTile = 1 << 16;
 constexpr int kGradCols = 128;                                // columns of a weight gradient's CTA
 
 struct RowsPass {
@@ -32,6 +34,7 @@ struct RowsArgs {
   const int* rank;
   const float* scale;
   int rp, pp, n_slots, rows, cluster;
+  int only;  // -1: every tile; 0: no crowds' tiles; 1: crowds' tiles alone
 };
 
 struct GradPass {
@@ -165,6 +168,25 @@ __device__ __forceinline__ void copy_rows(const RowsPass& a, int n_rows, const i
     const size_t at = (size_t)rows[i / n] * a.N;
     const int c = 8 * (lo + i % n);
     write_piece(a.out + at, c, a.N, vec, a.base ? read_piece(a.base + at, c, a.N, vec, a.base + (size_t)n_rows * a.N) : make_uint4(0, 0, 0, 0));
+  }
+}
+
+// Whether a launch is to take a tile (slots' and, unless the output is in place, those of
+// rows without an adapter).
+__device__ __forceinline__ bool takes_tile(const RowsArgs& g, int tile_no, const int4& tile, bool in_place) {
+  return tile_no < g.n_tiles[in_place ? 0 : 1] && (g.only < 0 || g.only == (tile.z >= kCrowdTile ? 1 : 0));
+}
+
+// Zeros over `width` columns of rows [0, n) of a gradient, shared by `parts` CTAs.
+__device__ __forceinline__ void zero_columns(float* out, int K, int width, int n, int part, int parts) {
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const bool vec = (K & 3) == 0 && (width & 3) == 0;
+  for (int j = part * warps + warp; j < n; j += parts * warps) {
+    float* row = out + (size_t)j * K;
+    if (vec)
+      for (int c = 4 * lane; c < width; c += 128) *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    else
+      for (int c = lane; c < width; c += 32) row[c] = 0.f;
   }
 }
 

@@ -88,8 +88,8 @@ __global__ void __launch_bounds__(kTallThreads) k_contract_tall(const __grid_con
   trigger_dependents();  // not before the tensor memory is ours: a dependent may want all of it
   const int4 tile = g.tiles[tile_no];
   const int run_row = g.runs[tile_no];
-  const bool live = tile_no < g.n_tiles[0];
-  const int count = tile.z, slot = tile.x;
+  const bool live = takes_tile(g, tile_no, tile, true);
+  const int count = tile.z & (kCrowdTile - 1), slot = tile.x;
   // the cluster's CTAs take the column blocks in turn, so that they read neighbouring parts
   // of the rows at the same time
   const int kc = (a.K + kCols - 1) / kCols, nk = (kc - rankc + cluster - 1) / cluster;
@@ -290,8 +290,8 @@ __global__ void __launch_bounds__(kExpandThreads) k_expand_tall(const __grid_con
   const bool in_place = a.base == a.out;
   const int4 tile = g.tiles[tile_no];
   const int run_row = g.runs[tile_no];
-  const bool live = tile_no < g.n_tiles[in_place ? 0 : 1];
-  const int count = tile.z, slot = tile.x;
+  const bool live = takes_tile(g, tile_no, tile, in_place);
+  const int count = tile.z & (kCrowdTile - 1), slot = tile.x;
   const int r = live && slot < g.n_slots ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
   const int blocks = (a.N + kCols - 1) / kCols, nb = (blocks - b0 + parts - 1) / parts;
   if (r == 0) {  // no tile, or base alone
@@ -491,9 +491,7 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
   if (r == 0) {
     trigger_dependents();
     grid_dependency_wait();
-    if (!g.accumulate)
-      for (int i = split * kTallThreads + threadIdx.x; i < g.max_rank * width; i += nsplit * kTallThreads)
-        out[(size_t)(i / width) * a.K + col0 + i % width] = 0.f;
+    if (!g.accumulate) zero_columns(out + col0, a.K, width, g.max_rank, split, nsplit);
     return;
   }
   const int nt_all = (rows + kWideRows - 1) / kWideRows, t_lo = (int)((long)nt_all * split / nsplit);
@@ -766,8 +764,14 @@ cudaError_t encode_adapter_maps(dictproj_adapters* a) {
   return cudaSuccess;
 }
 
-// Rows that TMA can read, and enough of them to fill 128-row tiles.
-bool tall_serves(const dictproj_adapters* a, const dictproj_rows* r) { return a->d_out % 8 == 0 && r->M >= 256; }
+// Rows that TMA can read, and enough of them to fill 128-row tiles: up to rank 32 the
+// mma.sync kernels are as fast until there are about a hundred rows a slot (backward, 4096
+// and 4096 wide, rank 16: 1 slot 384 rows 20.8 us there, 16.5 here; 16 slots 1024 rows 29
+// and 39), above it their instructions cost more from 256 rows on (rank 64: 1 slot 256 rows
+// 24.3 and 18.7, 16 slots 53 and 46).
+bool tall_serves(const dictproj_adapters* a, const dictproj_rows* r) {
+  return a->d_out % 8 == 0 && r->M >= (a->rp <= 32 ? std::max(384, 96 * a->n_slots) : 256);
+}
 
 struct TallKernel {
   const void* fn;
