@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kPlanWarps * 32)
     k_rows_plan(const int* __restrict__ ids, int M, int n_slots, int* __restrict__ perm, int* __restrict__ start,
                 int* __restrict__ n_tiles, int4* __restrict__ tiles4, int4* __restrict__ tiles64,
                 int4* __restrict__ tiles128, int* __restrict__ runs64, int* __restrict__ runs128,
-                int* __restrict__ first64) {
+                int* __restrict__ first64, int* __restrict__ used) {
   extern __shared__ int plan_smem[];
   __shared__ int wsum[kPlanWarps];
   const int nb = n_slots + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -115,6 +115,10 @@ __global__ void __launch_bounds__(kPlanWarps * 32)
       at += c;
     }
   }
+  int n_used;
+  const int at_used = block_exclusive_sum(count > 0 ? 1 : 0, wsum, &n_used);
+  if (count > 0) used[at_used] = s;
+  if (threadIdx.x == 0) n_tiles[6] = n_used;
 #pragma unroll 1
   for (int q = 0; q < 3; ++q) {
     const int T = plan_rows(q);
@@ -234,7 +238,7 @@ __device__ __forceinline__ void dot8(float& acc, const uint4& x, const uint4& w)
 }
 struct FewTile {
   int row[kFewRows];
-  int count, r, rankc;
+  int first, count, r, rankc;  // first: the tile's first position in the plan
   float scale;
   const __half* P;
   const __half* Q;
@@ -250,9 +254,9 @@ __device__ __forceinline__ void prefetch_rows(const __half* w, int ld, int lo, i
 }
 
 template <int R, int NR, bool VEC>
-__device__ __forceinline__ void few_rows(const RowsPass& a, int n_rows, const FewTile& f, float* part, float* full) {
+__device__ __forceinline__ void few_rows(const RowsPass& a, int n_rows, int pp, const FewTile& f, float* part, float* full) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int kp = (a.K + 7) / 8, np = (a.N + 7) / 8;
+  const int kp = (a.K + 7) / 8, np = a.out ? (a.N + 7) / 8 : 0;
   const int n_lo = np * f.rankc / kCluster, n_hi = np * (f.rankc + 1) / kCluster;
   if (R > 16) prefetch_rows(f.Q, a.ld_q, n_lo, n_hi, 16, f.r);
   float acc[R / 8][NR];
@@ -297,6 +301,8 @@ __device__ __forceinline__ void few_rows(const RowsPass& a, int n_rows, const Fe
   }
   cluster_arrive();  // waited for at the end: no CTA leaves while its sums are read
   __syncthreads();
+  if (a.sums && f.rankc < f.count)  // a row each for the weight gradients
+    for (int j = tid; j < ((f.r + 7) & ~7); j += kRowThreads) a.sums[(size_t)(f.first + f.rankc) * pp + j] = full[f.rankc * R + j];
   const int js = lane >> 3;
   for (int p0 = n_lo + 8 * warp; p0 < n_hi; p0 += 8 * (kRowThreads / 32)) {  // the warp's lanes stay together
     const int p = p0 + (lane & 7);
@@ -369,13 +375,14 @@ __global__ void __launch_bounds__(kRowThreads, R <= 32 ? 4 : 2) k_adapter_few(co
   const int4 tile = g.tiles[tile_no];
   if (!takes_tile(g, tile_no, tile, in_place)) return;  // the whole cluster
   FewTile f;
+  f.first = tile.y;
   f.count = tile.z & (kCrowdTile - 1);
   f.rankc = blockIdx.x % kCluster;
   if (tile.x < g.n_slots) {
     f.P = a.P + (size_t)tile.x * g.rp * a.ld_p;
     f.Q = a.Q + (size_t)tile.x * g.rp * a.ld_q;
     // the first 16 ranks (every slot holds as many rows) start before the rank is known
-    const int kp = (a.K + 7) / 8, np = (a.N + 7) / 8;
+    const int kp = (a.K + 7) / 8, np = a.out ? (a.N + 7) / 8 : 0;
     prefetch_rows(f.P, a.ld_p, kp * f.rankc / kCluster, kp * (f.rankc + 1) / kCluster, 0, 16);
     prefetch_rows(f.Q, a.ld_q, np * f.rankc / kCluster, np * (f.rankc + 1) / kCluster, 0, 16);
   }
@@ -390,8 +397,8 @@ __global__ void __launch_bounds__(kRowThreads, R <= 32 ? 4 : 2) k_adapter_few(co
     return;
   }
   f.scale = g.scale[tile.x];
-  if (f.count == 1) few_rows<R, 1, VEC>(a, g.rows, f, part, full);
-  else few_rows<R, kFewRows, VEC>(a, g.rows, f, part, full);
+  if (f.count == 1) few_rows<R, 1, VEC>(a, g.rows, g.pp, f, part, full);
+  else few_rows<R, kFewRows, VEC>(a, g.rows, g.pp, f, part, full);
 }
 
 // ---- many rows of a slot: prefill and training ----------------------------------------------
@@ -697,19 +704,23 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
   using S = GradShape<R>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int split = blockIdx.z, nsplit = gridDim.z, slot = blockIdx.y;
+  const int split = blockIdx.z, nsplit = gridDim.z, slot = grad_slot(g);
   const int which = (int)blockIdx.x < g.pass[0].blocks ? 0 : 1;
   const GradPass& a = g.pass[which];
   const int col0 = ((int)blockIdx.x - (which ? g.pass[0].blocks : 0)) * kGradCols;
   const uint32_t ring = smem_u32(smem);
   trigger_dependents();
+  if (slot < 0) {
+    grid_dependency_wait();
+    return;
+  }
   const int p0 = g.start[slot], rows = g.start[slot + 1] - p0, tile0 = g.first64[slot];
   const int r = rows ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
   float* out = a.g + (size_t)slot * g.max_rank * a.K;
   const int width = min(kGradCols, a.K - col0);
   if (r == 0) {
     grid_dependency_wait();
-    if (!g.accumulate) zero_columns(out + col0, a.K, width, g.max_rank, split, nsplit);
+    if (!g.zeroed && !g.accumulate) zero_columns(out + col0, a.K, width, g.max_rank, split, nsplit);
     return;
   }
   const int nt_all = (rows + 63) / 64, t_lo = (int)((long)nt_all * split / nsplit);
@@ -847,6 +858,102 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
   }
 }
 
+// Few rows: the gradient is mostly its own output. A thread sums eight ranks of four columns
+// over the slot's rows, in plan order, in fp32; a slot without rows gets its zeros the same way.
+constexpr int kFewGradThreads = 128, kFewGradRanks = 8, kFewGradCols = 4 * kFewGradThreads;
+
+__global__ void __launch_bounds__(kFewGradThreads) k_grad_few(const __grid_constant__ GradArgs g) {
+  const int which = (int)blockIdx.x < g.pass[0].blocks ? 0 : 1, slot = blockIdx.y, j0 = blockIdx.z * kFewGradRanks;
+  const GradPass& a = g.pass[which];
+  const int c = ((int)blockIdx.x - (which ? g.pass[0].blocks : 0)) * kFewGradCols + 4 * threadIdx.x;
+  // what the call found is read before the wait on its first kernel (see the expansion)
+  trigger_dependents();
+  const int p0 = g.start[slot], r = g.rank[slot], p1 = r > j0 ? g.start[slot + 1] : p0;
+  const bool vec = (a.K & 3) == 0;
+  // eight rows at a time, their loads together: one row's took 0.6 us after the other's
+  constexpr int kAhead = 8;
+  uint2 x[kAhead];
+  auto fetch = [&](int p) {
+    int row[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) row[q] = g.perm[min(p + q, p1 - 1)];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      const __half* h = a.in + (size_t)row[q] * a.K + c;
+      x[q] = make_uint2(0, 0);
+      if (p + q >= p1 || c >= a.K) continue;
+      if (vec) {
+        x[q] = *reinterpret_cast<const uint2*>(h);
+      } else {
+        const unsigned short e0 = __half_as_ushort(h[0]), e1 = c + 1 < a.K ? __half_as_ushort(h[1]) : 0;
+        const unsigned short e2 = c + 2 < a.K ? __half_as_ushort(h[2]) : 0, e3 = c + 3 < a.K ? __half_as_ushort(h[3]) : 0;
+        x[q] = make_uint2((uint32_t)e0 | (uint32_t)e1 << 16, (uint32_t)e2 | (uint32_t)e3 << 16);
+      }
+    }
+  };
+  if (p0 < p1) fetch(p0);
+  float acc[kFewGradRanks][4];
+#pragma unroll
+  for (int j = 0; j < kFewGradRanks; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+  grid_dependency_wait();
+  for (int p = p0; p < p1; p += kAhead) {
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      // past the end x is 0 beside a repeated row's T
+      const float4* t = reinterpret_cast<const float4*>(a.sums + (size_t)min(p + q, p1 - 1) * g.pp + j0);
+      const float4 t0 = t[0], t1 = t[1];
+      const float tv[kFewGradRanks] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+      const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&x[q].x)), hi = __half22float2(*reinterpret_cast<const __half2*>(&x[q].y));
+#pragma unroll
+      for (int j = 0; j < kFewGradRanks; ++j) {
+        acc[j][0] = fmaf(tv[j], lo.x, acc[j][0]), acc[j][1] = fmaf(tv[j], lo.y, acc[j][1]);
+        acc[j][2] = fmaf(tv[j], hi.x, acc[j][2]), acc[j][3] = fmaf(tv[j], hi.y, acc[j][3]);
+      }
+    }
+    if (p + kAhead < p1) fetch(p + kAhead);
+  }
+  if (c >= a.K) return;
+  float* out = a.g + (size_t)slot * g.max_rank * a.K + c;
+#pragma unroll
+  for (int j = 0; j < kFewGradRanks; ++j) {
+    if (j0 + j >= g.max_rank) break;
+    float* dst = out + (size_t)(j0 + j) * a.K;
+    const bool add = g.accumulate && j0 + j < r && p0 < p1;
+    if (g.accumulate && !add) continue;
+    if (vec) {
+      float4 x = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+      if (add) {
+        const float4 y = *reinterpret_cast<const float4*>(dst);
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      }
+      *reinterpret_cast<float4*>(dst) = x;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < a.K) dst[e] = add ? dst[e] + acc[j][e] : acc[j][e];
+    }
+  }
+}
+
+// Zeros in the gradients of slots without rows or rank (of several): most slots of a large
+// pool, which the gradient kernels' large CTAs would take waves for.
+__global__ void __launch_bounds__(256) k_zero_unused(const __grid_constant__ GradArgs g) {
+  grid_dependency_wait();
+  trigger_dependents();
+  const int slot = blockIdx.y;
+  if (g.start[slot + 1] > g.start[slot] && g.rank[slot] > 0) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const size_t n = (size_t)g.max_rank * g.pass[i].K;
+    float* out = g.pass[i].g + slot * n;
+    const size_t first = (size_t)blockIdx.x * 256 + threadIdx.x, step = (size_t)gridDim.x * 256;
+    if ((n & 3) == 0)
+      for (size_t e = first; e < n / 4; e += step) reinterpret_cast<float4*>(out)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    else
+      for (size_t e = first; e < n; e += step) out[e] = 0.f;
+  }
+}
+
 // ---- launches --------------------------------------------------------------------------
 cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, void** args,
                        dim3 cluster = dim3(1, 1, 1)) {
@@ -901,11 +1008,11 @@ RowsPass rows_pass(const dictproj_adapters* a, bool forward, const __half* in, c
 #define DICTPROJ_BY_RANK(rp, call) \
   ((rp) <= 16 ? call(16) : (rp) <= 32 ? call(32) : (rp) <= 64 ? call(64) : call(128))
 
-cudaError_t launch_few(const RowsArgs& g, const dictproj_rows* r, cudaStream_t stream) {
+cudaError_t launch_few(const RowsArgs& g, int passes, const dictproj_rows* r, cudaStream_t stream) {
   void* args[] = {(void*)&g};
   const bool vec = ((g.pass[0].K | g.pass[0].N) & 7) == 0;
 #define FEW(R) (vec ? (const void*)k_adapter_few<R, true> : (const void*)k_adapter_few<R, false>)
-  return launch_pdl(DICTPROJ_BY_RANK(g.rp, FEW), dim3((unsigned)(adapter_tiles(r->M, r->n_slots, kFewRows) * kCluster)),
+  return launch_pdl(DICTPROJ_BY_RANK(g.rp, FEW), dim3((unsigned)(adapter_tiles(r->M, r->n_slots, kFewRows) * kCluster), passes),
                     dim3(kRowThreads), 0, stream, args, dim3(kCluster, 1, 1));
 #undef FEW
 }
@@ -982,7 +1089,7 @@ cudaError_t launch_rows_plan(const dictproj_rows* r, const int* ids, int M, cuda
   int ns = r->n_slots;
   void* args[] = {&ids, &M, &ns, (void*)&r->perm, (void*)&r->start, (void*)&r->n_tiles, (void*)&r->tiles[0],
                   (void*)&r->tiles[1], (void*)&r->tiles[2], (void*)&r->runs[0], (void*)&r->runs[1],
-                  (void*)&r->first64};
+                  (void*)&r->first64, (void*)&r->used};
   return launch_pdl((const void*)k_rows_plan, dim3(1), dim3(kPlanWarps * 32),
                     ((size_t)kPlanWarps * (ns + 1) + 4 * (ns + 2)) * sizeof(int), stream, args);
 }
@@ -1011,7 +1118,7 @@ cudaError_t launch_adapter_forward(const dictproj_adapters* a, const dictproj_ro
     RowsArgs g = rows_args(a, r, false);
     g.pass[0] = rows_pass(a, true, X, base, Y);
     if (many) g.only = 0;
-    e = launch_few(g, r, stream);
+    e = launch_few(g, 1, r, stream);
   }
   if (e != cudaSuccess || !many) return e;
   RowsArgs g = rows_args(a, r, true);
@@ -1029,9 +1136,6 @@ cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_r
   g.pass[0] = rows_pass(a, false, dY, base, dX);
   g.pass[1] = rows_pass(a, true, X, nullptr, nullptr);
   set_parts(a, g);
-  cudaError_t e = launch_contract(g, dA ? 2 : 1, a, r, stream);
-  if (e == cudaSuccess && dX) e = launch_expand(g, a, r, stream);
-  if (e != cudaSuccess || !dA) return e;
   GradArgs w = {};
   for (int i = 0; i < 2; ++i) {
     w.pass[i].in = i ? dY : X;
@@ -1051,11 +1155,42 @@ cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_r
   w.max_rank = a->max_rank;
   w.accumulate = accumulate;
   w.n_rows = r->M;
+  w.used = r->used;
+  w.n_used = r->n_tiles + 6;
+  w.zeroed = a->n_slots > 1;
+  // The kernels of few rows, both contractions and dX in one launch, for some rows a slot
+  // (4096 and 4096 wide, rank 16: 1 slot 8 rows 8.5 us against 10.5, 32 rows 15.6 against
+  // 10.7; 16 slots 64 rows 16.7 against 23.3, 128 rows 23.1 and 23.8).
+  if (r->M <= std::min(128, 12 + 4 * a->n_slots)) {
+    RowsArgs f = rows_args(a, r, false);
+    for (int i = 0; i < 2; ++i) {
+      f.pass[i] = g.pass[i];
+      w.pass[i].sums = f.pass[i].sums = dA ? reinterpret_cast<float*>(a->parts[i]) : nullptr;
+      w.pass[i].blocks = (w.pass[i].K + kFewGradCols - 1) / kFewGradCols;
+    }
+    const cudaError_t e = launch_few(f, dA ? 2 : 1, r, stream);
+    if (e != cudaSuccess || !dA) return e;
+    void* args[] = {(void*)&w};
+    return launch_pdl((const void*)k_grad_few,
+                      dim3(w.pass[0].blocks + w.pass[1].blocks, a->n_slots, (a->max_rank + kFewGradRanks - 1) / kFewGradRanks),
+                      dim3(kFewGradThreads), 0, stream, args);
+  }
+  const int slots = std::min(a->n_slots, r->M);  // that can have rows
+  if (dA && w.zeroed && !accumulate) {
+    void* args[] = {(void*)&w};
+    const size_t most = (size_t)a->max_rank * std::max(a->d_in, a->d_out) / 4;
+    const int per = (int)std::min<size_t>(std::max(1, 8 * a->n_sm / a->n_slots), most / 1024 + 1);
+    const cudaError_t z = launch_pdl((const void*)k_zero_unused, dim3(per, a->n_slots), dim3(256), 0, stream, args);
+    if (z != cudaSuccess) return z;
+  }
+  cudaError_t e = launch_contract(g, dA ? 2 : 1, a, r, stream);
+  if (e == cudaSuccess && dX) e = launch_expand(g, a, r, stream);
+  if (e != cudaSuccess || !dA) return e;
   if (tall_serves(a, r)) return launch_grad_tall(w, a, r, stream);
   const int blocks = w.pass[0].blocks + w.pass[1].blocks;
   int split = 1;
-  while (split < 8 && blocks * a->n_slots * split < 3 * a->n_sm && 64 * a->n_slots * split < r->M) split *= 2;
-  const dim3 grid(blocks, a->n_slots, split);
+  while (split < 8 && blocks * slots * split < 3 * a->n_sm && 64 * slots * split < r->M) split *= 2;
+  const dim3 grid(blocks, slots, split);
   if (a->rp <= 16) return launch_grad<16>(w, grid, stream);
   if (a->rp <= 32) return launch_grad<32>(w, grid, stream);
   if (a->rp <= 64) return launch_grad<64>(w, grid, stream);

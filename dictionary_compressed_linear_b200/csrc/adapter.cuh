@@ -23,6 +23,7 @@ struct RowsPass {
   // a tile's rows, and what the parts of a tile are multiplied with
   __half* parts;
   float* unit;
+  float* sums;  // few rows, backward: scale * T in plan order, [rows][pp], or null
   int K, N, ld_p, ld_q;
 };
 struct RowsArgs {
@@ -41,6 +42,7 @@ struct GradPass {
   const __half* in;
   const __half* parts;
   const float* unit;
+  const float* sums;  // few rows
   float* g;
   int K, blocks;
 };
@@ -51,8 +53,17 @@ struct GradArgs {
   const int* runs;  // of the 64-row tiles
   const int* perm;
   const int* rank;
+  const int* used;    // the slots that have rows
+  const int* n_used;
   int rp, pp, max_rank, accumulate, n_rows;
+  int zeroed;         // several slots: those without rows or rank are zeroed by a launch of their own
 };
+
+// The slot of a gradient CTA (blockIdx.y counts the slots that have rows), -1: none.
+__device__ __forceinline__ int grad_slot(const GradArgs& g) {
+  if (!g.zeroed) return blockIdx.y;
+  return (int)blockIdx.y < *g.n_used ? g.used[blockIdx.y] : -1;
+}
 
 // ---- clusters and distributed shared memory
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }

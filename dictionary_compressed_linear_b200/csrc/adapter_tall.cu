@@ -478,7 +478,12 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
   __shared__ uint32_t tmem_slot;
   const GradArgs& g = args.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, stages = args.stages;
-  const int split = blockIdx.z, nsplit = gridDim.z, slot = blockIdx.y;
+  const int split = blockIdx.z, nsplit = gridDim.z, slot = grad_slot(g);
+  if (slot < 0) {
+    trigger_dependents();
+    grid_dependency_wait();
+    return;
+  }
   const int which = (int)blockIdx.x < g.pass[0].blocks ? 0 : 1;
   const GradPass& a = g.pass[which];
   const int col0 = ((int)blockIdx.x - (which ? g.pass[0].blocks : 0)) * kGradCols;
@@ -491,7 +496,7 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
   if (r == 0) {
     trigger_dependents();
     grid_dependency_wait();
-    if (!g.accumulate) zero_columns(out + col0, a.K, width, g.max_rank, split, nsplit);
+    if (!g.zeroed && !g.accumulate) zero_columns(out + col0, a.K, width, g.max_rank, split, nsplit);
     return;
   }
   const int nt_all = (rows + kWideRows - 1) / kWideRows, t_lo = (int)((long)nt_all * split / nsplit);
@@ -855,13 +860,14 @@ cudaError_t launch_grad_tall(const GradArgs& w, const dictproj_adapters* a, cons
   }
   args.g = w;
   const int blocks = w.pass[0].blocks + w.pass[1].blocks;
-  const int split = grad_split(blocks * a->n_slots, r->M / (kWideRows * a->n_slots), a->n_sm * (w.rp <= 32 ? 3 : w.rp <= 64 ? 2 : 1));
+  const int slots = std::min(a->n_slots, r->M);  // that can have rows
+  const int split = grad_split(blocks * slots, r->M / (kWideRows * slots), a->n_sm * (w.rp <= 32 ? 3 : w.rp <= 64 ? 2 : 1));
   const TallKernel k = DICTPROJ_TALL(w.rp, k_grad_tall, TallGrad);
-  const int tiles = (r->M / (kWideRows * a->n_slots) + split) / split;
-  const Ring ring = plan_ring(k.stage_bytes, k.part_bytes, 0, tiles, sm_share((long)blocks * a->n_slots * split, a->n_sm));
+  const int tiles = (r->M / (kWideRows * slots) + split) / split;
+  const Ring ring = plan_ring(k.stage_bytes, k.part_bytes, 0, tiles, sm_share((long)blocks * slots * split, a->n_sm));
   args.stages = ring.stages;
   void* p[] = {(void*)&args};
-  return launch_pdl_cluster(k.fn, dim3(blocks, a->n_slots, split), ring.smem, stream, p, dim3(1, 1, split));
+  return launch_pdl_cluster(k.fn, dim3(blocks, slots, split), ring.smem, stream, p, dim3(1, 1, split));
 }
 
 cudaError_t launch_wait_probe_tall(long long cycles, cudaStream_t stream) {

@@ -186,7 +186,7 @@ int dictproj_rows_create(int max_rows, int n_slots, dictproj_rows** out) {
   r->n_slots = n_slots;
   cudaError_t e;
   if ((e = dmalloc((void**)&r->perm, (size_t)max_rows * 4)) || (e = dmalloc((void**)&r->start, (size_t)(n_slots + 2) * 4)) ||
-      (e = dmalloc((void**)&r->n_tiles, 6 * sizeof(int))) || (e = dmalloc((void**)&r->first64, (size_t)n_slots * 4)) ||
+      (e = dmalloc((void**)&r->n_tiles, 7 * sizeof(int))) || (e = dmalloc((void**)&r->used, (size_t)n_slots * 4)) || (e = dmalloc((void**)&r->first64, (size_t)n_slots * 4)) ||
       (e = dmalloc((void**)&r->tiles[0], (size_t)adapter_tiles(max_rows, n_slots, 4) * sizeof(int4))) ||
       (e = dmalloc((void**)&r->tiles[1], (size_t)adapter_tiles(max_rows, n_slots, 64) * sizeof(int4))) ||
       (e = dmalloc((void**)&r->runs[0], (size_t)adapter_tiles(max_rows, n_slots, 64) * sizeof(int))) ||
@@ -205,6 +205,7 @@ void dictproj_free_rows(dictproj_rows* r) {
   cudaFree(r->perm);
   cudaFree(r->start);
   cudaFree(r->n_tiles);
+  cudaFree(r->used);
   cudaFree(r->first64);
   cudaFree(r->tiles[0]);
   cudaFree(r->tiles[1]);
