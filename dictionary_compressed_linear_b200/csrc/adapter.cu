@@ -464,11 +464,17 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_c
     if (i < nk) {
       const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes + spot;
       const int col = (i * cluster + rankc) * CW, c = col + 8 * piece;
+      bool want[TM / STEP];
 #pragma unroll
       for (int q = 0; q < TM / STEP; ++q) {
-        const bool in = row0 + STEP * q < count && c < a.K;
-        if (vec) cp_async16(st + STEP * q * PITCH, line[q] + (in ? c : 0), in ? 16 : 0);
-        else sts16(st + STEP * q * PITCH, in ? read_piece(line[q], c, a.K, false, a.in + (size_t)g.rows * a.K) : make_uint4(0, 0, 0, 0));
+        want[q] = row0 + STEP * q < count && c < a.K;
+        if (vec) cp_async16(st + STEP * q * PITCH, line[q] + (want[q] ? c : 0), want[q] ? 16 : 0);
+      }
+      if (!vec) {
+        uint4 v[TM / STEP];
+        read_pieces(v, line, want, c, a.K, a.in + (size_t)g.rows * a.K);
+#pragma unroll
+        for (int q = 0; q < TM / STEP; ++q) sts16(st + STEP * q * PITCH, v[q]);
       }
       const bool in = c < a.ld_p;
 #pragma unroll
@@ -579,7 +585,7 @@ struct ExpandShape {
 };
 
 template <int R>
-__global__ void __launch_bounds__(kRowThreads) k_adapter_expand(const __grid_constant__ RowsArgs g) {
+__global__ void __launch_bounds__(kRowThreads, R == 128 ? 2 : 1) k_adapter_expand(const __grid_constant__ RowsArgs g) {
   using S = ExpandShape<R>;
   constexpr int TM = S::TM, CW = S::CW, PITCH = S::kPitch;
   static_assert(kRowThreads == 16 * PITCH / 16, "a thread loads one 16-byte column of every 16th row");
@@ -621,14 +627,22 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_expand(const __grid_con
 #pragma unroll
       for (int j = 0; j < R / 16; ++j)
         if (16 * j < r16) cp_async16(dst + (TM + 16 * j) * PITCH, wq + (inq ? (size_t)(16 * j) * a.ld_q + c : 0), inq ? 16 : 0);
-      if (a.base)
+      if (a.base) {
+        const __half* line[TM / 16];
+        bool want[TM / 16];
 #pragma unroll
         for (int q = 0; q < TM / 16; ++q) {
-          const bool in = row[q] >= 0 && c < a.N;
-          const __half* line = a.base + (size_t)max(row[q], 0) * a.N;
-          if (vec) cp_async16(dst + 16 * q * PITCH, line + (in ? c : 0), in ? 16 : 0);
-          else sts16(dst + 16 * q * PITCH, in ? read_piece(line, c, a.N, false, a.base + (size_t)g.rows * a.N) : make_uint4(0, 0, 0, 0));
+          want[q] = row[q] >= 0 && c < a.N;
+          line[q] = a.base + (size_t)max(row[q], 0) * a.N;
+          if (vec) cp_async16(dst + 16 * q * PITCH, line[q] + (want[q] ? c : 0), want[q] ? 16 : 0);
         }
+        if (!vec) {
+          uint4 v[TM / 16];
+          read_pieces(v, line, want, c, a.N, a.base + (size_t)g.rows * a.N);
+#pragma unroll
+          for (int q = 0; q < TM / 16; ++q) sts16(dst + 16 * q * PITCH, v[q]);
+        }
+      }
     }
     cp_async_commit();
   };
@@ -748,13 +762,19 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
   auto issue_in = [&](int i) {
     if (i < nt) {
       const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
+      const __half* line[4];
+      bool want[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const uint32_t dst = st + spot + 16 * q * S::kInPitch;
-        const bool in = next[q] >= 0 && col < a.K;
-        const __half* line = a.in + (size_t)max(next[q], 0) * a.K;
-        if (vec) cp_async16(dst, line + (in ? col : 0), in ? 16 : 0);
-        else sts16(dst, in ? read_piece(line, col, a.K, false, a.in + (size_t)g.n_rows * a.K) : make_uint4(0, 0, 0, 0));
+        want[q] = next[q] >= 0 && col < a.K;
+        line[q] = a.in + (size_t)max(next[q], 0) * a.K;
+        if (vec) cp_async16(st + spot + 16 * q * S::kInPitch, line[q] + (want[q] ? col : 0), want[q] ? 16 : 0);
+      }
+      if (!vec) {
+        uint4 v[4];
+        read_pieces(v, line, want, col, a.K, a.in + (size_t)g.n_rows * a.K);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sts16(st + spot + 16 * q * S::kInPitch, v[q]);
       }
       fetch(i + 1);
     }

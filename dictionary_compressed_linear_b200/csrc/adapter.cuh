@@ -122,30 +122,69 @@ __device__ __forceinline__ float split_unit(float m) {
   return __uint_as_float((uint32_t)(min(13 - e, 126) + 127) << 23);
 }
 
-// 8 elements from column c of a row of n elements, zeros past the end. Rows of an odd
-// length start at any even byte: two aligned 16-byte loads and a shift, as long as both
-// lie inside the array (which ends at `end`), single elements otherwise.
-__device__ __forceinline__ uint4 read_piece(const __half* row, int c, int n, bool vec, const __half* end) {
-  if (vec) return c < n ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
-  const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
-  const uint4* q = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
-  if (c + 8 <= n && reinterpret_cast<uintptr_t>(q + 2) <= reinterpret_cast<uintptr_t>(end)) {
-    const uint4 a = q[0], b = q[1];
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    const uint32_t words = (uint32_t)(at >> 2) & 3u, shift = 8u * ((uint32_t)at & 2u);
-    if (words & 2) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = w[6], w[5] = w[7];
-    if (words & 1) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
-    return make_uint4(__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift),
-                      __funnelshift_r(w[2], w[3], shift), __funnelshift_r(w[3], w[4], shift));
-  }
+// Rows of a length that is no multiple of 8 start at any even byte. Eight elements from
+// `src` are then two aligned 16-byte loads and a shift, as long as both lie inside the array
+// (which ends at `end`).
+__device__ __forceinline__ const uint4* window_of(const __half* src) {
+  return reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(src) & ~(uintptr_t)15);
+}
+__device__ __forceinline__ bool window_inside(const __half* src, const __half* end) {
+  return reinterpret_cast<uintptr_t>(window_of(src) + 2) <= reinterpret_cast<uintptr_t>(end);
+}
+// The first `left` of the eight elements, zeros behind them.
+__device__ __forceinline__ uint4 shift_window(const uint4& a, const uint4& b, const __half* src, int left) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(src);
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const uint32_t words = (uint32_t)(at >> 2) & 3u, shift = 8u * ((uint32_t)at & 2u);
+  if (words & 2) w[0] = w[2], w[1] = w[3], w[2] = w[4], w[3] = w[5], w[4] = w[6], w[5] = w[7];
+  if (words & 1) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = w[5];
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = __funnelshift_r(w[i], w[i + 1], shift) & (left >= 2 * i + 2 ? 0xFFFFFFFFu : left == 2 * i + 1 ? 0xFFFFu : 0u);
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ uint4 single_elements(const __half* src, int left) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const unsigned short a = c + 2 * i < n ? __half_as_ushort(row[c + 2 * i]) : 0;
-    const unsigned short b = c + 2 * i + 1 < n ? __half_as_ushort(row[c + 2 * i + 1]) : 0;
+    const unsigned short a = 2 * i < left ? __half_as_ushort(src[2 * i]) : 0;
+    const unsigned short b = 2 * i + 1 < left ? __half_as_ushort(src[2 * i + 1]) : 0;
     w[i] = (uint32_t)a | ((uint32_t)b << 16);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// 8 elements from column c of a row of n elements, zeros past the end (vec: n % 8 == 0).
+__device__ __forceinline__ uint4 read_piece(const __half* row, int c, int n, bool vec, const __half* end) {
+  if (vec) return c < n ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+  if (!window_inside(row + c, end)) return single_elements(row + c, n - c);
+  const uint4* q = window_of(row + c);
+  return shift_window(q[0], q[1], row + c, n - c);
+}
+// The same column of several unaligned rows (in: whether a row is wanted), all loads
+// together: one after the other they took 2 us a stage.
+template <int N>
+__device__ __forceinline__ void read_pieces(uint4 (&out)[N], const __half* const (&row)[N], const bool (&in)[N], int c, int n,
+                                            const __half* end) {
+  bool all = true;
+#pragma unroll
+  for (int i = 0; i < N; ++i) all = all && (!in[i] || window_inside(row[i] + c, end));
+  if (all) {
+    uint4 a[N], b[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      a[i] = b[i] = make_uint4(0, 0, 0, 0);
+      if (in[i]) {
+        a[i] = window_of(row[i] + c)[0];
+        b[i] = window_of(row[i] + c)[1];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = shift_window(a[i], b[i], row[i] + c, in[i] ? n - c : 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = in[i] ? read_piece(row[i], c, n, false, end) : make_uint4(0, 0, 0, 0);
+  }
 }
 __device__ __forceinline__ void write_piece(__half* row, int c, int n, bool vec, const uint4& v) {
   if (vec) {

@@ -25,6 +25,8 @@ def ids_of(kind, M, n, seed=1):
     a = {"one": np.zeros(M, int), "each": np.arange(M) % n, "random": g.integers(0, n, M),
          "some": np.where(g.random(M) < 0.3, -1, g.integers(0, n, M)), "none": np.full(M, -1),
          "last": np.full(M, n - 1), "runs": np.sort(g.integers(0, n, M)),
+         # half of the rows in one run of slot 3, the others anywhere (or nowhere)
+         "crowd": np.where(np.arange(M) < M // 2, 3, g.integers(-1, n, M)),
          "wild": g.choice([-7, n, n + 5, 2 ** 31 - 1, -2 ** 31, 0, n - 1], M)}[kind]
     return torch.tensor(a, dtype=torch.int32, device="cuda")
 
@@ -53,7 +55,17 @@ CASES = [  # rows, d_in, d_out, max_rank, ranks, ids
     (300, 320, 2000, 48, [40, 48, 16], "runs"), (1000, 160, 88, 100, [100, 3], "random"), (15, 11008, 40, 80, [80], "one")]
 
 
-@pytest.mark.parametrize("M,d_in,d_out,R,ranks,kind", CASES)
+# batches of many rows: tiles of 64 and 128 rows, runs of rows and scattered ones, slots with many rows beside
+# slots with few, every template rank, widths that end inside a block of columns
+MANY = [
+    (400, 96, 72, 16, [16], "one"), (513, 352, 328, 16, [16, 9, 0], "runs"), (700, 160, 200, 32, [32, 17], "some"),
+    (640, 4096, 1000, 32, [20, 32, 1], "random"), (1500, 224, 136, 64, [64, 33], "runs"), (260, 64, 520, 64, [50], "last"),
+    (900, 288, 1096, 128, [128, 40], "random"), (777, 544, 776, 128, [100, 65, 3], "runs"), (1030, 128, 77, 16, [16, 5], "runs"),
+    (600, 192, 129, 64, [64, 30], "some"), (520, 96, 264, 32, [24] * 40, "crowd"), (1100, 160, 96, 96, [96] * 60, "crowd"),
+    (600, 64, 75, 16, [16] * 50, "crowd"), (300, 64, 64, 16, [16, 8], "none"), (2048, 64, 64, 8, [8] * 9, "wild")]
+
+
+@pytest.mark.parametrize("M,d_in,d_out,R,ranks,kind", CASES + MANY)
 @pytest.mark.parametrize("mode", ["apart", "in place", "zero"])
 def test_forward(M, d_in, d_out, R, ranks, kind, mode):
     pool = ref.Pool(d_in, d_out, R, ranks, seed=M)
@@ -68,7 +80,7 @@ def test_forward(M, d_in, d_out, R, ranks, kind, mode):
     ref.assert_half(Y, want, W, d_in + R, mode)
 
 
-@pytest.mark.parametrize("M,d_in,d_out,R,ranks,kind", CASES)
+@pytest.mark.parametrize("M,d_in,d_out,R,ranks,kind", CASES + MANY)
 def test_backward(M, d_in, d_out, R, ranks, kind):
     pool = ref.Pool(d_in, d_out, R, ranks, seed=M)
     n = len(ranks)
@@ -175,6 +187,65 @@ def test_rows_without_an_adapter_and_foreign_values_stay_apart():
     assert torch.isfinite(dA).all() and torch.isfinite(dB).all()
 
 
+@pytest.mark.parametrize("d_out", [96, 75])
+@pytest.mark.parametrize("order", ["runs", "scattered"])
+def test_many_rows_keep_foreign_values_apart(order, d_out):
+    # slot 0 ends inside a tile; behind it lie rows of slot 1 and of none, full of infinities and NaN
+    M, n0 = 600, 300
+    pool = ref.Pool(128, d_out, 16, [16, 16], seed=2)
+    ids = torch.tensor([0] * n0 + [1] * 200 + [-1] * 100, dtype=torch.int32, device="cuda")
+    if order == "scattered":
+        ids = ids[torch.randperm(M, generator=torch.Generator().manual_seed(1)).cuda()]
+    X, dY, base = normal(M, 128), normal(M, d_out, seed=3), normal(M, d_out, seed=4)
+    X[ids != 0], dY[ids != 0] = float("inf"), NAN
+    mine = ids == 0
+    h, rows = pool.upload(dp, M, stream()), planned(ids, 2)
+    Y, dX = base.clone(), torch.zeros_like(X)
+    dA, dB = torch.empty(2, 16, 128, device="cuda"), torch.empty(2, 16, d_out, device="cuda")
+    dp.dictproj_adapter_forward(h, rows, X.data_ptr(), Y.data_ptr(), Y.data_ptr(), stream())
+    dp.dictproj_adapter_backward(h, rows, X.data_ptr(), dY.data_ptr(), 0, dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), False, stream())
+    torch.cuda.synchronize()
+    one = ref.Pool(128, d_out, 16, [16], seed=2)
+    one.A, one.B, one.scale = pool.A[:1], pool.B[:1], pool.scale[:1]
+    own = ids[mine]
+    want, W = ref.forward(one, own, X[mine], base[mine])
+    ref.assert_half(Y[mine], want, W, 144)
+    assert torch.equal(Y[ids == -1], base[ids == -1])
+    w = ref.backward(one, own, X[mine], dY[mine])
+    ref.assert_half(dX[mine], w["dX"], w["WX"], d_out + 16)
+    ref.assert_float(dA[:1], w["dA"], w["WA"], d_out + n0)
+    ref.assert_float(dB[:1], w["dB"], w["WB"], 128 + n0)
+    assert (dX[ids == -1] == 0).all()
+
+
+def test_two_pools_on_two_streams_at_once():
+    # nothing is shared between pools: their workspaces are their own
+    work = []
+    for k, (M, d_out) in enumerate(((1024, 512), (700, 264))):
+        pool = ref.Pool(256, d_out, 32, [32, 20], seed=k)
+        ids, X, dY = ids_of("runs", M, 2, seed=k), normal(M, 256, seed=k), normal(M, d_out, seed=k + 5)
+        work.append(dict(pool=pool, ids=ids, X=X, dY=dY, h=pool.upload(dp, M, stream()), rows=planned(ids, 2), s=torch.cuda.Stream(),
+                         Y=torch.empty(M, d_out, dtype=torch.float16, device="cuda"), dX=torch.empty_like(X),
+                         dA=torch.empty(2, 32, 256, device="cuda"), dB=torch.empty(2, 32, d_out, device="cuda")))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for w in work:
+            s = w["s"].cuda_stream
+            dp.dictproj_adapter_forward(w["h"], w["rows"], w["X"].data_ptr(), 0, w["Y"].data_ptr(), s)
+            dp.dictproj_adapter_backward(w["h"], w["rows"], w["X"].data_ptr(), w["dY"].data_ptr(), 0, w["dX"].data_ptr(),
+                                         w["dA"].data_ptr(), w["dB"].data_ptr(), False, s)
+    torch.cuda.synchronize()
+    for w in work:
+        want, W = ref.forward(w["pool"], w["ids"], w["X"])
+        ref.assert_half(w["Y"], want, W, 288)
+        b = ref.backward(w["pool"], w["ids"], w["X"], w["dY"])
+        n = w["dY"].shape
+        ref.assert_half(w["dX"], b["dX"], b["WX"], n[1] + 32)
+        ref.assert_float(w["dA"], b["dA"], b["WA"], n[1] + n[0])
+        ref.assert_float(w["dB"], b["dB"], b["WB"], 256 + n[0])
+    assert dp.dictproj_check_status(stream()) == 0
+
+
 @pytest.mark.parametrize("size", [1e-7, 1e4])
 def test_small_and_large_activations_keep_their_digits(size):
     # T is far outside fp16's comfortable range: small gradients must not fall to zero in a sum
@@ -233,9 +304,10 @@ def test_many_slots_and_offsets_past_32_bits():
     ref.assert_half(Y[at], want, W, 33)
 
 
-def test_captured_calls_plan_anew_and_other_streams():
+@pytest.mark.parametrize("M", [20, 600])
+def test_captured_calls_plan_anew_and_other_streams(M):
     pool = ref.Pool(256, 264, 16, [16, 8, 4], seed=2)
-    h, M = pool.upload(dp, 20, stream()), 20
+    h = pool.upload(dp, M, stream())
     ids, X = ids_of("random", M, 3), normal(M, 256)
     rows = dp.dictproj_rows_create(M, 3)
     Y, dX = torch.zeros(M, 264, dtype=torch.float16, device="cuda"), torch.zeros_like(X)
@@ -265,8 +337,8 @@ def test_captured_calls_plan_anew_and_other_streams():
         ref.assert_half(Y, want, W, 272)
         w = ref.backward(pool, ids, X, dY)
         ref.assert_half(dX, w["dX"], w["WX"], 280)
-        ref.assert_float(dA, w["dA"], w["WA"], 284)
-        ref.assert_float(dB, w["dB"], w["WB"], 276)
+        ref.assert_float(dA, w["dA"], w["WA"], 264 + M)
+        ref.assert_float(dB, w["dB"], w["WB"], 256 + M)
 
 
 def _projection(d_in, d_out, k, M, seed=30):
