@@ -585,7 +585,7 @@ struct ExpandShape {
 };
 
 template <int R>
-__global__ void __launch_bounds__(kRowThreads, R == 128 ? 2 : 1) k_adapter_expand(const __grid_constant__ RowsArgs g) {
+__global__ void __launch_bounds__(kRowThreads, R <= 32 ? 3 : 2) k_adapter_expand(const __grid_constant__ RowsArgs g) {
   using S = ExpandShape<R>;
   constexpr int TM = S::TM, CW = S::CW, PITCH = S::kPitch;
   static_assert(kRowThreads == 16 * PITCH / 16, "a thread loads one 16-byte column of every 16th row");

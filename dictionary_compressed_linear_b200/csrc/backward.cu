@@ -29,25 +29,31 @@
 namespace dictproj {
 namespace {
 
-// Dense fp16 copy of D^ (Dd[j][i], E2M1 x E4M3 exact in fp16, without s_D): one
-// thread per 16-value block, 8 + 1 bytes in, 32 bytes out.
-__global__ void __launch_bounds__(256)
-    k_densify_dict(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, long n_blocks,
-                   __half* __restrict__ dd) {
-  grid_dependency_wait();  // Dd may still be read by the previous input-gradient GEMM
-  trigger_dependents();
-  const long b = (long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (b >= n_blocks) return;
-  const uint2 c = ld_stream_v2(codes + 8 * b);
-  const uint32_t sv = dup_lo(e4m3x2_to_f16x2(scales[b]));
+// Dense fp16 copy of D^ (Dd[j][i], E2M1 x E4M3 exact in fp16, without s_D): a thread per
+// 16-value block, 8 + 1 bytes in, 32 bytes out.
+struct DictCopy {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  __half* dd;
+  long n_blocks;
+};
+__device__ __forceinline__ void densify_block(const DictCopy& d, long b) {
+  const uint2 c = ld_stream_v2(d.codes + 8 * b);
+  const uint32_t sv = dup_lo(e4m3x2_to_f16x2(d.scales[b]));
   uint32_t v[8];
   e2m1x8_to_f16x2x4(c.x, *reinterpret_cast<uint32_t(*)[4]>(v));
   e2m1x8_to_f16x2x4(c.y, *reinterpret_cast<uint32_t(*)[4]>(v + 4));
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = hmul2_u32(v[i], sv);
-  uint4* dst = reinterpret_cast<uint4*>(dd + 16 * b);
+  uint4* dst = reinterpret_cast<uint4*>(d.dd + 16 * b);
   dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
   dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
+}
+__global__ void __launch_bounds__(256) k_densify_dict(DictCopy d) {
+  grid_dependency_wait();  // Dd may still be read by the previous input-gradient GEMM
+  trigger_dependents();
+  const long b = (long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (b < d.n_blocks) densify_block(d, b);
 }
 
 constexpr int kNnM = 128, kNnK = 64, kNnMaxN = 256, kNnStages = 4;
@@ -60,10 +66,11 @@ static_assert(kNnM * (kNnSplitN + 4) * 4 <= kNnStages * (kNnABytes + kNnBBytes),
 // One 128 x bn tile (bn a multiple of 64) of out = scale A B. With gridDim.z = S > 1 the S
 // CTAs of a cluster (1, 1, S) take consecutive ranges of the reduction's stages; the fp32
 // partial tiles meet through distributed shared memory, in rank order, each CTA writing its
-// share of the rows.
+// share of the rows. CTAs past the tiles (only without a split, on SMs that the tiles leave
+// idle) make the dense dictionary that the next product reads.
 __global__ void __launch_bounds__(kNnThreads, 1)
     k_gemm_nn(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, int M, int N, int K,
-              int bn, float scale, __half* __restrict__ out) {
+              int bn, float scale, __half* __restrict__ out, int nx, int tiles, const __grid_constant__ DictCopy copy) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint8_t* sb = smem + kNnStages * kNnABytes;
@@ -72,7 +79,14 @@ __global__ void __launch_bounds__(kNnThreads, 1)
   uint64_t* accf = empty + kNnStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n0 = blockIdx.x * bn, m0 = blockIdx.y * kNnM, split = blockIdx.z, nsplit = gridDim.z;
+  if ((int)blockIdx.x >= tiles) {
+    grid_dependency_wait();
+    trigger_dependents();
+    const long step = (long)(gridDim.x - tiles) * kNnThreads;
+    for (long b = (long)(blockIdx.x - tiles) * kNnThreads + threadIdx.x; b < copy.n_blocks; b += step) densify_block(copy, b);
+    return;
+  }
+  const int n0 = blockIdx.x % nx * bn, m0 = blockIdx.x / nx * kNnM, split = blockIdx.z, nsplit = gridDim.z;
   const int nk_all = (K + kNnK - 1) / kNnK, s_lo = (int)((long)nk_all * split / nsplit);
   const int nk = (int)((long)nk_all * (split + 1) / nsplit) - s_lo;
 
@@ -244,10 +258,11 @@ int nn_clusters_that_fit(int S, int n_sm) {
 // fixed part, its stages (0.1 + 0.0014 per column each) and, split, the sum over the cluster.
 struct NnPlan {
   int bn, split;
+  double us;
 };
 NnPlan nn_plan(int M, int N, int K, int n_sm) {
   const int nk = (K + kNnK - 1) / kNnK, rows = (M + kNnM - 1) / kNnM;
-  NnPlan best = {256, 1};
+  NnPlan best = {256, 1, 0.0};
   double cost = 1e30;
   for (int bn = 64; bn <= kNnMaxN; bn += 64) {
     const long tiles = (long)rows * ((N + bn - 1) / bn);
@@ -255,7 +270,7 @@ NnPlan nn_plan(int M, int N, int K, int n_sm) {
       const int fit = nn_clusters_that_fit(S, n_sm);
       if (fit < 1) continue;
       const double t = (double)((tiles + fit - 1) / fit) * (3.0 + (double)((nk + S - 1) / S) * (0.1 + 0.0014 * bn) + (S > 1 ? 2.5 : 0.0));
-      if (t < cost) cost = t, best = {bn, S};
+      if (t < cost) cost = t, best = {bn, S, t};
     }
   }
   return best;
@@ -268,8 +283,8 @@ cudaError_t prepare_backward_kernels(int device) {
   return cudaFuncSetAttribute(k_gemm_nn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNnSmem);
 }
 
-cudaError_t launch_gemm_nn(const __half* A, const __half* B, int M, int N, int K, float scale, __half* out, int n_sm,
-                           cudaStream_t stream) {
+static cudaError_t launch_nn(const __half* A, const __half* B, int M, int N, int K, float scale, __half* out,
+                             const NnPlan& plan, const DictCopy& copy, int helpers, cudaStream_t stream) {
   CUtensorMap ta, tb;
   cudaError_t e = encode_tiled_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, A, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2, kNnK, kNnM,
                                   CU_TENSOR_MAP_SWIZZLE_128B);
@@ -277,10 +292,9 @@ cudaError_t launch_gemm_nn(const __half* A, const __half* B, int M, int N, int K
   e = encode_tiled_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, B, (uint64_t)N, (uint64_t)K, (uint64_t)N * 2, 64, kNnK,
                       CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
-  const NnPlan plan = nn_plan(M, N, K, n_sm);
-  int bn = plan.bn;
+  int bn = plan.bn, nx = (N + bn - 1) / bn, tiles = nx * ((M + kNnM - 1) / kNnM);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((N + bn - 1) / bn, (M + kNnM - 1) / kNnM, plan.split);
+  cfg.gridDim = dim3(tiles + helpers, 1, plan.split);
   cfg.blockDim = dim3(kNnThreads);
   cfg.dynamicSmemBytes = kNnSmem;
   cfg.stream = stream;
@@ -289,23 +303,34 @@ cudaError_t launch_gemm_nn(const __half* A, const __half* B, int M, int N, int K
   set_cluster_z(attr[1], plan.split);
   cfg.attrs = attr;
   cfg.numAttrs = plan.split > 1 ? 2 : 1;
-  void* args[] = {(void*)&ta, (void*)&tb, &M, &N, &K, &bn, &scale, (void*)&out};
+  void* args[] = {(void*)&ta, (void*)&tb, &M, &N, &K, &bn, &scale, (void*)&out, &nx, &tiles, (void*)&copy};
   return cudaLaunchKernelExC(&cfg, (const void*)k_gemm_nn, args);
 }
 
-cudaError_t launch_densify_dict(const dictproj_group* g, __half* Dd, cudaStream_t stream) {
-  const long blocks = (long)g->k * (g->d_in / 16);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((blocks + 255) / 256));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  set_pdl(attr[0]);
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  long n = blocks;
-  void* args[] = {(void*)&g->codes, (void*)&g->scales, &n, (void*)&Dd};
-  return cudaLaunchKernelExC(&cfg, (const void*)k_densify_dict, args);
+cudaError_t launch_backward_input(const dictproj_group* g, const dictproj_layer* l, const __half* dY, int M, __half* z,
+                                  const __half* Cd, __half* Dd, __half* dX, cudaStream_t stream) {
+  cudaError_t e;
+  const DictCopy copy = {g->codes, g->scales, Dd, (long)g->k * (g->d_in / 16)};
+  const NnPlan p = nn_plan(M, g->k, l->d_out, g->n_sm);
+  // SMs that the first product leaves idle make the dense dictionary, where they can in its
+  // time (41 bytes a block at some 60 GB/s an SM): 2048 rows (4096 <- 2048 <- 11008) took 119 us
+  // with a launch for it.
+  const int tiles = (g->k + p.bn - 1) / p.bn * ((M + kNnM - 1) / kNnM), idle = g->n_sm - tiles;
+  int helpers = p.split == 1 && idle >= 8 && copy.n_blocks * 41e-3 / 60 / idle < 0.7 * p.us ? idle : 0;
+  if (!helpers) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((copy.n_blocks + 255) / 256));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    set_pdl(attr[0]);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {(void*)&copy};
+    if ((e = cudaLaunchKernelExC(&cfg, (const void*)k_densify_dict, args))) return e;
+  }
+  if ((e = launch_nn(dY, Cd, M, g->k, l->d_out, l->s, z, p, copy, helpers, stream))) return e;
+  return launch_nn(z, Dd, M, g->d_in, g->k, g->s, dX, nn_plan(M, g->d_in, g->k, g->n_sm), copy, 0, stream);
 }
 
 cudaError_t launch_wait_probe_backward(long long cycles, cudaStream_t stream) {

@@ -118,11 +118,10 @@ cudaError_t launch_densify_coeff(const dictproj_layer* l, __half* Cd, cudaStream
 cudaError_t launch_coeff_prefill(const dictproj_layer* l, const __half* Z, const __half* Cd, int M, __half* Y,
                                  cudaStream_t stream);
 cudaError_t take_prefill_error(unsigned int* out);
-// Input gradient: Dd[j][i] = D^ densified to fp16, [k][d_in]
-cudaError_t launch_densify_dict(const dictproj_group* g, __half* Dd, cudaStream_t stream);
-// out[M][N] = scale A[M][K] B[K][N] (fp16 row-major operands, fp32 accumulation)
-cudaError_t launch_gemm_nn(const __half* A, const __half* B, int M, int N, int K, float scale, __half* out, int n_sm,
-                           cudaStream_t stream);
+// Input gradient of the projection from its densified coefficients Cd: z (fp16 [M][k]) =
+// s_C dY Cd, Dd = D^ densified (fp16 [k][d_in]), dX = s_D z Dd.
+cudaError_t launch_backward_input(const dictproj_group* g, const dictproj_layer* l, const __half* dY, int M, __half* z,
+                                  const __half* Cd, __half* Dd, __half* dX, cudaStream_t stream);
 cudaError_t prepare_backward_kernels(int device);
 cudaError_t take_backward_error(unsigned int* out);
 cudaError_t launch_wait_probe_backward(long long cycles, cudaStream_t stream);

@@ -289,8 +289,10 @@ int dictproj_adapter_backward(const dictproj_adapters* a, const dictproj_rows* r
 }
 
 int dictproj_group_reserve_backward(dictproj_group* g, int max_d_out) {
-  const int st = dictproj_group_reserve_prefill(g, max_d_out);
-  if (st || g->ddense) return st;
+  clear_error();
+  if (!g) return fail(DICTPROJ_ERR_NULL, "group_reserve_backward: NULL handle");
+  int st = check_device(g->device, "group_reserve_backward");
+  if (st || (st = dictproj_group_reserve_prefill(g, max_d_out)) || g->ddense) return st;
   uint16_t* p = nullptr;
   const cudaError_t e = dmalloc((void**)&p, (size_t)g->k * g->d_in * sizeof(uint16_t));
   if (e != cudaSuccess) {
@@ -330,12 +332,9 @@ int dictproj_backward_input(const void* dY, int M, const dictproj_layer* layer, 
   cudaError_t e;
   if ((e = launch_densify_coeff(layer, cd, s)) != cudaSuccess)
     return cuda_fail(e, "backward_input: coefficient densify launch");
-  if ((e = launch_densify_dict(group, dd, s)) != cudaSuccess)
-    return cuda_fail(e, "backward_input: dictionary densify launch");
-  if ((e = launch_gemm_nn(static_cast<const __half*>(dY), cd, M, group->k, layer->d_out, layer->s, z, group->n_sm, s)) != cudaSuccess)
-    return cuda_fail(e, "backward_input: coefficient stage launch");
-  if ((e = launch_gemm_nn(z, dd, M, group->d_in, group->k, group->s, static_cast<__half*>(dX), group->n_sm, s)) != cudaSuccess)
-    return cuda_fail(e, "backward_input: dictionary stage launch");
+  if ((e = launch_backward_input(group, layer, static_cast<const __half*>(dY), M, z, cd, dd, static_cast<__half*>(dX), s)) !=
+      cudaSuccess)
+    return cuda_fail(e, "backward_input: launch");
   return DICTPROJ_OK;
 }
 

@@ -409,11 +409,11 @@ int dictproj_dictionary_stage_prefill(const void* X, int M, const dictproj_group
  * row j of A is the j-th input direction, row j of B the j-th output direction).
  *
  * A pool (dictproj_adapters) owns the device copies of up to n_slots adapters of
- * one projection shape, and the workspaces of the backward pass. A rows plan
+ * one projection shape, and the workspaces of its calls. A rows plan
  * (dictproj_rows) sorts a batch's rows by the slot each row uses; every
- * projection of a step shares one plan. Calls that use the same pool's backward
- * pass, or that read a plan or a slot while another call writes it, must be
- * ordered on one stream (or otherwise serialised). */
+ * projection of a step shares one plan. Like a group, a pool serves one stream at a
+ * time: its calls share its workspaces, captured ones among them. A plan may be read
+ * by several streams, but not while dictproj_rows_set writes it. */
 typedef struct dictproj_adapters dictproj_adapters;
 typedef struct dictproj_rows dictproj_rows;
 
@@ -451,8 +451,10 @@ void dictproj_free_rows(dictproj_rows* rows); /* NULL is a no-op */
 
 /* Plan a batch of M rows: ids device int32[M], ids[m] the slot of row m; any value
  * outside [0, n_slots) means that the row uses no adapter. The ids are read on the
- * device, so a captured call plans anew with what they hold at each replay. Rows
- * of one slot need not be neighbours. Asynchronous on `stream`.
+ * device, so a captured call plans anew with what they hold at each replay; a
+ * captured call keeps the M it was captured with (and one that uses a plan serves at
+ * most the rows planned at its capture). Rows of one slot need not be neighbours,
+ * and are fastest when they are. Asynchronous on `stream`.
  * Errors: NULL, RANGE (M outside [1, max_rows]), ALIGN (ids not 4-byte aligned),
  * MISMATCH (device), CUDA. */
 int dictproj_rows_set(dictproj_rows* rows, const int* ids, int M, void* stream);
@@ -461,9 +463,9 @@ int dictproj_rows_set(dictproj_rows* rows, const int* ids, int M, void* stream);
  * dictproj_rows_set: X device fp16 [M][d_in], base and Y device fp16 [M][d_out].
  * base may be Y itself (the result of a dictproj_forward*: rows without an adapter
  * are then not touched at all) or NULL (base = 0); rows without an adapter get
- * base. T is summed in fp32 and used in two fp16 parts (22 bits or more); Y is
- * rounded once. Masked or unused rows do not reach other rows: an infinity or NaN
- * stays in its own row. Asynchronous on `stream`; one launch.
+ * base. T is summed in fp32 and used in fp32 or in two fp16 parts (22 bits or
+ * more); Y is rounded once. Rows do not reach other rows: an infinity or NaN
+ * stays in its own. Asynchronous on `stream`; up to three launches.
  * Errors: NULL, RANGE (no rows planned, more than the pool's max_tokens, the plan
  * made for another n_slots, Y overlapping X, or overlapping base without being
  * base), ALIGN (16 bytes), MISMATCH (device), CUDA. */
@@ -491,7 +493,8 @@ int dictproj_forward_adapters(const void* X, const dictproj_layer* layer, const 
  * accumulate == 0 overwrites every element of dA and dB: zero where a slot has no
  * rows in the batch and past a slot's rank. accumulate != 0 adds. dX may be NULL
  * (no input gradient) and dA and dB may both be NULL (only dX); not all three. The
- * sums run in fp32 in a fixed order: repeated calls give the same bits.
+ * sums run in fp32 in a fixed order: repeated calls give the same bits. A slot's
+ * gradients are its own rows' alone. At most four launches.
  * Asynchronous on `stream`. Errors as dictproj_adapter_forward (dX must not overlap
  * X or dY, dA and dB must not overlap anything), NULL also when only one of dA, dB
  * is given. */
@@ -692,7 +695,7 @@ int dictproj_diag_gather_times(unsigned long long* buf, int max_ctas);
 
 /* Self-test of the bounded-wait error path (diagnostic; no counterpart in the
  * paper). Launches, on `stream`, one warp per kernel file (decode, prefill, fused
- * decode: each has its own device error word) that waits on an mbarrier which
+ * decode, input gradient, adapters: each has its own device error word) that waits on an mbarrier which
  * can never complete, with a limit of `cycles` SM clocks (1 <= cycles <= 2^31).
  * Each wait gives up at the limit, sets its file's error word and the kernel
  * returns; no copy or tensor-core operation is in flight. A following dictproj_check(stream)

@@ -1,4 +1,8 @@
 """Low-rank adapters of many requests beside a projection: forward, gradients, plans and refusals."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -14,6 +18,7 @@ import synth  # noqa: E402
 from gpu_helpers import device_projection, oracle_forward, oracle_projection  # noqa: E402
 
 NAN = float("nan")
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def stream():
@@ -447,3 +452,38 @@ def test_a_training_step_and_the_serving_of_its_result():
     torch.cuda.synchronize()
     want, W = ref.forward(pool, ids, X, P)
     ref.assert_half(Y, want, W, d_in + r, "served after the step")
+
+
+@pytest.mark.parametrize("kind", ["alloc", "copy"])
+def test_injected_host_faults_leave_nothing_allocated(kind):
+    code = (
+        "import torch, dictionary_compressed_linear_b200 as dp\n"
+        "x = torch.zeros(1 << 20, device='cuda')\n"
+        "import os; os.environ['DICTPROJ_FAULT'] = ''\n"
+        "free0 = torch.cuda.mem_get_info()[0]\n"
+        f"os.environ['DICTPROJ_FAULT'] = '{kind}'\n"
+        "t = [{'p': x.data_ptr(), 'g': x.data_ptr(), 'm': x.data_ptr(), 'v': x.data_ptr(), 'n': 1 << 20}] * 500\n"
+        "calls = {'adamw': lambda: dp.dictproj_adamw_create(t, 32)}\n"
+        f"if '{kind}' == 'alloc':\n"
+        "    calls.update(pool=lambda: dp.dictproj_adapters_create(4096, 11008, 64, 64, 2048),\n"
+        "                 rows=lambda: dp.dictproj_rows_create(1 << 20, 1024))\n"
+        f"want = {{'alloc': -7, 'copy': -6}}['{kind}']\n"
+        "for name, call in calls.items():\n"
+        "    for _ in range(20):\n"
+        "        try:\n"
+        "            call()\n"
+        "            raise SystemExit('no error from ' + name)\n"
+        "        except dp.DictprojError as e:\n"
+        "            assert e.status == want, (name, e)\n"
+        "free1 = torch.cuda.mem_get_info()[0]\n"
+        "assert free0 - free1 < 32 << 20, (free0, free1)\n"
+        "print('ok')\n")
+    env = dict(os.environ, DICTPROJ_FAULT="", PYTHONPATH=ROOT)
+    r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stdout + r.stderr
+
+
+def test_a_wait_that_gives_up_is_reported_by_every_kernel_file():
+    dp.dictproj_selftest_wait_timeout(100000, stream())
+    assert dp.dictproj_check_status(stream()) == -8
+    assert dp.dictproj_check_status(stream()) == 0  # every word is cleared
