@@ -595,13 +595,13 @@ __global__ void __launch_bounds__(kRowThreads, R <= 32 ? 3 : 2) k_adapter_expand
   trigger_dependents();
   const int tile_no = blockIdx.y;
   const bool in_place = a.base == a.out;
-  const int4 tile = g.tiles[tile_no];
+  const int4 tile = __ldcg(g.tiles + tile_no);
   if (!takes_tile(g, tile_no, tile, in_place)) {
     grid_dependency_wait();
     return;
   }
   const int count = tile.z & (kCrowdTile - 1), slot = tile.x;
-  const int r = slot < g.n_slots ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
+  const int r = slot < g.n_slots ? __ldcg(g.rank + slot) : 0, r16 = (r + 15) & ~15;
   const bool vec = (a.N & 7) == 0;
   // the CTAs of a tile take its column blocks in turn, so that they read and write
   // neighbouring parts of the rows at the same time
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kRowThreads, R <= 32 ? 3 : 2) k_adapter_expand
   const uint32_t spot = smem_u32(smem) + swz<PITCH>(row0, piece);
   int row[TM / 16];
 #pragma unroll
-  for (int i = 0; i < TM / 16; ++i) row[i] = row0 + 16 * i < count ? g.perm[tile.y + row0 + 16 * i] : -1;
+  for (int i = 0; i < TM / 16; ++i) row[i] = row0 + 16 * i < count ? __ldcg(g.perm + tile.y + row0 + 16 * i) : -1;
   const __half* wq = a.Q + ((size_t)slot * g.rp + row0) * a.ld_q;
   auto issue = [&](int i) {
     if (i < nb) {
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(kRowThreads, R <= 32 ? 3 : 2) k_adapter_expand
     cp_async_commit();
   };
   for (int i = 0; i < S::kStages - 1; ++i) issue(i);
-  grid_dependency_wait();
+  if (!g.last) grid_dependency_wait();
   const int rg = warp & 3, half = warp >> 2, g0 = rg * 16 + (lane >> 2), c0 = 2 * (lane & 3);
   uint32_t thi[R / 16][4], tlo[R / 16][4];
 #pragma unroll
@@ -656,10 +656,10 @@ __global__ void __launch_bounds__(kRowThreads, R <= 32 ? 3 : 2) k_adapter_expand
     for (int q = 0; q < 4; ++q) {
       const __half* at = a.parts + (size_t)(tile_no * TM + g0 + 8 * (q & 1)) * (2 * g.pp) + 16 * t + c0 + 8 * (q >> 1);
       const bool in = 16 * t < r16;
-      thi[t][q] = in ? *reinterpret_cast<const uint32_t*>(at) : 0u;
-      tlo[t][q] = in ? *reinterpret_cast<const uint32_t*>(at + g.pp) : 0u;
+      thi[t][q] = in ? __ldcg(reinterpret_cast<const uint32_t*>(at)) : 0u;
+      tlo[t][q] = in ? __ldcg(reinterpret_cast<const uint32_t*>(at + g.pp)) : 0u;
     }
-  const float back = a.unit[tile_no];
+  const float back = __ldcg(a.unit + tile_no);
   constexpr int NT = CW / 16;  // 8-column tiles of a warp
   const int cw = 8 * NT * half;
   for (int i = 0; i < nb; ++i) {
@@ -701,6 +701,7 @@ __global__ void __launch_bounds__(kRowThreads, R <= 32 ? 3 : 2) k_adapter_expand
       if (row[q] >= 0) write_piece(a.out + (size_t)row[q] * a.N, c, a.N, vec, lds_u32x4(spot + off + 16 * q * PITCH));
   }
   cp_async_wait<0>();
+  if (g.last) grid_dependency_wait();  // who waits for this launch waits for the gradients too
 }
 
 // ---- weight gradients --------------------------------------------------------------------
@@ -730,13 +731,12 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
   const GradPass& a = g.pass[which];
   const int col0 = ((int)blockIdx.x - (which ? g.pass[0].blocks : 0)) * kGradCols;
   const uint32_t ring = smem_u32(smem);
-  trigger_dependents();
   if (slot < 0) {
     grid_dependency_wait();
     return;
   }
-  const int p0 = g.start[slot], rows = g.start[slot + 1] - p0, tile0 = g.first64[slot];
-  const int r = rows ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
+  const int p0 = __ldcg(g.start + slot), rows = __ldcg(g.start + slot + 1) - p0, tile0 = __ldcg(g.first64 + slot);
+  const int r = rows ? __ldcg(g.rank + slot) : 0, r16 = (r + 15) & ~15;
   float* out = a.g + (size_t)slot * g.max_rank * a.K;
   const int width = min(kGradCols, a.K - col0);
   if (r == 0) {
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int p = (t_lo + i) * 64 + row0 + 16 * q;
-      next[q] = i < nt && p < rows ? g.perm[p0 + p] : -1;
+      next[q] = i < nt && p < rows ? __ldcg(g.perm + p0 + p) : -1;
     }
   };
   auto issue_in = [&](int i) {
@@ -798,6 +798,7 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
   fetch(0);
   for (int i = 0; i < S::kStages - 1; ++i) issue_in(i);
   grid_dependency_wait();  // T is the call's own; the rest was there before the call
+  trigger_dependents();    // the expansion starts on the contraction's end and does not wait for this launch
   for (int i = 0; i < S::kStages - 1; ++i) issue_t(i);
   float sum[R / 16][2][4];
 #pragma unroll
@@ -810,7 +811,7 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
     issue_in(i + S::kStages - 1);
     issue_t(i + S::kStages - 1);
     const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
-    const float unit = a.unit[tile0 + t_lo + i];
+    const float unit = __ldcg(a.unit + tile0 + t_lo + i);
     uint32_t bf[4][4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -895,7 +896,7 @@ __global__ void __launch_bounds__(kFewGradThreads) k_grad_few(const __grid_const
   const int c = ((int)blockIdx.x - (which ? g.pass[0].blocks : 0)) * kFewGradCols + 4 * threadIdx.x;
   // what the call found is read before the wait on its first kernel (see the expansion)
   trigger_dependents();
-  const int p0 = g.start[slot], r = g.rank[slot], p1 = r > j0 ? g.start[slot + 1] : p0;
+  const int p0 = __ldcg(g.start + slot), r = __ldcg(g.rank + slot), p1 = r > j0 ? __ldcg(g.start + slot + 1) : p0;
   const bool vec = (a.K & 3) == 0;
   // eight rows at a time, their loads together: one row's took 0.6 us after the other's
   constexpr int kAhead = 8;
@@ -903,17 +904,18 @@ __global__ void __launch_bounds__(kFewGradThreads) k_grad_few(const __grid_const
   auto fetch = [&](int p) {
     int row[kAhead];
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q) row[q] = g.perm[min(p + q, p1 - 1)];
+    for (int q = 0; q < kAhead; ++q) row[q] = __ldcg(g.perm + min(p + q, p1 - 1));
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) {
       const __half* h = a.in + (size_t)row[q] * a.K + c;
       x[q] = make_uint2(0, 0);
       if (p + q >= p1 || c >= a.K) continue;
       if (vec) {
-        x[q] = *reinterpret_cast<const uint2*>(h);
+        x[q] = __ldcg(reinterpret_cast<const uint2*>(h));
       } else {
-        const unsigned short e0 = __half_as_ushort(h[0]), e1 = c + 1 < a.K ? __half_as_ushort(h[1]) : 0;
-        const unsigned short e2 = c + 2 < a.K ? __half_as_ushort(h[2]) : 0, e3 = c + 3 < a.K ? __half_as_ushort(h[3]) : 0;
+        const unsigned short* u = reinterpret_cast<const unsigned short*>(h);
+        const unsigned short e0 = __ldcg(u), e1 = c + 1 < a.K ? __ldcg(u + 1) : 0;
+        const unsigned short e2 = c + 2 < a.K ? __ldcg(u + 2) : 0, e3 = c + 3 < a.K ? __ldcg(u + 3) : 0;
         x[q] = make_uint2((uint32_t)e0 | (uint32_t)e1 << 16, (uint32_t)e2 | (uint32_t)e3 << 16);
       }
     }
@@ -928,7 +930,7 @@ __global__ void __launch_bounds__(kFewGradThreads) k_grad_few(const __grid_const
     for (int q = 0; q < kAhead; ++q) {
       // past the end x is 0 beside a repeated row's T
       const float4* t = reinterpret_cast<const float4*>(a.sums + (size_t)min(p + q, p1 - 1) * g.pp + j0);
-      const float4 t0 = t[0], t1 = t[1];
+      const float4 t0 = __ldcg(t), t1 = __ldcg(t + 1);
       const float tv[kFewGradRanks] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
       const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&x[q].x)), hi = __half22float2(*reinterpret_cast<const __half2*>(&x[q].y));
 #pragma unroll
@@ -1156,6 +1158,19 @@ cudaError_t launch_adapter_forward(const dictproj_adapters* a, const dictproj_ro
   return e == cudaSuccess ? launch_expand(g, a, r, stream) : e;
 }
 
+static cudaError_t launch_grads(const GradArgs& w, const dictproj_adapters* a, const dictproj_rows* r, int slots,
+                                cudaStream_t stream) {
+  if (tall_serves(a, r)) return launch_grad_tall(w, a, r, stream);
+  const int blocks = w.pass[0].blocks + w.pass[1].blocks;
+  int split = 1;
+  while (split < 8 && blocks * slots * split < 3 * a->n_sm && 64 * slots * split < r->M) split *= 2;
+  const dim3 grid(blocks, slots, split);
+  if (a->rp <= 16) return launch_grad<16>(w, grid, stream);
+  if (a->rp <= 32) return launch_grad<32>(w, grid, stream);
+  if (a->rp <= 64) return launch_grad<64>(w, grid, stream);
+  return launch_grad<128>(w, grid, stream);
+}
+
 cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_rows* r, const __half* X,
                                     const __half* dY, const __half* base, __half* dX, float* dA, float* dB,
                                     bool accumulate, cudaStream_t stream) {
@@ -1210,18 +1225,14 @@ cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_r
     const cudaError_t z = launch_pdl((const void*)k_zero_unused, dim3(per, a->n_slots), dim3(256), 0, stream, args);
     if (z != cudaSuccess) return z;
   }
+  // The gradients before the expansion, which needs only the contraction: they let it start
+  // when their own wait for the contraction is over, it reads T without a wait of its own and
+  // fills the SMs that they leave, and waits for them at its end.
   cudaError_t e = launch_contract(g, dA ? 2 : 1, a, r, stream);
-  if (e == cudaSuccess && dX) e = launch_expand(g, a, r, stream);
-  if (e != cudaSuccess || !dA) return e;
-  if (tall_serves(a, r)) return launch_grad_tall(w, a, r, stream);
-  const int blocks = w.pass[0].blocks + w.pass[1].blocks;
-  int split = 1;
-  while (split < 8 && blocks * slots * split < 3 * a->n_sm && 64 * slots * split < r->M) split *= 2;
-  const dim3 grid(blocks, slots, split);
-  if (a->rp <= 16) return launch_grad<16>(w, grid, stream);
-  if (a->rp <= 32) return launch_grad<32>(w, grid, stream);
-  if (a->rp <= 64) return launch_grad<64>(w, grid, stream);
-  return launch_grad<128>(w, grid, stream);
+  if (e == cudaSuccess && dA) e = launch_grads(w, a, r, slots, stream);
+  if (e != cudaSuccess || !dX) return e;
+  g.last = dA != nullptr;
+  return launch_expand(g, a, r, stream);
 }
 
 }  // namespace dictproj

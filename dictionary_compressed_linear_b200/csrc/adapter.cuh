@@ -36,6 +36,7 @@ struct RowsArgs {
   const float* scale;
   int rp, pp, n_slots, rows, cluster;
   int only;  // -1: every tile; 0: no crowds' tiles; 1: crowds' tiles alone
+  int last;  // the expansion follows the weight gradients (see launch_adapter_backward), not the contraction
 };
 
 struct GradPass {
@@ -62,8 +63,12 @@ struct GradArgs {
 // The slot of a gradient CTA (blockIdx.y counts the slots that have rows), -1: none.
 __device__ __forceinline__ int grad_slot(const GradArgs& g) {
   if (!g.zeroed) return blockIdx.y;
-  return (int)blockIdx.y < *g.n_used ? g.used[blockIdx.y] : -1;
+  return (int)blockIdx.y < __ldcg(g.n_used) ? __ldcg(g.used + blockIdx.y) : -1;
 }
+
+// Kernels that start before the launch ahead of them has ended read what was there before
+// the call through L2 (__ldcg, cp.async.cg, TMA): a line of an earlier launch that an SM's L1
+// may still hold is not what they want.
 
 // ---- clusters and distributed shared memory
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -148,18 +153,18 @@ __device__ __forceinline__ uint4 single_elements(const __half* src, int left) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const unsigned short a = 2 * i < left ? __half_as_ushort(src[2 * i]) : 0;
-    const unsigned short b = 2 * i + 1 < left ? __half_as_ushort(src[2 * i + 1]) : 0;
+    const unsigned short* h = reinterpret_cast<const unsigned short*>(src) + 2 * i;
+    const unsigned short a = 2 * i < left ? __ldcg(h) : 0, b = 2 * i + 1 < left ? __ldcg(h + 1) : 0;
     w[i] = (uint32_t)a | ((uint32_t)b << 16);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // 8 elements from column c of a row of n elements, zeros past the end (vec: n % 8 == 0).
 __device__ __forceinline__ uint4 read_piece(const __half* row, int c, int n, bool vec, const __half* end) {
-  if (vec) return c < n ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+  if (vec) return c < n ? __ldcg(reinterpret_cast<const uint4*>(row + c)) : make_uint4(0, 0, 0, 0);
   if (!window_inside(row + c, end)) return single_elements(row + c, n - c);
   const uint4* q = window_of(row + c);
-  return shift_window(q[0], q[1], row + c, n - c);
+  return shift_window(__ldcg(q), __ldcg(q + 1), row + c, n - c);
 }
 // The same column of several unaligned rows (in: whether a row is wanted), all loads
 // together: one after the other they took 2 us a stage.
@@ -175,8 +180,8 @@ __device__ __forceinline__ void read_pieces(uint4 (&out)[N], const __half* const
     for (int i = 0; i < N; ++i) {
       a[i] = b[i] = make_uint4(0, 0, 0, 0);
       if (in[i]) {
-        a[i] = window_of(row[i] + c)[0];
-        b[i] = window_of(row[i] + c)[1];
+        a[i] = __ldcg(window_of(row[i] + c));
+        b[i] = __ldcg(window_of(row[i] + c) + 1);
       }
     }
 #pragma unroll
@@ -224,7 +229,7 @@ __device__ __forceinline__ void copy_rows(const RowsPass& a, int n_rows, const i
 // Whether a launch is to take a tile (slots' and, unless the output is in place, those of
 // rows without an adapter).
 __device__ __forceinline__ bool takes_tile(const RowsArgs& g, int tile_no, const int4& tile, bool in_place) {
-  return tile_no < g.n_tiles[in_place ? 0 : 1] && (g.only < 0 || g.only == (tile.z >= kCrowdTile ? 1 : 0));
+  return tile_no < __ldcg(g.n_tiles + (in_place ? 0 : 1)) && (g.only < 0 || g.only == (tile.z >= kCrowdTile ? 1 : 0));
 }
 
 // Zeros over `width` columns of rows [0, n) of a gradient, shared by `parts` CTAs.

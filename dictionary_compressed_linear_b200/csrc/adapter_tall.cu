@@ -288,11 +288,11 @@ __global__ void __launch_bounds__(kExpandThreads) k_expand_tall(const __grid_con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, stages = args.stages;
   const int tile_no = blockIdx.y, parts = gridDim.x, b0 = blockIdx.x;
   const bool in_place = a.base == a.out;
-  const int4 tile = g.tiles[tile_no];
-  const int run_row = g.runs[tile_no];
+  const int4 tile = __ldcg(g.tiles + tile_no);
+  const int run_row = __ldcg(g.runs + tile_no);
   const bool live = takes_tile(g, tile_no, tile, in_place);
   const int count = tile.z & (kCrowdTile - 1), slot = tile.x;
-  const int r = live && slot < g.n_slots ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
+  const int r = live && slot < g.n_slots ? __ldcg(g.rank + slot) : 0, r16 = (r + 15) & ~15;
   const int blocks = (a.N + kCols - 1) / kCols, nb = (blocks - b0 + parts - 1) / parts;
   if (r == 0) {  // no tile, or base alone
     trigger_dependents();
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_expand_tall(const __grid_con
     tma_prefetch_map(&args.parts);
   }
   if (warp == 1) tmem_alloc(&tmem_slot, S::kTmem);
-  for (int i = threadIdx.x; i < kTallRows; i += kExpandThreads) srow[i] = g.perm[tile.y + min(i, count - 1)];
+  for (int i = threadIdx.x; i < kTallRows; i += kExpandThreads) srow[i] = __ldcg(g.perm + tile.y + min(i, count - 1));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_expand_tall(const __grid_con
     };
     const int first = min(stages, nb);
     for (int i = 0; i < first; ++i) load(i);
-    grid_dependency_wait();
+    if (!g.last) grid_dependency_wait();
     {  // T: chunks of 64 of a row's 2 R elements, 64 rows a box; past the tile's rows whatever is there
       const int half = S::kTChunks / 2, used = R <= 64 ? S::kTChunks : r16 > 64 ? 4 : 2;
       if (lane == 0) mbar_arrive_expect_tx(&tfull, used * kTallRows * 128);
@@ -391,10 +391,10 @@ __global__ void __launch_bounds__(kExpandThreads) k_expand_tall(const __grid_con
   }
   __syncwarp();
   if (warp >= 2) {
-    grid_dependency_wait();  // the units are the contraction's, and it may still read what out replaces
+    if (!g.last) grid_dependency_wait();  // the units are the contraction's
     const int q = warp & 3, h = (warp - 2) >> 2, tr = 32 * q + lane;
     const uint32_t mine = smem_u32(smem + S::kTBytes) + (warp - 2) * 2048;
-    const float back = a.unit[tile.w + (tr >= kWideRows && count > kWideRows ? 1 : 0)];
+    const float back = __ldcg(a.unit + tile.w + (tr >= kWideRows && count > kWideRows ? 1 : 0));
     RingPos at;
     for (int i = 0; i < nb; ++i, at.next(stages)) {
       const uint32_t st = smem_u32(ring + at.slot * S::kStageBytes);
@@ -431,9 +431,8 @@ __global__ void __launch_bounds__(kExpandThreads) k_expand_tall(const __grid_con
       }
       __syncwarp();
     }
-  } else {
-    grid_dependency_wait();
   }
+  grid_dependency_wait();  // who waits for this launch waits for those before it too
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -480,7 +479,6 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, stages = args.stages;
   const int split = blockIdx.z, nsplit = gridDim.z, slot = grad_slot(g);
   if (slot < 0) {
-    trigger_dependents();
     grid_dependency_wait();
     return;
   }
@@ -489,12 +487,11 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
   const int col0 = ((int)blockIdx.x - (which ? g.pass[0].blocks : 0)) * kGradCols;
   // The launch before is the expansion or the contraction of the same call: what was there
   // before the call (plan, ranks, In) is complete and may be read before the wait.
-  const int p0 = g.start[slot], rows = g.start[slot + 1] - p0, tile0 = g.first64[slot];
-  const int r = rows ? g.rank[slot] : 0, r16 = (r + 15) & ~15;
+  const int p0 = __ldcg(g.start + slot), rows = __ldcg(g.start + slot + 1) - p0, tile0 = __ldcg(g.first64 + slot);
+  const int r = rows ? __ldcg(g.rank + slot) : 0, r16 = (r + 15) & ~15;
   float* out = a.g + (size_t)slot * g.max_rank * a.K;
   const int width = min(kGradCols, a.K - col0);
   if (r == 0) {
-    trigger_dependents();
     grid_dependency_wait();
     if (!g.zeroed && !g.accumulate) zero_columns(out + col0, a.K, width, g.max_rank, split, nsplit);
     return;
@@ -518,7 +515,6 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  trigger_dependents();  // not before the tensor memory is ours
   const uint32_t tmem = tmem_slot;
 
   if (warp == 0) {
@@ -529,7 +525,7 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
     // In's part of stage s: a whole tile of rows in a run as two boxes. Rows past the slot's
     // end must not be others' (0 * inf): the ragged tile gathers, repeating its last row (T
     // is zero there). Whether a tile is a run is loaded one stage ahead.
-    int next = nt > 0 ? g.runs[tile0 + t_lo] : -1;
+    int next = nt > 0 ? __ldcg(g.runs + tile0 + t_lo) : -1;
     auto gather = [&](int s) {
       const uint32_t st = smem_u32(smem + s % stages * S::kStageBytes);
       const int row_a = next;
@@ -538,10 +534,10 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
       } else {
         int row[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) row[q] = g.perm[p0 + min((t_lo + s) * kWideRows + r4 + q, rows - 1)];
+        for (int q = 0; q < 4; ++q) row[q] = __ldcg(g.perm + p0 + min((t_lo + s) * kWideRows + r4 + q, rows - 1));
         tma_gather4(st + 8192 * chunk + 128 * r4, &args.in[which], x, row[0], row[1], row[2], row[3], &full[s % stages]);
       }
-      next = s + 1 < nt ? g.runs[tile0 + t_lo + s + 1] : -1;
+      next = s + 1 < nt ? __ldcg(g.runs + tile0 + t_lo + s + 1) : -1;
     };
     auto parts = [&](int s) {
       if (lane < used) {
@@ -557,6 +553,7 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
       gather(s);
     }
     grid_dependency_wait();
+    trigger_dependents();  // all CTAs hold their tensor memory; the expansion may start on the contraction's end
     for (int s = 0; s < first; ++s) parts(s);
     for (int s = first; s < nt; ++s) {
       bool ok = true;
@@ -600,14 +597,15 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
   float* part = reinterpret_cast<float*>(smem);  // [R][128], over the drained ring
   if (warp >= 2) {
     grid_dependency_wait();  // the units are the contraction's
+    trigger_dependents();
     const int q = warp & 3;
     float sum[R];
 #pragma unroll
     for (int j = 0; j < R; ++j) sum[j] = 0.f;
-    float next = nt > 0 ? a.unit[tile0 + t_lo] : 0.f;
+    float next = nt > 0 ? __ldcg(a.unit + tile0 + t_lo) : 0.f;
     for (int s = 0; s < nt; ++s) {
       const float unit = next;
-      if (s + 1 < nt) next = a.unit[tile0 + t_lo + s + 1];
+      if (s + 1 < nt) next = __ldcg(a.unit + tile0 + t_lo + s + 1);
       if (!mbar_wait_bounded(&dfull[s & 1], (s / 2) & 1)) break;
       tc_fence_after();
 #pragma unroll
@@ -634,7 +632,7 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
     // operand of the ring is in use any more
 #pragma unroll
     for (int j = 0; j < R; ++j) part[j * kGradCols + 32 * q + lane] = sum[j];
-  } else {
+  } else if (warp == 1) {
     grid_dependency_wait();
   }
   tc_fence_before();
@@ -733,8 +731,10 @@ Ring plan_ring(int stage_bytes, int part_bytes, int fixed_bytes, int work, int s
   return r;
 }
 // CTAs of an SM: two (clusters of eight with one an SM leave SMs idle: 16 of them fit a
-// GPU of 148), or three where there are more than two anyway.
-int sm_share(long ctas, int n_sm) { return ctas > 2l * n_sm ? 3 : 2; }
+// GPU of 148), or three where there are more than that anyway
+// (384 CTAs of the gradients, 8192 rows of rank 64: the whole pass 101.8 us with two, 106.4
+// with three).
+int sm_share(long ctas, int n_sm) { return ctas > 3l * n_sm ? 3 : 2; }
 
 template <int R>
 cudaError_t allow_tall() {
