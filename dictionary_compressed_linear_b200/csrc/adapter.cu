@@ -1045,9 +1045,9 @@ cudaError_t launch_few(const RowsArgs& g, int passes, const dictproj_rows* r, cu
                     dim3(kRowThreads), 0, stream, args, dim3(kCluster, 1, 1));
 #undef FEW
 }
-cudaError_t launch_contract(RowsArgs& g, int passes, const dictproj_adapters* pool, const dictproj_rows* r, cudaStream_t stream) {
+cudaError_t launch_contract(RowsArgs& g, int passes, bool exact_sums, const dictproj_adapters* pool, const dictproj_rows* r, cudaStream_t stream) {
   const int n_sm = pool->n_sm;
-  if (tall_serves(pool, r)) return launch_contract_tall(g, passes, pool, r, stream);
+  if (tall_serves(pool, r)) return launch_contract_tall(g, passes, exact_sums, pool, r, stream);
   const int tiles = adapter_tiles(r->M, r->n_slots, kWideRows);
   const int full = r->M / kWideRows * passes;  // tiles that do exist, about
   g.cluster = 2;
@@ -1154,7 +1154,7 @@ cudaError_t launch_adapter_forward(const dictproj_adapters* a, const dictproj_ro
   g.pass[0] = rows_pass(a, true, X, base, Y);
   if (!all) g.only = 1;
   set_parts(a, g);
-  e = launch_contract(g, 1, a, r, stream);
+  e = launch_contract(g, 1, false, a, r, stream);
   return e == cudaSuccess ? launch_expand(g, a, r, stream) : e;
 }
 
@@ -1228,7 +1228,7 @@ cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_r
   // The gradients before the expansion, which needs only the contraction: they let it start
   // when their own wait for the contraction is over, it reads T without a wait of its own and
   // fills the SMs that they leave, and waits for them at its end.
-  cudaError_t e = launch_contract(g, dA ? 2 : 1, a, r, stream);
+  cudaError_t e = launch_contract(g, dA ? 2 : 1, dA != nullptr, a, r, stream);
   if (e == cudaSuccess && dA) e = launch_grads(w, a, r, slots, stream);
   if (e != cudaSuccess || !dX) return e;
   g.last = dA != nullptr;

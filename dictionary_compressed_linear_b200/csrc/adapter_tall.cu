@@ -40,10 +40,15 @@ constexpr int kCols = 64;          // columns of a stage (one 128-byte swizzle r
 // stage 128 gathered rows of In (16 KB) and r rows of P_s; D = In P^T, rows x r, in tensor
 // memory. The CTAs' partial sums meet through distributed shared memory, in rank order;
 // each CTA writes its share of the rows as two fp16 parts, with a unit for each 64 rows.
+// A long accumulation on the tensor cores is less exact than fp32 sums: with all of K in one
+// accumulator the weight gradients of 2048 rows came out more than 1e-6 off (relative norm).
+// For them every `flush` stages get an accumulator of their own (two in turn), which the
+// epilogue warps add in fp32 (3e-7, at no cost in time); the forward's fp16 result takes one
+// for all.
 struct TallContractArgs {
   CUtensorMap in[2], box[2], p[2];  // In by single rows and by 64, P by 16
   RowsArgs g;
-  int stages;
+  int stages, flush;
 };
 
 constexpr int kMaxStages = 12;
@@ -53,7 +58,7 @@ struct TallContract {
   static constexpr int kInBytes = kTallRows * 128, kStageBytes = kInBytes + R * 128;
   static constexpr int kPitch = R + 4;  // floats of a row of the partial sums, which lie over the drained ring
   static constexpr int kPart = kTallRows * kPitch * 4;
-  static constexpr int kTmem = R < 32 ? 32 : R;
+  static constexpr int kTmem = 2 * R;
 };
 
 template <int R>
@@ -61,7 +66,7 @@ __global__ void __launch_bounds__(kTallThreads) k_contract_tall(const __grid_con
   using S = TallContract<R>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], accf;
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], dfull[2], dempty[2];
   __shared__ uint32_t tmem_slot;
   __shared__ float smax[2][kTallThreads / 32], cmax[2][8];
   const RowsArgs& g = args.g;
@@ -74,7 +79,10 @@ __global__ void __launch_bounds__(kTallThreads) k_contract_tall(const __grid_con
       mbar_init(&full[s], 2);  // In's bytes and P's are announced apart
       mbar_init(&empty[s], 1);
     }
-    mbar_init(&accf, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&dfull[s], 1);
+      mbar_init(&dempty[s], 4);
+    }
     fence_mbar_init();
     tma_prefetch_map(&args.box[blockIdx.y]);
     tma_prefetch_map(&args.p[blockIdx.y]);
@@ -152,36 +160,53 @@ __global__ void __launch_bounds__(kTallThreads) k_contract_tall(const __grid_con
       const uint32_t idesc = (1u << 4) | ((uint32_t)(r16 >> 3) << 17) | ((uint32_t)(kTallRows >> 4) << 24);
       const uint64_t in0 = smem_desc_sw128(smem_u32(smem)), p0 = smem_desc_sw128(smem_u32(smem) + S::kInBytes);
       RingPos at;
+      int group = 0, in_group = 0;  // accumulators done, stages in the present one
       for (int s = 0; s < nk; ++s, at.next(stages)) {
+        const int d = group & 1;
+        if (in_group == 0 && group >= 2 && !mbar_wait_bounded(&dempty[d], (group / 2 - 1) & 1)) break;
         if (!mbar_wait_bounded(&full[at.slot], at.phase)) break;
         tc_fence_after();
         const uint32_t off = at.slot * S::kStageBytes;
         const uint64_t in = desc_at(in0, off), pd = desc_at(p0, off);
 #pragma unroll
         for (int j = 0; j < kCols / 16; ++j)
-          mma_f16_ss(tmem, desc_at(in, 32 * j), desc_at(pd, 32 * j), idesc, (s | j) != 0);
+          mma_f16_ss(tmem + d * R, desc_at(in, 32 * j), desc_at(pd, 32 * j), idesc, (in_group | j) != 0);
         mma_commit(&empty[at.slot]);
+        if (++in_group == args.flush || s == nk - 1) {
+          mma_commit(&dfull[d]);
+          ++group, in_group = 0;
+        }
       }
-      mma_commit(&accf);
     }
   }
   __syncwarp();
   float* part = reinterpret_cast<float*>(smem);  // [128][kPitch], over the drained ring
   if (warp >= 2) {
-    const int q = warp & 3, tr = 32 * q + lane;
-    const bool ok = mbar_wait_bounded(&accf, 0);
-    tc_fence_after();
+    const int q = warp & 3, tr = 32 * q + lane, groups = (nk + args.flush - 1) / args.flush;
+    float sum[R];
 #pragma unroll
-    for (int t = 0; t < R / 16; ++t) {
-      if (16 * t >= r16) break;
-      uint32_t v[16];
-      tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + 16 * t, v);
+    for (int j = 0; j < R; ++j) sum[j] = 0.f;
+    for (int k = 0; k < groups; ++k) {
+      if (!mbar_wait_bounded(&dfull[k & 1], (k / 2) & 1)) break;
+      tc_fence_after();
 #pragma unroll
-      for (int e = 0; e < 16; e += 4)
-        *reinterpret_cast<float4*>(part + tr * S::kPitch + 16 * t + e) =
-            ok && nk > 0 ? make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]))
-                         : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int t = 0; t < R / 16; ++t) {
+        if (16 * t >= r16) break;
+        uint32_t v[16];
+        tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + (k & 1) * R + 16 * t, v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum[16 * t + e] += __uint_as_float(v[e]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dempty[k & 1]);
     }
+    // the last accumulator was read: no operand of the ring is in use any more (all four warps
+    // have to be here, since the sums of one lie where another's last operands may)
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < R; j += 4)
+      if (j < r16) *reinterpret_cast<float4*>(part + tr * S::kPitch + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
   }
   tc_fence_before();
   cluster_arrive();
@@ -789,7 +814,7 @@ struct TallKernel {
    : (rp) <= 64 ? DICTPROJ_TALL_R(kernel, shape, 64)      \
                 : DICTPROJ_TALL_R(kernel, shape, 128))
 
-cudaError_t launch_contract_tall(RowsArgs& g, int passes, const dictproj_adapters* a, const dictproj_rows* r,
+cudaError_t launch_contract_tall(RowsArgs& g, int passes, bool exact_sums, const dictproj_adapters* a, const dictproj_rows* r,
                                  cudaStream_t stream) {
   TallContractArgs args;
   cudaError_t e;
@@ -809,6 +834,7 @@ cudaError_t launch_contract_tall(RowsArgs& g, int passes, const dictproj_adapter
   const Ring ring = plan_ring(k.stage_bytes, k.part_bytes, 0, (kc + args.g.cluster - 1) / args.g.cluster,
                               sm_share((long)full * args.g.cluster, a->n_sm));
   args.stages = ring.stages;
+  args.flush = exact_sums ? 2 : 1 << 20;
   void* p[] = {(void*)&args};
   return launch_pdl_cluster(k.fn, dim3((unsigned)(adapter_tiles(r->M, r->n_slots, kTallRows) * args.g.cluster), passes), ring.smem,
                             stream, p, dim3(args.g.cluster, 1, 1));

@@ -10,6 +10,10 @@
 // At 2048 rows the dense products (127 GFLOP for 4096 <- 2048 <- 11008) are what the time
 // goes to; with few rows it is the chain of stages, which a cluster then splits.
 //
+// dZ is rounded to fp16 between the products, as the forward rounds Z. Up to kFineRows rows,
+// where the second product waits for its loads and not for the tensor cores, it is kept as two
+// fp16 parts (22 bits), the product's reduction running over both.
+//
 // Every spin-wait is bounded; a wait that gives up sets the file's device error word and
 // the kernel unwinds (frees its tensor memory) without hanging.
 #include <cuda.h>
@@ -63,6 +67,19 @@ constexpr size_t kNnSmem = (size_t)kNnStages * (kNnABytes + kNnBBytes) + 1024 + 
 constexpr int kNnSplitN = 128;  // widest tile of a split product: its fp32 sums fit the ring
 static_assert(kNnM * (kNnSplitN + 4) * 4 <= kNnStages * (kNnABytes + kNnBBytes), "partial sums");
 
+// Eight results rounded to fp16, and, where wanted, what the rounding left as a second part.
+__device__ __forceinline__ void store8(__half* out, __half* low, const float (&f)[8]) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const Split a = split_half(f[2 * e]), b = split_half(f[2 * e + 1]);
+    h[e] = half2_bits(a.hi, b.hi);
+    l[e] = half2_bits(a.lo, b.lo);
+  }
+  *reinterpret_cast<uint4*>(out) = make_uint4(h[0], h[1], h[2], h[3]);
+  if (low) *reinterpret_cast<uint4*>(low) = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
 // One 128 x bn tile (bn a multiple of 64) of out = scale A B. With gridDim.z = S > 1 the S
 // CTAs of a cluster (1, 1, S) take consecutive ranges of the reduction's stages; the fp32
 // partial tiles meet through distributed shared memory, in rank order, each CTA writing its
@@ -70,7 +87,8 @@ static_assert(kNnM * (kNnSplitN + 4) * 4 <= kNnStages * (kNnABytes + kNnBBytes),
 // idle) make the dense dictionary that the next product reads.
 __global__ void __launch_bounds__(kNnThreads, 1)
     k_gemm_nn(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, int M, int N, int K,
-              int bn, float scale, __half* __restrict__ out, int nx, int tiles, const __grid_constant__ DictCopy copy) {
+              int bn, float scale, __half* __restrict__ out, __half* __restrict__ low,
+              const __grid_constant__ CUtensorMap tm_low, int parts, int nx, int tiles, const __grid_constant__ DictCopy copy) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint8_t* sb = smem + kNnStages * kNnABytes;
@@ -87,7 +105,8 @@ __global__ void __launch_bounds__(kNnThreads, 1)
     return;
   }
   const int n0 = blockIdx.x % nx * bn, m0 = blockIdx.x / nx * kNnM, split = blockIdx.z, nsplit = gridDim.z;
-  const int nk_all = (K + kNnK - 1) / kNnK, s_lo = (int)((long)nk_all * split / nsplit);
+  const int nk_one = (K + kNnK - 1) / kNnK, nk_all = parts * nk_one;  // A's high part, then its low
+  const int s_lo = (int)((long)nk_all * split / nsplit);
   const int nk = (int)((long)nk_all * (split + 1) / nsplit) - s_lo;
 
   if (threadIdx.x == 0) {
@@ -117,9 +136,11 @@ __global__ void __launch_bounds__(kNnThreads, 1)
           break;
         }
         mbar_arrive_expect_tx(&full[at.slot], kNnABytes + bn * kNnK * 2);
-        tma_load_2d(smem_u32(smem + at.slot * kNnABytes), &tm_a, (s_lo + s) * kNnK, m0, &full[at.slot]);
+        const bool second = s_lo + s >= nk_one;
+        const int kx = (s_lo + s - (second ? nk_one : 0)) * kNnK;
+        tma_load_2d(smem_u32(smem + at.slot * kNnABytes), second ? &tm_low : &tm_a, kx, m0, &full[at.slot]);
         for (int c = 0; c < bn / 64; ++c)
-          tma_load_2d(smem_u32(sb + at.slot * kNnBBytes + c * kMnChunk), &tm_b, n0 + 64 * c, (s_lo + s) * kNnK, &full[at.slot]);
+          tma_load_2d(smem_u32(sb + at.slot * kNnBBytes + c * kMnChunk), &tm_b, n0 + 64 * c, kx, &full[at.slot]);
       }
     }
   } else if (warp == 1) {
@@ -164,13 +185,10 @@ __global__ void __launch_bounds__(kNnThreads, 1)
       for (int j = 0; j < 4; ++j) {
         const int gc = n0 + 32 * c + 8 * j;
         if (gc >= N) break;  // N % 8 == 0
-        uint32_t o[4];
+        float f[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __half2 h = __floats2half2_rn(__uint_as_float(v[8 * j + 2 * e]) * scale, __uint_as_float(v[8 * j + 2 * e + 1]) * scale);
-          o[e] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *reinterpret_cast<uint4*>(orow + gc) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * j + e]) * scale;
+        store8(orow + gc, low ? low + (size_t)(m0 + row) * N + gc : nullptr, f);
       }
     }
   }
@@ -193,9 +211,9 @@ __global__ void __launch_bounds__(kNnThreads, 1)
       if (m0 + row >= M || n0 + c >= N) continue;
       const uint32_t at = pbase + 4 * (row * pitch + c);
       const float4 x = sum_peers(at, nsplit), y = sum_peers(at + 16, nsplit);
-      const __half2 h[4] = {__floats2half2_rn(x.x * scale, x.y * scale), __floats2half2_rn(x.z * scale, x.w * scale),
-                            __floats2half2_rn(y.x * scale, y.y * scale), __floats2half2_rn(y.z * scale, y.w * scale)};
-      *reinterpret_cast<uint4*>(out + (size_t)(m0 + row) * N + n0 + c) = *reinterpret_cast<const uint4*>(h);
+      const float f[8] = {x.x * scale, x.y * scale, x.z * scale, x.w * scale, y.x * scale, y.y * scale, y.z * scale, y.w * scale};
+      const size_t o = (size_t)(m0 + row) * N + n0 + c;
+      store8(out + o, low ? low + o : nullptr, f);
     }
     cluster_arrive();  // no CTA leaves while its sums are read
     cluster_wait();
@@ -283,13 +301,18 @@ cudaError_t prepare_backward_kernels(int device) {
   return cudaFuncSetAttribute(k_gemm_nn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNnSmem);
 }
 
-static cudaError_t launch_nn(const __half* A, const __half* B, int M, int N, int K, float scale, __half* out,
-                             const NnPlan& plan, const DictCopy& copy, int helpers, cudaStream_t stream) {
-  CUtensorMap ta, tb;
+// A_low: A's second part, or null; low: where out's second part goes, or null.
+static cudaError_t launch_nn(const __half* A, const __half* A_low, const __half* B, int M, int N, int K, float scale,
+                             __half* out, __half* low, const NnPlan& plan, const DictCopy& copy, int helpers, cudaStream_t stream) {
+  CUtensorMap ta, tb, tl;
   cudaError_t e = encode_tiled_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, A, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2, kNnK, kNnM,
                                   CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
   e = encode_tiled_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, B, (uint64_t)N, (uint64_t)K, (uint64_t)N * 2, 64, kNnK,
+                      CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  int parts = A_low ? 2 : 1;
+  e = encode_tiled_2d(&tl, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, A_low ? A_low : A, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2, kNnK, kNnM,
                       CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
   int bn = plan.bn, nx = (N + bn - 1) / bn, tiles = nx * ((M + kNnM - 1) / kNnM);
@@ -303,7 +326,7 @@ static cudaError_t launch_nn(const __half* A, const __half* B, int M, int N, int
   set_cluster_z(attr[1], plan.split);
   cfg.attrs = attr;
   cfg.numAttrs = plan.split > 1 ? 2 : 1;
-  void* args[] = {(void*)&ta, (void*)&tb, &M, &N, &K, &bn, &scale, (void*)&out, &nx, &tiles, (void*)&copy};
+  void* args[] = {(void*)&ta, (void*)&tb, &M, &N, &K, &bn, &scale, (void*)&out, (void*)&low, (void*)&tl, &parts, &nx, &tiles, (void*)&copy};
   return cudaLaunchKernelExC(&cfg, (const void*)k_gemm_nn, args);
 }
 
@@ -329,8 +352,10 @@ cudaError_t launch_backward_input(const dictproj_group* g, const dictproj_layer*
     void* args[] = {(void*)&copy};
     if ((e = cudaLaunchKernelExC(&cfg, (const void*)k_densify_dict, args))) return e;
   }
-  if ((e = launch_nn(dY, Cd, M, g->k, l->d_out, l->s, z, p, copy, helpers, stream))) return e;
-  return launch_nn(z, Dd, M, g->d_in, g->k, g->s, dX, nn_plan(M, g->d_in, g->k, g->n_sm), copy, 0, stream);
+  __half* low = M <= kFineRows ? reinterpret_cast<__half*>(g->zlow) : nullptr;
+  if ((e = launch_nn(dY, nullptr, Cd, M, g->k, l->d_out, l->s, z, low, p, copy, helpers, stream))) return e;
+  return launch_nn(z, low, Dd, M, g->d_in, g->k, g->s, dX, nullptr, nn_plan(M, g->d_in, low ? 2 * g->k : g->k, g->n_sm), copy, 0,
+                   stream);
 }
 
 cudaError_t launch_wait_probe_backward(long long cycles, cudaStream_t stream) {

@@ -66,6 +66,7 @@ struct dictproj_group {
   uint16_t* z16;           // prefill Z, fp16 [max_tokens][k]
   uint16_t* cdense;        // prefill coefficient operand, fp16 [d_out][k] for d_out <= cdense_cols
   int cdense_cols;         // reserved output columns (dictproj_group_reserve_prefill)
+  uint16_t* zlow;          // input gradient of few rows: dZ's second part, fp16 [kFineRows][k], or null
   uint16_t* ddense;        // input gradient: D^ densified, fp16 [k][d_in] (dictproj_group_reserve_backward), or null
   CUtensorMap codes_map;   // TMA map of codes: [k] rows x [d_in/2] bytes, box 32 x 256
   // fused decode kernel

@@ -118,6 +118,7 @@ cudaError_t launch_densify_coeff(const dictproj_layer* l, __half* Cd, cudaStream
 cudaError_t launch_coeff_prefill(const dictproj_layer* l, const __half* Z, const __half* Cd, int M, __half* Y,
                                  cudaStream_t stream);
 cudaError_t take_prefill_error(unsigned int* out);
+constexpr int kFineRows = 32;  // rows up to which dZ keeps two parts
 // Input gradient of the projection from its densified coefficients Cd: z (fp16 [M][k]) =
 // s_C dY Cd, Dd = D^ densified (fp16 [k][d_in]), dX = s_D z Dd.
 cudaError_t launch_backward_input(const dictproj_group* g, const dictproj_layer* l, const __half* dY, int M, __half* z,
@@ -135,7 +136,7 @@ cudaError_t encode_adapter_maps(dictproj_adapters* a);
 bool tall_serves(const dictproj_adapters* a, const dictproj_rows* r);
 struct RowsArgs;
 struct GradArgs;
-cudaError_t launch_contract_tall(RowsArgs& g, int passes, const dictproj_adapters* a, const dictproj_rows* r,
+cudaError_t launch_contract_tall(RowsArgs& g, int passes, bool exact_sums, const dictproj_adapters* a, const dictproj_rows* r,
                                  cudaStream_t stream);
 cudaError_t launch_expand_tall(const RowsArgs& g, const dictproj_adapters* a, const dictproj_rows* r,
                                cudaStream_t stream);

@@ -293,12 +293,15 @@ int dictproj_group_reserve_backward(dictproj_group* g, int max_d_out) {
   if (!g) return fail(DICTPROJ_ERR_NULL, "group_reserve_backward: NULL handle");
   int st = check_device(g->device, "group_reserve_backward");
   if (st || (st = dictproj_group_reserve_prefill(g, max_d_out)) || g->ddense) return st;
-  uint16_t* p = nullptr;
-  const cudaError_t e = dmalloc((void**)&p, (size_t)g->k * g->d_in * sizeof(uint16_t));
+  uint16_t *p = nullptr, *low = nullptr;
+  cudaError_t e = dmalloc((void**)&p, (size_t)g->k * g->d_in * sizeof(uint16_t));
+  if (e == cudaSuccess) e = dmalloc((void**)&low, (size_t)g->k * kFineRows * sizeof(uint16_t));
   if (e != cudaSuccess) {
+    cudaFree(p);
     cudaGetLastError();
     return fail(DICTPROJ_ERR_OOM, "group_reserve_backward: device allocation failed (%s)", cudaGetErrorName(e));
   }
+  g->zlow = low;
   g->ddense = p;
   return DICTPROJ_OK;
 }

@@ -503,7 +503,7 @@ int dictproj_adapter_backward(const dictproj_adapters* a, const dictproj_rows* r
 
 /* Reserve what dictproj_backward_input needs for layers with up to max_d_out
  * columns: the prefill coefficient scratch (dictproj_group_reserve_prefill) and
- * the group's dense dictionary, fp16 [k][d_in] (2 * k * d_in bytes). Errors as
+ * the group's dense dictionary, fp16 [k][d_in] (2 * k * d_in bytes), and 64 * k bytes. Errors as
  * dictproj_group_reserve_prefill. */
 int dictproj_group_reserve_backward(dictproj_group* g, int max_d_out);
 
@@ -511,7 +511,8 @@ int dictproj_group_reserve_backward(dictproj_group* g, int max_d_out);
  * fp16 [M][d_out], dX device fp16 [M][d_in], 1 <= M <= max_tokens, d_out % 8 == 0.
  * Every layer format is served. dZ = s_C dY C^T and dX = s_D dZ D^T are tensor-core
  * products with fp32 accumulation; dZ is rounded to fp16 between them, as the
- * prefill forward rounds Z (gradients below 2^-24 of it are lost: scale the loss).
+ * prefill forward rounds Z (gradients below 2^-24 of it are lost: scale the loss); up
+ * to 32 rows it keeps two fp16 parts.
  * Asynchronous on `stream`, uses the group's scratch (one stream at a time).
  * Errors: NULL, RANGE (M, or not reserved), SHAPE (d_out % 8), MISMATCH, ALIGN
  * (dY, dX 16 bytes), CUDA. */

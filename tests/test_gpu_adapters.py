@@ -251,6 +251,23 @@ def test_two_pools_on_two_streams_at_once():
     assert dp.dictproj_check_status(stream()) == 0
 
 
+@pytest.mark.parametrize("M,R", [(2048, 16), (1024, 64), (300, 128)])
+def test_long_sums_keep_the_accuracy_of_fp32(M, R):
+    # The tensor cores sum runs of at most 8 steps (128 columns, or a 64-row tile in two parts) on their own,
+    # 2^-23 of the run a step at most; the runs' sums are fp32 additions, 2^-24 each at random over some 150 of them.
+    pool = ref.Pool(4096, 1024, R, [R], seed=4)
+    ids = torch.zeros(M, dtype=torch.int32, device="cuda")
+    X, dY = normal(M, 4096), normal(M, 1024, seed=3)
+    h, rows = pool.upload(dp, M, stream()), planned(ids, 1)
+    dA, dB = torch.empty(1, R, 4096, device="cuda"), torch.empty(1, R, 1024, device="cuda")
+    dp.dictproj_adapter_backward(h, rows, X.data_ptr(), dY.data_ptr(), 0, 0, dA.data_ptr(), dB.data_ptr(), False, stream())
+    torch.cuda.synchronize()
+    w = ref.backward(pool, ids, X, dY)
+    limit = 8 * 2.0 ** -23 + 2.0 ** -24 * 150 ** 0.5
+    for got, want in ((dA, w["dA"]), (dB, w["dB"])):
+        assert ((got.double() - want).norm() / want.norm()).item() <= limit
+
+
 @pytest.mark.parametrize("size", [1e-7, 1e4])
 def test_small_and_large_activations_keep_their_digits(size):
     # T is far outside fp16's comfortable range: small gradients must not fall to zero in a sum

@@ -46,6 +46,18 @@ def projection(d_in, k, d_out, fmt, M, seed=0, rho=0.3):
     return g, l, cuda(F.decode_dictionary(pack_dictionary(D))), cuda(dense)
 
 
+def test_few_rows_round_once():
+    # up to 32 rows dZ keeps two parts (22 bits): what is left is dX's own rounding, a third of its bound in
+    # the mean square, and the fp32 sums
+    g, l, D, C = projection(1376, 1040, 1000, "u8", 32)
+    dY = torch.randn(32, 1000, generator=torch.Generator().manual_seed(3)).half().cuda()
+    dX = torch.empty(32, 1376, dtype=torch.float16, device="cuda")
+    dp.dictproj_backward_input(dY.data_ptr(), 32, l, g, dX.data_ptr(), stream())
+    torch.cuda.synchronize()
+    want = (dY.double() @ C.T) @ D.T
+    assert (dX.double() - want).norm().item() <= 1.1 * U16 / math.sqrt(3) * want.norm().item()
+
+
 def check(dX, dY, D, C):
     """Two roundings to fp16 (dZ and dX) and two fp32 sums. Element by element the worst case: half a step
     of dX, half a step of every dZ (2^-25 at least) carried through |D|, and 2^-23 of the absolute sum for each
