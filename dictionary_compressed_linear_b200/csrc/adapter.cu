@@ -487,9 +487,13 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_c
   for (int i = 0; i < S::kStages - 1; ++i) issue(i);
 
   const int rg = warp & 3, half = warp >> 2, g0 = lane >> 2, c0 = 2 * (lane & 3);
-  float acc[R / 8][4];
+  // a long accumulation on the tensor cores is less exact than fp32 sums: every eight steps
+  // the accumulators are added to sums of their own
+  float acc[R / 8][4], sum[R / 8][4];
 #pragma unroll
-  for (int t = 0; t < R / 8; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+  for (int t = 0; t < R / 8; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[t][q] = sum[t][q] = 0.f;
   for (int i = 0; i < nk; ++i) {
     cp_async_wait<S::kStages - 2>();
     __syncthreads();
@@ -509,6 +513,11 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_c
         mma_16816(acc[2 * t + 1], af, bf + 2);
       }
     }
+    if ((i & 3) == 3 || i == nk - 1)
+#pragma unroll
+      for (int t = 0; t < R / 8; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum[t][q] += acc[t][q], acc[t][q] = 0.f;
   }
   // the CTA's sum: the second half of the steps, then the first on top
   float* mine = part + (rg * 16) * R;
@@ -521,8 +530,8 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_c
         float2* lo = reinterpret_cast<float2*>(mine + g0 * R + 8 * t + c0);
         float2* hi = reinterpret_cast<float2*>(mine + (g0 + 8) * R + 8 * t + c0);
         const float2 x = h ? make_float2(0.f, 0.f) : *lo, y = h ? make_float2(0.f, 0.f) : *hi;
-        *lo = make_float2(acc[t][0] + x.x, acc[t][1] + x.y);
-        *hi = make_float2(acc[t][2] + y.x, acc[t][3] + y.y);
+        *lo = make_float2(sum[t][0] + x.x, sum[t][1] + x.y);
+        *hi = make_float2(sum[t][2] + y.x, sum[t][3] + y.y);
       }
     __syncthreads();
   }
