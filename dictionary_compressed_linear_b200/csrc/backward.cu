@@ -22,7 +22,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <mutex>
 
 #include "adapter.cuh"
 #include "common.cuh"
@@ -248,13 +247,11 @@ void set_cluster_z(cudaLaunchAttribute& a, int s) {
 
 // Clusters of S CTAs of k_gemm_nn (one CTA an SM) that the device holds at once; cached.
 int nn_clusters_that_fit(int S, int n_sm) {
-  static std::mutex mu;
-  static int cache[16][9];
+  static std::atomic<int> cache[16][9];  // the answer + 1; zero: not asked yet
   if (S == 1) return n_sm;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16 || S > 8) return 0;
-  std::lock_guard<std::mutex> lk(mu);
-  if (cache[dev][S]) return cache[dev][S] - 1;
+  if (const int known = cache[dev][S].load(std::memory_order_relaxed)) return known - 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1, 1, S);
   cfg.blockDim = dim3(kNnThreads);
@@ -268,7 +265,7 @@ int nn_clusters_that_fit(int S, int n_sm) {
     cudaGetLastError();
     n = 0;
   }
-  cache[dev][S] = n + 1;
+  cache[dev][S].store(n + 1, std::memory_order_relaxed);
   return n;
 }
 
@@ -312,9 +309,10 @@ static cudaError_t launch_nn(const __half* A, const __half* A_low, const __half*
                       CU_TENSOR_MAP_SWIZZLE_128B);
   if (e != cudaSuccess) return e;
   int parts = A_low ? 2 : 1;
-  e = encode_tiled_2d(&tl, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, A_low ? A_low : A, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2, kNnK, kNnM,
-                      CU_TENSOR_MAP_SWIZZLE_128B);
-  if (e != cudaSuccess) return e;
+  tl = ta;
+  if (A_low && (e = encode_tiled_2d(&tl, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, A_low, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2, kNnK,
+                                    kNnM, CU_TENSOR_MAP_SWIZZLE_128B)))
+    return e;
   int bn = plan.bn, nx = (N + bn - 1) / bn, tiles = nx * ((M + kNnM - 1) / kNnM);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles + helpers, 1, plan.split);
