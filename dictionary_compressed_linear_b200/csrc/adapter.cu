@@ -5,14 +5,13 @@
 //   dA_s = scale_s sum_m U[m]^T X[m],  dB_s = scale_s sum_m T[m]^T dY[m]
 //
 // A and B are stored rank-major ([rank][d_in], [rank][d_out]), so the forward and
-// the input gradient are one kernel with A and B exchanged (k_adapter_rows): a
-// contraction along the rows of the first, an expansion along the rows of the
-// second. Both weight gradients are one kernel as well (k_adapter_grad).
+// the input gradient are the same kernels with A and B exchanged: a contraction along
+// the rows of the first, an expansion along the rows of the second. Both weight
+// gradients are one kernel as well.
 //
-// All of them move far more bytes than the legacy tensor path (mma.sync) needs time
-// for: a row of d elements is read or written once for 2 r d multiply-adds, and r is
-// at most 128. tcgen05 would need tiles of 128 rows of one slot, which a batch of
-// many requests does not have.
+// Here are the plan, the kernels of few rows (CUDA cores) and those of many rows on
+// mma.sync, which serve any row length; adapter_tall.cu has those on tcgen05 for row
+// lengths that TMA can read.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -170,18 +169,22 @@ __global__ void __launch_bounds__(kPlanWarps * 32)
 }
 
 // Copy an adapter into its slot, with zeros past its rank and past d_out.
+constexpr int kSetCols = 1024;  // columns of a CTA
+
 __global__ void __launch_bounds__(256)
     k_adapter_set(const __half* __restrict__ A, const __half* __restrict__ B, int rank, float scale, int rp, int d_in,
                   int d_out, int ld_b, __half* __restrict__ sa, __half* __restrict__ sb, int* __restrict__ srank,
                   float* __restrict__ sscale) {
   grid_dependency_wait();
-  const int j = blockIdx.x;
+  const int j = blockIdx.x, c0 = blockIdx.y * kSetCols + threadIdx.x;
   const __half zero = __float2half_rn(0.f);
-  for (int i = threadIdx.x; i < d_in; i += blockDim.x)
-    sa[(size_t)j * d_in + i] = j < rank ? A[(size_t)j * d_in + i] : zero;
-  for (int o = threadIdx.x; o < ld_b; o += blockDim.x)
-    sb[(size_t)j * ld_b + o] = j < rank && o < d_out ? B[(size_t)j * d_out + o] : zero;
-  if (j == 0 && threadIdx.x == 0) {
+#pragma unroll
+  for (int q = 0; q < kSetCols / 256; ++q) {
+    const int c = c0 + 256 * q;
+    if (c < d_in) sa[(size_t)j * d_in + c] = j < rank ? A[(size_t)j * d_in + c] : zero;
+    if (c < ld_b) sb[(size_t)j * ld_b + c] = j < rank && c < d_out ? B[(size_t)j * d_out + c] : zero;
+  }
+  if (j == 0 && c0 == 0) {
     *srank = rank;
     *sscale = scale;
   }
@@ -225,7 +228,10 @@ constexpr int kRowThreads = 256;
 //   2. the CTAs' partial sums meet through distributed shared memory, in rank order;
 //   3. CTA c expands T into its share of the N columns: four lanes split the ranks of
 //      eight columns. Its part of Q is on its way to L2 since before 1.
-// Bound by latency: the chain is plan -> rank and rows -> X and P -> cluster -> Q.
+// Bound by latency: the chain is plan -> rank and rows -> X and P -> cluster -> Q. One row of
+// rank 16 (4096 -> 4096) takes 4.2 us, 64 requests with an adapter each (4096 -> 11008, 34 MB)
+// 12.1 us: 2.8 TB/s. With tiles of 16 rows on mma.sync, staged through shared memory, they
+// took 7.0 and 29.9 us; without the prefetch of the first ranks the second took 17.0 us.
 __device__ __forceinline__ void dot2(float& acc, uint32_t x2, uint32_t w2) {
   asm("{\n\t.reg .f16 a, b, c, d;\n\tmov.b32 {a, b}, %1;\n\tmov.b32 {c, d}, %2;\n\t"
       "fma.rn.f32.f16 %0, a, c, %0;\n\tfma.rn.f32.f16 %0, b, d, %0;\n\t}" : "+f"(acc) : "r"(x2), "r"(w2));
@@ -1120,7 +1126,8 @@ cudaError_t launch_adapter_set(const dictproj_adapters* a, int slot, int rank, f
   float* ss = a->scale + slot;
   int rp = a->rp, d_in = a->d_in, d_out = a->d_out, ld_b = a->ld_b;
   void* args[] = {&A, &B, &rank, &scale, &rp, &d_in, &d_out, &ld_b, &sa, &sb, &sr, &ss};
-  return launch_pdl((const void*)k_adapter_set, dim3(a->rp), dim3(256), 0, stream, args);
+  return launch_pdl((const void*)k_adapter_set, dim3(a->rp, (std::max(d_in, ld_b) + kSetCols - 1) / kSetCols), dim3(256), 0,
+                    stream, args);
 }
 
 cudaError_t launch_rows_plan(const dictproj_rows* r, const int* ids, int M, cudaStream_t stream) {
