@@ -117,7 +117,10 @@ __global__ void __launch_bounds__(kPlanWarps * 32)
   int n_used;
   const int at_used = block_exclusive_sum(count > 0 ? 1 : 0, wsum, &n_used);
   if (count > 0) used[at_used] = s;
-  if (threadIdx.x == 0) n_tiles[6] = n_used;
+  if (threadIdx.x == 0) {
+    n_tiles[6] = n_used;
+    n_tiles[7] = M;
+  }
 #pragma unroll 1
   for (int q = 0; q < 3; ++q) {
     const int T = plan_rows(q);
@@ -911,7 +914,7 @@ __global__ void __launch_bounds__(kFewGradThreads) k_grad_few(const __grid_const
   const int c = ((int)blockIdx.x - (which ? g.pass[0].blocks : 0)) * kFewGradCols + 4 * threadIdx.x;
   // what the call found is read before the wait on its first kernel (see the expansion)
   trigger_dependents();
-  const int p0 = __ldcg(g.start + slot), r = __ldcg(g.rank + slot), p1 = r > j0 ? __ldcg(g.start + slot + 1) : p0;
+  const int p0 = __ldcg(g.start + slot), r = __ldcg(g.rank + slot), p1 = r > j0 && __ldcg(g.planned) <= g.n_rows ? __ldcg(g.start + slot + 1) : p0;
   const bool vec = (a.K & 3) == 0;
   // eight rows at a time, their loads together: one row's took 0.6 us after the other's
   constexpr int kAhead = 8;
@@ -1021,6 +1024,7 @@ cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, size_t smem, cudaS
 RowsArgs rows_args(const dictproj_adapters* a, const dictproj_rows* r, bool wide) {
   RowsArgs g = {};
   g.n_tiles = r->n_tiles + (wide ? 2 : 0);
+  g.planned = r->n_tiles + 7;
   g.tiles = r->tiles[wide];
   g.perm = r->perm;
   g.rank = a->rank;
@@ -1215,6 +1219,7 @@ cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_r
   w.n_rows = r->M;
   w.used = r->used;
   w.n_used = r->n_tiles + 6;
+  w.planned = r->n_tiles + 7;
   w.zeroed = a->n_slots > 1;
   // The kernels of few rows, both contractions and dX in one launch, for some rows a slot
   // (4096 and 4096 wide, rank 16: 1 slot 8 rows 8.5 us against 10.5, 32 rows 15.6 against

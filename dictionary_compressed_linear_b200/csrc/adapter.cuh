@@ -29,6 +29,7 @@ struct RowsPass {
 struct RowsArgs {
   RowsPass pass[2];
   const int* n_tiles;
+  const int* planned;  // the plan's rows, on the device
   const int4* tiles;
   const int* runs;  // 128-row tiles: the first row of a tile whose rows follow one another, else -1
   const int* perm;
@@ -56,12 +57,14 @@ struct GradArgs {
   const int* rank;
   const int* used;    // the slots that have rows
   const int* n_used;
+  const int* planned;
   int rp, pp, max_rank, accumulate, n_rows;
   int zeroed;         // several slots: those without rows or rank are zeroed by a launch of their own
 };
 
 // The slot of a gradient CTA (blockIdx.y counts the slots that have rows), -1: none.
 __device__ __forceinline__ int grad_slot(const GradArgs& g) {
+  if (__ldcg(g.planned) > g.n_rows) return -1;
   if (!g.zeroed) return blockIdx.y;
   return (int)blockIdx.y < __ldcg(g.n_used) ? __ldcg(g.used + blockIdx.y) : -1;
 }
@@ -227,9 +230,10 @@ __device__ __forceinline__ void copy_rows(const RowsPass& a, int n_rows, const i
 }
 
 // Whether a launch is to take a tile (slots' and, unless the output is in place, those of
-// rows without an adapter).
+// rows without an adapter). A captured call may meet a plan of more rows than it was made
+// for, whose row numbers reach past its arrays: it takes none of them.
 __device__ __forceinline__ bool takes_tile(const RowsArgs& g, int tile_no, const int4& tile, bool in_place) {
-  return tile_no < __ldcg(g.n_tiles + (in_place ? 0 : 1)) && (g.only < 0 || g.only == (tile.z >= kCrowdTile ? 1 : 0));
+  return __ldcg(g.planned) <= g.rows && tile_no < __ldcg(g.n_tiles + (in_place ? 0 : 1)) && (g.only < 0 || g.only == (tile.z >= kCrowdTile ? 1 : 0));
 }
 
 // Zeros over `width` columns of rows [0, n) of a gradient, shared by `parts` CTAs.

@@ -142,7 +142,7 @@ struct dictproj_rows {
   int* start;              // [n_slots + 2] first position of each slot, of the rows without one, M
   // tiles of up to 4 (index 0), 64 (1) and 128 (2) rows of one slot, in plan order; those
   // of rows without an adapter (slot n_slots) come last
-  int* n_tiles;            // [3][2] tiles of the slots, all tiles; [6] slots that have rows
+  int* n_tiles;            // [3][2] tiles of the slots, all tiles; [6] slots that have rows; [7] rows planned
   int* used;               // [n_slots] the slots that have rows, ascending
   int4* tiles[3];          // {slot, first position, rows, row number of the first (2: its first 64-row tile)}
   int* runs[2];            // of the 64- and 128-row tiles: the first row where a tile's rows follow one another, else -1

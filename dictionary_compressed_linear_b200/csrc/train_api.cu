@@ -31,10 +31,41 @@ bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) !=
 struct Range {
   const void* p;
   size_t bytes;
+  bool written = false;
 };
 bool overlap(Range a, Range b) {
   const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
   return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+
+// Whether an array that the AdamW step writes overlaps another one of the list (gradients,
+// which it only reads, may be shared).
+bool written_twice(const dictproj_adamw_tensor* tensors, int n, int state_bytes) {
+  std::vector<Range> all;
+  all.reserve(7 * (size_t)n);
+  for (int i = 0; i < n; ++i) {
+    const dictproj_adamw_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    const size_t e = (size_t)t.n, blocks = (e + DICTPROJ_ADAMW_BLOCK - 1) / DICTPROJ_ADAMW_BLOCK;
+    all.push_back({t.g, 4 * e, false});
+    all.push_back({t.p, 4 * e, true});
+    all.push_back({t.m, state_bytes * e, true});
+    all.push_back({t.v, state_bytes * e, true});
+    if (t.copy) all.push_back({t.copy, 2 * e, true});
+    if (state_bytes == 1) {
+      all.push_back({t.m_scale, 4 * blocks, true});
+      all.push_back({t.v_scale, 4 * blocks, true});
+    }
+  }
+  std::sort(all.begin(), all.end(), [](const Range& a, const Range& b) { return (uintptr_t)a.p < (uintptr_t)b.p; });
+  uintptr_t end = 0, written_end = 0;  // of the arrays that start at or before this one
+  for (const Range& r : all) {
+    const uintptr_t first = (uintptr_t)r.p;
+    if (first < (r.written ? end : written_end)) return true;
+    end = std::max(end, first + r.bytes);
+    if (r.written) written_end = std::max(written_end, first + r.bytes);
+  }
+  return false;
 }
 
 // What every call on a pool and a plan checks; *M gets the planned rows.
@@ -186,7 +217,7 @@ int dictproj_rows_create(int max_rows, int n_slots, dictproj_rows** out) {
   r->n_slots = n_slots;
   cudaError_t e;
   if ((e = dmalloc((void**)&r->perm, (size_t)max_rows * 4)) || (e = dmalloc((void**)&r->start, (size_t)(n_slots + 2) * 4)) ||
-      (e = dmalloc((void**)&r->n_tiles, 7 * sizeof(int))) || (e = dmalloc((void**)&r->used, (size_t)n_slots * 4)) || (e = dmalloc((void**)&r->first64, (size_t)n_slots * 4)) ||
+      (e = dmalloc((void**)&r->n_tiles, 8 * sizeof(int))) || (e = dmalloc((void**)&r->used, (size_t)n_slots * 4)) || (e = dmalloc((void**)&r->first64, (size_t)n_slots * 4)) ||
       (e = dmalloc((void**)&r->tiles[0], (size_t)adapter_tiles(max_rows, n_slots, 4) * sizeof(int4))) ||
       (e = dmalloc((void**)&r->tiles[1], (size_t)adapter_tiles(max_rows, n_slots, 64) * sizeof(int4))) ||
       (e = dmalloc((void**)&r->runs[0], (size_t)adapter_tiles(max_rows, n_slots, 64) * sizeof(int))) ||
@@ -195,6 +226,13 @@ int dictproj_rows_create(int max_rows, int n_slots, dictproj_rows** out) {
     dictproj_free_rows(r);
     cudaGetLastError();
     return fail(DICTPROJ_ERR_OOM, "rows_create: device allocation failed (%s)", cudaGetErrorName(e));
+  }
+  // no rows until a plan has run: rows_set may have been captured and not replayed yet
+  if ((e = cudaMemset(r->start, 0, (size_t)(n_slots + 2) * 4)) || (e = cudaMemset(r->n_tiles, 0, 8 * sizeof(int))) ||
+      (e = cudaDeviceSynchronize())) {
+    dictproj_free_rows(r);
+    cudaGetLastError();
+    return cuda_fail(e, "rows_create: empty plan");
   }
   *out = r;
   return DICTPROJ_OK;
@@ -366,14 +404,17 @@ int dictproj_adamw_create(const dictproj_adamw_tensor* tensors, int n_tensors, i
   }
   if (chunks > 0x7fffffffll)
     return fail(DICTPROJ_ERR_RANGE, "adamw_create: more than 2^31 - 1 chunks of %d elements", kAdamwChunk);
-  int dev, st;
-  if ((st = ensure_device(&dev))) return st;
   std::vector<AdamwChunk> table;
+  bool twice;
   try {
+    twice = written_twice(tensors, n_tensors, sb);
     table.resize((size_t)chunks);
   } catch (...) {
     return fail(DICTPROJ_ERR_OOM, "adamw_create: host allocation failed");
   }
+  if (twice) return fail(DICTPROJ_ERR_RANGE, "adamw_create: an array that the step writes overlaps another array");
+  int dev, st;
+  if ((st = ensure_device(&dev))) return st;
   size_t at = 0;
   for (int i = 0; i < n_tensors; ++i) {
     const dictproj_adamw_tensor& t = tensors[i];

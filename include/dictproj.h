@@ -452,8 +452,10 @@ void dictproj_free_rows(dictproj_rows* rows); /* NULL is a no-op */
 /* Plan a batch of M rows: ids device int32[M], ids[m] the slot of row m; any value
  * outside [0, n_slots) means that the row uses no adapter. The ids are read on the
  * device, so a captured call plans anew with what they hold at each replay; a
- * captured call keeps the M it was captured with (and one that uses a plan serves at
- * most the rows planned at its capture). Rows of one slot need not be neighbours,
+ * captured call keeps the M it was captured with, and one that uses a plan serves at
+ * most the rows planned at its capture: replayed with a plan of more rows it takes
+ * none of them (rows and gradients are left as they were, or zero). A plan whose first
+ * dictproj_rows_set was captured has no rows until the replay. Rows of one slot need not be neighbours,
  * and are fastest when they are. Asynchronous on `stream`.
  * Errors: NULL, RANGE (M outside [1, max_rows]), ALIGN (ids not 4-byte aligned),
  * MISMATCH (device), CUDA. */
@@ -551,7 +553,7 @@ int dictproj_backward_input(const void* dY, int M, const dictproj_layer* layer, 
  * into its block: check before the step.
  *
  * p, g, m, v (32 bits) and the scales must be 4-byte aligned, copy 2-byte; 16-byte
- * alignment of all (4 for the codes) is faster. No two tensors may overlap. */
+ * alignment of all (4 for the codes) is faster. Only gradients may overlap one another. */
 #define DICTPROJ_ADAMW_BLOCK 128
 typedef struct dictproj_adamw_tensor {
   float* p;          /* [n] master weights */
@@ -568,7 +570,7 @@ typedef struct dictproj_adamw dictproj_adamw;
 /* Keep a table of the tensors on the current device (the tensors stay the
  * caller's). Errors: NULL (an array, or a pointer of a tensor with n > 0), RANGE
  * (n_tensors outside [1, 2^20], n, state_bits not 8 or 32, more than 2^31 - 1
- * chunks of 2048 elements in all), ALIGN, OOM, CUDA. */
+ * chunks of 2048 elements in all, a written array that overlaps another), ALIGN, OOM, CUDA. */
 int dictproj_adamw_create(const dictproj_adamw_tensor* tensors, int n_tensors, int state_bits, dictproj_adamw** out);
 void dictproj_free_adamw(dictproj_adamw* w); /* NULL is a no-op */
 

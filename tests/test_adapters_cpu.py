@@ -66,6 +66,28 @@ def test_optimiser_tables(dp, tensors, bits, status):
     assert _status(lambda: dp.dictproj_adamw_create(tensors, bits)) == status
 
 
+def _apart(at, **kw):
+    return {"p": at, "g": at + 64, "m": at + 128, "v": at + 192, "n": 16, **kw}
+
+
+@pytest.mark.parametrize("tensors,bits", [
+    ([_apart(4096), _apart(4096)], 32), ([_apart(4096, g=4096)], 32), ([_apart(4096), _apart(8192, copy=4156)], 32),
+    ([_apart(4096, n=17)], 32), ([_apart(4096), _apart(8192, g=4096 + 128)], 32), ([_apart(4096, n=1 << 20), _apart(8192, n=0), _apart(1 << 25)], 32),
+    ([_apart(4096, m_scale=4096 + 132, v_scale=1024)], 8)])
+def test_an_optimiser_writes_an_array_once(dp, tensors, bits):
+    assert _status(lambda: dp.dictproj_adamw_create(tensors, bits)) == -5
+
+
+@pytest.mark.parametrize("tensors,bits", [
+    ([_apart(4096), _apart(4352)], 32), ([_apart(4096, g=1024), _apart(4352, g=1024), _apart(8192, g=1028)], 32),
+    ([_apart(4096, n=0), _apart(4096)], 32), ([_apart(4096, m_scale=1024, v_scale=1028), _apart(4352, m_scale=1032, v_scale=1036)], 8)])
+def test_neighbours_and_shared_gradients_do_not_overlap(dp, tensors, bits):
+    # past the checks of the list there is no device to keep it on
+    import torch
+    if not torch.cuda.is_available():
+        assert _status(lambda: dp.dictproj_adamw_create(tensors, bits)) not in (0, -5)
+
+
 def test_the_reference_step_is_adamw():
     # the tests' fp32 restatement against the textbook form in fp64
     from adapter_reference import adamw

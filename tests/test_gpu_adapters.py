@@ -363,6 +363,66 @@ def test_captured_calls_plan_anew_and_other_streams(M):
         ref.assert_float(dB, w["dB"], w["WB"], 256 + M)
 
 
+@pytest.mark.parametrize("M", [8, 300, 700])
+@pytest.mark.parametrize("slots", [1, 3])
+def test_a_captured_call_takes_no_plan_of_more_rows(M, slots):
+    # the arrays hold twice the rows, so that only the kernels' own check is tested
+    pool = ref.Pool(256, 264, 16, [16, 8, 4][:slots], seed=2)
+    h = pool.upload(dp, 2 * M, stream())
+    rows = dp.dictproj_rows_create(2 * M, slots)
+    ids, X, dY = ids_of("each", 2 * M, slots), normal(2 * M, 256), normal(2 * M, 264, seed=8)
+    Y, dX = torch.zeros_like(dY), torch.zeros_like(X)
+    dA, dB = torch.zeros(slots, 16, 256, device="cuda"), torch.zeros(slots, 16, 264, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    dp.dictproj_rows_set(rows, ids.data_ptr(), M, side.cuda_stream)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        dp.dictproj_adapter_forward(h, rows, X.data_ptr(), 0, Y.data_ptr(), side.cuda_stream)
+        dp.dictproj_adapter_backward(h, rows, X.data_ptr(), dY.data_ptr(), 0, dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), False,
+                                     side.cuda_stream)
+    outs = (Y, dX, dA, dB)
+    for planned_rows in (M, 2 * M, M - 3):  # as captured, more, fewer
+        for t in outs:
+            t.fill_(7)
+        dp.dictproj_rows_set(rows, ids.data_ptr(), planned_rows, stream())
+        graph.replay()
+        torch.cuda.synchronize()
+        if planned_rows > M:
+            assert (Y == 7).all() and (dX == 7).all()
+            assert ((dA == 7) | (dA == 0)).all() and ((dB == 7) | (dB == 0)).all()
+            continue
+        n = planned_rows
+        want, W = ref.forward(pool, ids[:n], X[:n])
+        ref.assert_half(Y[:n], want, W, 272)
+        w = ref.backward(pool, ids[:n], X[:n], dY[:n])
+        ref.assert_half(dX[:n], w["dX"], w["WX"], 280)
+        ref.assert_float(dA, w["dA"], w["WA"], 264 + M)
+        ref.assert_float(dB, w["dB"], w["WB"], 256 + M)
+        assert (Y[n:] == 7).all() and (dX[n:] == 7).all()
+
+
+def test_a_plan_that_was_only_captured_has_no_rows():
+    pool = ref.Pool(256, 264, 16, [16, 8], seed=2)
+    h = pool.upload(dp, 8, stream())
+    rows = dp.dictproj_rows_create(8, 2)
+    ids, X = ids_of("each", 8, 2), normal(8, 256)
+    Y = torch.full((8, 264), 7.0, dtype=torch.float16, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dp.dictproj_rows_set(rows, ids.data_ptr(), 8, stream())
+    dp.dictproj_adapter_forward(h, rows, X.data_ptr(), 0, Y.data_ptr(), stream())
+    torch.cuda.synchronize()
+    assert (Y == 7).all()
+    graph.replay()
+    dp.dictproj_adapter_forward(h, rows, X.data_ptr(), 0, Y.data_ptr(), stream())
+    torch.cuda.synchronize()
+    want, W = ref.forward(pool, ids, X)
+    ref.assert_half(Y, want, W, 272)
+
+
 def _projection(d_in, d_out, k, M, seed=30):
     D, C = synth.gen_dictionary(seed, 0, 0, d_in, k), synth.gen_coeff(seed, 0, 0, 0, k, d_out, 0.4)
     g, l = device_projection(D, C, M)
@@ -479,7 +539,8 @@ def test_injected_host_faults_leave_nothing_allocated(kind):
         "import os; os.environ['DICTPROJ_FAULT'] = ''\n"
         "free0 = torch.cuda.mem_get_info()[0]\n"
         f"os.environ['DICTPROJ_FAULT'] = '{kind}'\n"
-        "t = [{'p': x.data_ptr(), 'g': x.data_ptr(), 'm': x.data_ptr(), 'v': x.data_ptr(), 'n': 1 << 20}] * 500\n"
+        # addresses alone: no step is made of them
+        "t = [{'n': 1 << 20, **{k: (1 << 40) + (4 * i + j << 22) for j, k in enumerate('pgmv')}} for i in range(500)]\n"
         "calls = {'adamw': lambda: dp.dictproj_adamw_create(t, 32)}\n"
         f"if '{kind}' == 'alloc':\n"
         "    calls.update(pool=lambda: dp.dictproj_adapters_create(4096, 11008, 64, 64, 2048),\n"
