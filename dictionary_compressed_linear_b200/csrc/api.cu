@@ -199,7 +199,7 @@ void dictproj_free_group(dictproj_group* g) {
   cudaFree(g->z16);
   cudaFree(g->cdense);
   cudaFree(g->ddense);
-  cudaFree(g->zlow);
+  cudaFree(g->zmore);
   cudaFree(g->fcodes);
   cudaFree(g->fscales);
   cudaFree(g->zx);

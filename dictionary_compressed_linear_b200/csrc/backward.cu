@@ -10,13 +10,20 @@
 // At 2048 rows the dense products (127 GFLOP for 4096 <- 2048 <- 11008) are what the time
 // goes to; with few rows it is the chain of stages, which a cluster then splits.
 //
-// dZ is rounded to fp16 between the products, as the forward rounds Z. Up to kFineRows rows,
-// where the second product waits for its loads and not for the tensor cores, it is kept as two
-// fp16 parts (22 bits), the product's reduction running over both.
+// Between the products dZ is kept as a sum of bf16 parts, the second product's reduction running
+// over them: bf16 has fp32's range, so that neither small nor large gradients leave it, and the
+// dense dictionary (a product of E2M1 and E4M3 has at most six bits) is exact in it. Two parts
+// hold 16 bits (2^-16 of an element at most beside dX's own 2^-11). One fp16 part made dX's
+// error 2.9e-4 (2.1e-4 now: its own rounding), lost what lay below 2^-24 and gave NaN above
+// 65504; it took 40 us where two take 44 (128 rows, 4096 <- 2048 <- 4096), and 130 where they
+// take 171 (2048 rows, 4096 <- 2048 <- 11008). Up to
+// kFineRows rows, where the second product waits for its loads and not for the tensor cores,
+// a third part makes it fp32's 24 bits.
 //
 // Every spin-wait is bounded; a wait that gives up sets the file's device error word and
 // the kernel unwinds (frees its tensor memory) without hanging.
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -32,12 +39,18 @@
 namespace dictproj {
 namespace {
 
-// Dense fp16 copy of D^ (Dd[j][i], E2M1 x E4M3 exact in fp16, without s_D): a thread per
-// 16-value block, 8 + 1 bytes in, 32 bytes out.
+__device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float bf16_value(uint32_t bits) { return __uint_as_float(bits << 16); }
+
+// Dense bf16 copy of D^ (Dd[j][i], E2M1 x E4M3 exact in fp16 and in bf16, without s_D): a
+// thread per 16-value block, 8 + 1 bytes in, 32 bytes out.
 struct DictCopy {
   const uint8_t* codes;
   const uint8_t* scales;
-  __half* dd;
+  __nv_bfloat16* dd;
   long n_blocks;
 };
 __device__ __forceinline__ void densify_block(const DictCopy& d, long b) {
@@ -47,7 +60,11 @@ __device__ __forceinline__ void densify_block(const DictCopy& d, long b) {
   e2m1x8_to_f16x2x4(c.x, *reinterpret_cast<uint32_t(*)[4]>(v));
   e2m1x8_to_f16x2x4(c.y, *reinterpret_cast<uint32_t(*)[4]>(v + 4));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = hmul2_u32(v[i], sv);
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t h = hmul2_u32(v[i], sv);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    v[i] = bf16x2_bits(f.x, f.y);
+  }
   uint4* dst = reinterpret_cast<uint4*>(d.dd + 16 * b);
   dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
   dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
@@ -66,28 +83,58 @@ constexpr size_t kNnSmem = (size_t)kNnStages * (kNnABytes + kNnBBytes) + 1024 + 
 constexpr int kNnSplitN = 128;  // widest tile of a split product: its fp32 sums fit the ring
 static_assert(kNnM * (kNnSplitN + 4) * 4 <= kNnStages * (kNnABytes + kNnBBytes), "partial sums");
 
-// Eight results rounded to fp16, and, where wanted, what the rounding left as a second part.
-__device__ __forceinline__ void store8(__half* out, __half* low, const float (&f)[8]) {
-  uint32_t h[4], l[4];
+// dZ's parts, each bf16 [M][k]: a part is the bf16 value nearest to what the parts before it leave.
+constexpr int kZParts = 3;
+struct ZParts {
+  __nv_bfloat16* p[kZParts];
+  int n;
+};
+__device__ __forceinline__ void store_parts(const ZParts& z, size_t at, float (&f)[8]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const Split a = split_half(f[2 * e]), b = split_half(f[2 * e + 1]);
-    h[e] = half2_bits(a.hi, b.hi);
-    l[e] = half2_bits(a.lo, b.lo);
+  for (int q = 0; q < kZParts; ++q) {
+    if (q >= z.n) break;
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      w[e] = bf16x2_bits(f[2 * e], f[2 * e + 1]);
+      const float a = bf16_value(w[e]), b = bf16_value(w[e] >> 16);
+      // nothing is left of an infinity or NaN
+      f[2 * e] = fabsf(a) <= 3.4e38f ? f[2 * e] - a : 0.f;
+      f[2 * e + 1] = fabsf(b) <= 3.4e38f ? f[2 * e + 1] - b : 0.f;
+    }
+    *reinterpret_cast<uint4*>(z.p[q] + at) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  *reinterpret_cast<uint4*>(out) = make_uint4(h[0], h[1], h[2], h[3]);
-  if (low) *reinterpret_cast<uint4*>(low) = make_uint4(l[0], l[1], l[2], l[3]);
 }
+__device__ __forceinline__ void store_half(__half* out, const float (&f)[8]) {
+  uint32_t h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = half2_bits(__float2half_rn(f[2 * e]), __float2half_rn(f[2 * e + 1]));
+  *reinterpret_cast<uint4*>(out) = make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+// A's parts (the first product has one), 128 rows by 64 columns, and B, 64 by 64.
+struct NnMaps {
+  CUtensorMap a[kZParts], b;
+};
+struct NnShape {
+  int M, N, K;
+  int parts;  // of A
+  int bn, nx, tiles;
+  float scale;
+};
 
 // One 128 x bn tile (bn a multiple of 64) of out = scale A B. With gridDim.z = S > 1 the S
 // CTAs of a cluster (1, 1, S) take consecutive ranges of the reduction's stages; the fp32
 // partial tiles meet through distributed shared memory, in rank order, each CTA writing its
 // share of the rows. CTAs past the tiles (only without a split, on SMs that the tiles leave
 // idle) make the dense dictionary that the next product reads.
+// FIRST: dZ = s_C dY Cd, fp16 operands, into z. Otherwise dX = s_D z Dd, bf16 operands, into out.
+template <bool FIRST>
 __global__ void __launch_bounds__(kNnThreads, 1)
-    k_gemm_nn(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, int M, int N, int K,
-              int bn, float scale, __half* __restrict__ out, __half* __restrict__ low,
-              const __grid_constant__ CUtensorMap tm_low, int parts, int nx, int tiles, const __grid_constant__ DictCopy copy) {
+    k_gemm_nn(const __grid_constant__ NnMaps maps, const __grid_constant__ NnShape shape, const __grid_constant__ ZParts z,
+              __half* __restrict__ out, const __grid_constant__ DictCopy copy) {
+  const int M = shape.M, N = shape.N, K = shape.K, bn = shape.bn, nx = shape.nx, tiles = shape.tiles;
+  const float scale = shape.scale;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint8_t* sb = smem + kNnStages * kNnABytes;
@@ -104,7 +151,7 @@ __global__ void __launch_bounds__(kNnThreads, 1)
     return;
   }
   const int n0 = blockIdx.x % nx * bn, m0 = blockIdx.x / nx * kNnM, split = blockIdx.z, nsplit = gridDim.z;
-  const int nk_one = (K + kNnK - 1) / kNnK, nk_all = parts * nk_one;  // A's high part, then its low
+  const int nk_one = (K + kNnK - 1) / kNnK, nk_all = shape.parts * nk_one;  // A's parts in turn
   const int s_lo = (int)((long)nk_all * split / nsplit);
   const int nk = (int)((long)nk_all * (split + 1) / nsplit) - s_lo;
 
@@ -115,8 +162,8 @@ __global__ void __launch_bounds__(kNnThreads, 1)
     }
     mbar_init(accf, 1);
     fence_mbar_init();
-    tma_prefetch_map(&tm_a);
-    tma_prefetch_map(&tm_b);
+    tma_prefetch_map(&maps.a[0]);
+    tma_prefetch_map(&maps.b);
   }
   if (warp == 1) tmem_alloc(tmem_slot, kNnMaxN);
   tc_fence_before();
@@ -135,17 +182,16 @@ __global__ void __launch_bounds__(kNnThreads, 1)
           break;
         }
         mbar_arrive_expect_tx(&full[at.slot], kNnABytes + bn * kNnK * 2);
-        const bool second = s_lo + s >= nk_one;
-        const int kx = (s_lo + s - (second ? nk_one : 0)) * kNnK;
-        tma_load_2d(smem_u32(smem + at.slot * kNnABytes), second ? &tm_low : &tm_a, kx, m0, &full[at.slot]);
+        const int part = (s_lo + s) / nk_one, kx = (s_lo + s - part * nk_one) * kNnK;
+        tma_load_2d(smem_u32(smem + at.slot * kNnABytes), &maps.a[part], kx, m0, &full[at.slot]);
         for (int c = 0; c < bn / 64; ++c)
-          tma_load_2d(smem_u32(sb + at.slot * kNnBBytes + c * kMnChunk), &tm_b, n0 + 64 * c, kx, &full[at.slot]);
+          tma_load_2d(smem_u32(sb + at.slot * kNnBBytes + c * kMnChunk), &maps.b, n0 + 64 * c, kx, &full[at.slot]);
       }
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      // kind::f16, A (K-major) and B (MN-major) fp16, D fp32, M = 128, N = bn
-      const uint32_t idesc = (1u << 4) | (1u << 16) | ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(kNnM >> 4) << 24);
+      // kind::f16, A (K-major) and B (MN-major) fp16 or bf16, D fp32, M = 128, N = bn
+      const uint32_t idesc = (1u << 4) | (FIRST ? 0u : (1u << 7) | (1u << 10)) | (1u << 16) | ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(kNnM >> 4) << 24);
       const uint64_t a0 = smem_desc_sw128(smem_u32(smem)), b0 = smem_desc_mn_sw128(smem_u32(sb));
       RingPos at;
       for (int s = 0; s < nk; ++s, at.next(kNnStages)) {
@@ -179,7 +225,6 @@ __global__ void __launch_bounds__(kNnThreads, 1)
         continue;
       }
       if (!ok || m0 + row >= M) continue;
-      __half* orow = out + (size_t)(m0 + row) * N;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int gc = n0 + 32 * c + 8 * j;
@@ -187,7 +232,9 @@ __global__ void __launch_bounds__(kNnThreads, 1)
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * j + e]) * scale;
-        store8(orow + gc, low ? low + (size_t)(m0 + row) * N + gc : nullptr, f);
+        const size_t o = (size_t)(m0 + row) * N + gc;
+        if (FIRST) store_parts(z, o, f);
+        else store_half(out + o, f);
       }
     }
   }
@@ -210,9 +257,10 @@ __global__ void __launch_bounds__(kNnThreads, 1)
       if (m0 + row >= M || n0 + c >= N) continue;
       const uint32_t at = pbase + 4 * (row * pitch + c);
       const float4 x = sum_peers(at, nsplit), y = sum_peers(at + 16, nsplit);
-      const float f[8] = {x.x * scale, x.y * scale, x.z * scale, x.w * scale, y.x * scale, y.y * scale, y.z * scale, y.w * scale};
+      float f[8] = {x.x * scale, x.y * scale, x.z * scale, x.w * scale, y.x * scale, y.y * scale, y.z * scale, y.w * scale};
       const size_t o = (size_t)(m0 + row) * N + n0 + c;
-      store8(out + o, low ? low + o : nullptr, f);
+      if (FIRST) store_parts(z, o, f);
+      else store_half(out + o, f);
     }
     cluster_arrive();  // no CTA leaves while its sums are read
     cluster_wait();
@@ -261,7 +309,7 @@ int nn_clusters_that_fit(int S, int n_sm) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, (const void*)k_gemm_nn, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, (const void*)k_gemm_nn<true>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
@@ -295,27 +343,27 @@ NnPlan nn_plan(int M, int N, int K, int n_sm) {
 
 cudaError_t prepare_backward_kernels(int device) {
   (void)device;
-  return cudaFuncSetAttribute(k_gemm_nn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNnSmem);
+  const cudaError_t e = cudaFuncSetAttribute(k_gemm_nn<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNnSmem);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(k_gemm_nn<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNnSmem);
 }
 
-// A_low: A's second part, or null; low: where out's second part goes, or null.
-static cudaError_t launch_nn(const __half* A, const __half* A_low, const __half* B, int M, int N, int K, float scale,
-                             __half* out, __half* low, const NnPlan& plan, const DictCopy& copy, int helpers, cudaStream_t stream) {
-  CUtensorMap ta, tb, tl;
-  cudaError_t e = encode_tiled_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, A, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2, kNnK, kNnM,
-                                  CU_TENSOR_MAP_SWIZZLE_128B);
-  if (e != cudaSuccess) return e;
-  e = encode_tiled_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, B, (uint64_t)N, (uint64_t)K, (uint64_t)N * 2, 64, kNnK,
-                      CU_TENSOR_MAP_SWIZZLE_128B);
-  if (e != cudaSuccess) return e;
-  int parts = A_low ? 2 : 1;
-  tl = ta;
-  if (A_low && (e = encode_tiled_2d(&tl, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, A_low, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2, kNnK,
-                                    kNnM, CU_TENSOR_MAP_SWIZZLE_128B)))
-    return e;
-  int bn = plan.bn, nx = (N + bn - 1) / bn, tiles = nx * ((M + kNnM - 1) / kNnM);
+// A: the product's left operand in shape.parts parts, [M][K] each; B [K][N].
+template <bool FIRST>
+static cudaError_t launch_nn(const void* const* A, const void* B, NnShape shape, const ZParts& z, __half* out, const NnPlan& plan,
+                             const DictCopy& copy, int helpers, cudaStream_t stream) {
+  const CUtensorMapDataType type = FIRST ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t M = shape.M, N = shape.N, K = shape.K;
+  NnMaps maps;
+  cudaError_t e;
+  for (int p = 0; p < shape.parts; ++p)
+    if ((e = encode_tiled_2d(&maps.a[p], type, A[p], K, M, K * 2, kNnK, kNnM, CU_TENSOR_MAP_SWIZZLE_128B))) return e;
+  for (int p = shape.parts; p < kZParts; ++p) maps.a[p] = maps.a[0];  // not used
+  if ((e = encode_tiled_2d(&maps.b, type, B, N, K, N * 2, 64, kNnK, CU_TENSOR_MAP_SWIZZLE_128B))) return e;
+  shape.bn = plan.bn;
+  shape.nx = (shape.N + plan.bn - 1) / plan.bn;
+  shape.tiles = shape.nx * ((shape.M + kNnM - 1) / kNnM);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles + helpers, 1, plan.split);
+  cfg.gridDim = dim3(shape.tiles + helpers, 1, plan.split);
   cfg.blockDim = dim3(kNnThreads);
   cfg.dynamicSmemBytes = kNnSmem;
   cfg.stream = stream;
@@ -324,18 +372,18 @@ static cudaError_t launch_nn(const __half* A, const __half* A_low, const __half*
   set_cluster_z(attr[1], plan.split);
   cfg.attrs = attr;
   cfg.numAttrs = plan.split > 1 ? 2 : 1;
-  void* args[] = {(void*)&ta, (void*)&tb, &M, &N, &K, &bn, &scale, (void*)&out, (void*)&low, (void*)&tl, &parts, &nx, &tiles, (void*)&copy};
-  return cudaLaunchKernelExC(&cfg, (const void*)k_gemm_nn, args);
+  void* args[] = {(void*)&maps, (void*)&shape, (void*)&z, (void*)&out, (void*)&copy};
+  return cudaLaunchKernelExC(&cfg, (const void*)k_gemm_nn<FIRST>, args);
 }
 
-cudaError_t launch_backward_input(const dictproj_group* g, const dictproj_layer* l, const __half* dY, int M, __half* z,
-                                  const __half* Cd, __half* Dd, __half* dX, cudaStream_t stream) {
+cudaError_t launch_backward_input(const dictproj_group* g, const dictproj_layer* l, const __half* dY, int M, const __half* Cd,
+                                  __half* dX, cudaStream_t stream) {
   cudaError_t e;
-  const DictCopy copy = {g->codes, g->scales, Dd, (long)g->k * (g->d_in / 16)};
+  const DictCopy copy = {g->codes, g->scales, reinterpret_cast<__nv_bfloat16*>(g->ddense), (long)g->k * (g->d_in / 16)};
   const NnPlan p = nn_plan(M, g->k, l->d_out, g->n_sm);
   // SMs that the first product leaves idle make the dense dictionary, where they can in its
   // time (41 bytes a block at some 60 GB/s an SM): 2048 rows (4096 <- 2048 <- 11008) took 119 us
-  // with a launch for it.
+  // with a launch for it and one part of dZ.
   const int tiles = (g->k + p.bn - 1) / p.bn * ((M + kNnM - 1) / kNnM), idle = g->n_sm - tiles;
   int helpers = p.split == 1 && idle >= 8 && copy.n_blocks * 41e-3 / 60 / idle < 0.7 * p.us ? idle : 0;
   if (!helpers) {
@@ -350,10 +398,13 @@ cudaError_t launch_backward_input(const dictproj_group* g, const dictproj_layer*
     void* args[] = {(void*)&copy};
     if ((e = cudaLaunchKernelExC(&cfg, (const void*)k_densify_dict, args))) return e;
   }
-  __half* low = M <= kFineRows ? reinterpret_cast<__half*>(g->zlow) : nullptr;
-  if ((e = launch_nn(dY, nullptr, Cd, M, g->k, l->d_out, l->s, z, low, p, copy, helpers, stream))) return e;
-  return launch_nn(z, low, Dd, M, g->d_in, g->k, g->s, dX, nullptr, nn_plan(M, g->d_in, low ? 2 * g->k : g->k, g->n_sm), copy, 0,
-                   stream);
+  __nv_bfloat16* more = reinterpret_cast<__nv_bfloat16*>(g->zmore);
+  const ZParts z = {{reinterpret_cast<__nv_bfloat16*>(g->z16), more, more + (size_t)g->max_tokens * g->k}, M <= kFineRows ? 3 : 2};
+  const void* dy[] = {dY};
+  if ((e = launch_nn<true>(dy, Cd, NnShape{M, g->k, l->d_out, 1, 0, 0, 0, l->s}, z, nullptr, p, copy, helpers, stream))) return e;
+  const void* parts[] = {z.p[0], z.p[1], z.p[2]};
+  return launch_nn<false>(parts, g->ddense, NnShape{M, g->d_in, g->k, z.n, 0, 0, 0, g->s}, z, dX,
+                          nn_plan(M, g->d_in, z.n * g->k, g->n_sm), copy, 0, stream);
 }
 
 cudaError_t launch_wait_probe_backward(long long cycles, cudaStream_t stream) {

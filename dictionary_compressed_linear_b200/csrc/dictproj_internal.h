@@ -63,11 +63,12 @@ struct dictproj_group {
   // scratch
   float* z32;              // decode Z partial sums, fp32 [zslices][k][8]
   int zslices;             // d_in slices of the decode dictionary stage
-  uint16_t* z16;           // prefill Z, fp16 [max_tokens][k]
+  uint16_t* z16;           // prefill Z, fp16 [max_tokens][k]; the input gradient's dZ, first bf16 part
   uint16_t* cdense;        // prefill coefficient operand, fp16 [d_out][k] for d_out <= cdense_cols
   int cdense_cols;         // reserved output columns (dictproj_group_reserve_prefill)
-  uint16_t* zlow;          // input gradient of few rows: dZ's second part, fp16 [kFineRows][k], or null
-  uint16_t* ddense;        // input gradient: D^ densified, fp16 [k][d_in] (dictproj_group_reserve_backward), or null
+  // input gradient (dictproj_group_reserve_backward), or null
+  uint16_t* zmore;         // dZ's second part, bf16 [max_tokens][k], then the third, [kFineRows][k]
+  uint16_t* ddense;        // D^ densified, bf16 [k][d_in]
   CUtensorMap codes_map;   // TMA map of codes: [k] rows x [d_in/2] bytes, box 32 x 256
   // fused decode kernel
   bool fused_ok;           // the fused kernel serves this group

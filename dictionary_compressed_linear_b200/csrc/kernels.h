@@ -118,11 +118,11 @@ cudaError_t launch_densify_coeff(const dictproj_layer* l, __half* Cd, cudaStream
 cudaError_t launch_coeff_prefill(const dictproj_layer* l, const __half* Z, const __half* Cd, int M, __half* Y,
                                  cudaStream_t stream);
 cudaError_t take_prefill_error(unsigned int* out);
-constexpr int kFineRows = 32;  // rows up to which dZ keeps two parts
-// Input gradient of the projection from its densified coefficients Cd: z (fp16 [M][k]) =
-// s_C dY Cd, Dd = D^ densified (fp16 [k][d_in]), dX = s_D z Dd.
-cudaError_t launch_backward_input(const dictproj_group* g, const dictproj_layer* l, const __half* dY, int M, __half* z,
-                                  const __half* Cd, __half* Dd, __half* dX, cudaStream_t stream);
+constexpr int kFineRows = 32;  // rows up to which dZ keeps three parts, instead of two
+// Input gradient of the projection from its densified coefficients Cd: dZ = s_C dY Cd in bf16
+// parts (g->z16, g->zmore), g->ddense = D^ densified, dX = s_D dZ D^T.
+cudaError_t launch_backward_input(const dictproj_group* g, const dictproj_layer* l, const __half* dY, int M, const __half* Cd,
+                                  __half* dX, cudaStream_t stream);
 cudaError_t prepare_backward_kernels(int device);
 cudaError_t take_backward_error(unsigned int* out);
 cudaError_t launch_wait_probe_backward(long long cycles, cudaStream_t stream);

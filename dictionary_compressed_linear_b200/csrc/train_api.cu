@@ -331,15 +331,15 @@ int dictproj_group_reserve_backward(dictproj_group* g, int max_d_out) {
   if (!g) return fail(DICTPROJ_ERR_NULL, "group_reserve_backward: NULL handle");
   int st = check_device(g->device, "group_reserve_backward");
   if (st || (st = dictproj_group_reserve_prefill(g, max_d_out)) || g->ddense) return st;
-  uint16_t *p = nullptr, *low = nullptr;
+  uint16_t *p = nullptr, *more = nullptr;
   cudaError_t e = dmalloc((void**)&p, (size_t)g->k * g->d_in * sizeof(uint16_t));
-  if (e == cudaSuccess) e = dmalloc((void**)&low, (size_t)g->k * kFineRows * sizeof(uint16_t));
+  if (e == cudaSuccess) e = dmalloc((void**)&more, ((size_t)g->max_tokens + kFineRows) * g->k * sizeof(uint16_t));
   if (e != cudaSuccess) {
     cudaFree(p);
     cudaGetLastError();
     return fail(DICTPROJ_ERR_OOM, "group_reserve_backward: device allocation failed (%s)", cudaGetErrorName(e));
   }
-  g->zlow = low;
+  g->zmore = more;
   g->ddense = p;
   return DICTPROJ_OK;
 }
@@ -367,14 +367,11 @@ int dictproj_backward_input(const void* dY, int M, const dictproj_layer* layer, 
   int st;
   if ((st = check_device(group->device, "backward_input"))) return st;
   cudaStream_t s = (cudaStream_t)stream;
-  __half* z = reinterpret_cast<__half*>(group->z16);
   __half* cd = reinterpret_cast<__half*>(group->cdense);
-  __half* dd = reinterpret_cast<__half*>(group->ddense);
   cudaError_t e;
   if ((e = launch_densify_coeff(layer, cd, s)) != cudaSuccess)
     return cuda_fail(e, "backward_input: coefficient densify launch");
-  if ((e = launch_backward_input(group, layer, static_cast<const __half*>(dY), M, z, cd, dd, static_cast<__half*>(dX), s)) !=
-      cudaSuccess)
+  if ((e = launch_backward_input(group, layer, static_cast<const __half*>(dY), M, cd, static_cast<__half*>(dX), s)) != cudaSuccess)
     return cuda_fail(e, "backward_input: launch");
   return DICTPROJ_OK;
 }

@@ -504,17 +504,17 @@ int dictproj_adapter_backward(const dictproj_adapters* a, const dictproj_rows* r
                               const void* base, void* dX, float* dA, float* dB, int accumulate, void* stream);
 
 /* Reserve what dictproj_backward_input needs for layers with up to max_d_out
- * columns: the prefill coefficient scratch (dictproj_group_reserve_prefill) and
- * the group's dense dictionary, fp16 [k][d_in] (2 * k * d_in bytes), and 64 * k bytes. Errors as
- * dictproj_group_reserve_prefill. */
+ * columns: the prefill coefficient scratch (dictproj_group_reserve_prefill),
+ * the group's dense dictionary, bf16 [k][d_in] (2 * k * d_in bytes), and parts of dZ
+ * (2 * k * (max_tokens + 32) bytes). Errors as dictproj_group_reserve_prefill. */
 int dictproj_group_reserve_backward(dictproj_group* g, int max_d_out);
 
 /* Input gradient of the frozen projection Y = X D C: dX = dY C^T D^T, dY device
  * fp16 [M][d_out], dX device fp16 [M][d_in], 1 <= M <= max_tokens, d_out % 8 == 0.
  * Every layer format is served. dZ = s_C dY C^T and dX = s_D dZ D^T are tensor-core
- * products with fp32 accumulation; dZ is rounded to fp16 between them, as the
- * prefill forward rounds Z (gradients below 2^-24 of it are lost: scale the loss); up
- * to 32 rows it keeps two fp16 parts.
+ * products with fp32 accumulation; between them dZ is held in two bf16 parts (16 bits
+ * of it, in fp32's range; up to 32 rows three parts, 24 bits), so that dX is rounded
+ * once, to fp16. Rows do not reach other rows.
  * Asynchronous on `stream`, uses the group's scratch (one stream at a time).
  * Errors: NULL, RANGE (M, or not reserved), SHAPE (d_out % 8), MISMATCH, ALIGN
  * (dY, dX 16 bytes), CUDA. */

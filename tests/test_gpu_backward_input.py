@@ -73,6 +73,58 @@ def check(dX, dY, D, C):
         assert err.norm().item() <= 2 * U16 / math.sqrt(3) * want.norm().item()
 
 
+@pytest.mark.parametrize("M", [1, 32, 33, 129, 300])
+def test_every_batch_rounds_once(M):
+    # dX is the fp16 value nearest to (exact + delta). delta: a part of dZ is off by at most 2^-16 of its element (two
+    # bf16 parts), a third of that squared in the mean square; the fp32 sums are a random walk of 2^-23 a term, with a
+    # factor 4 of room. It moves a result to the neighbouring value, a step of at most 2^-10 of it away, with
+    # probability |delta| / step, so that the squared difference from the rounded exact result is |delta| step on the
+    # average: at most |delta| |step| in norms (Cauchy-Schwarz). A dZ in one fp16 part differs by 3e-4.
+    d_in, k, d_out = 1376, 1040, 1000
+    g, l, D, C = projection(d_in, k, d_out, "u8", M)
+    dY = torch.randn(M, d_out, generator=torch.Generator().manual_seed(3)).half().cuda()
+    dX = torch.empty(M, d_in, dtype=torch.float16, device="cuda")
+    dp.dictproj_backward_input(dY.data_ptr(), M, l, g, dX.data_ptr(), stream())
+    torch.cuda.synchronize()
+    want = (dY.double() @ C.T) @ D.T
+    delta = 2.0 ** -16 / math.sqrt(3) + 4 * 2.0 ** -23 * math.sqrt(d_out + 2 * k)
+    assert (dX.double() - want.half().double()).norm().item() <= math.sqrt(delta * 2.0 ** -10) * want.norm().item()
+
+
+@pytest.mark.parametrize("M", [5, 100])
+@pytest.mark.parametrize("power", [-30, -16, 16, 30])
+def test_dz_has_the_range_of_fp32(M, power):
+    # a power of two moved from C to D changes dZ's size and nothing else: the same bits
+    D, C = synth.gen_dictionary(40, 0, 0, 256, 128), synth.gen_coeff(40, 0, 0, 0, 128, 200, 0.3)
+    dY = torch.randn(M, 200, generator=torch.Generator().manual_seed(M)).half().cuda()
+    out = []
+    for e in (0, power):
+        g = dp.dictproj_pack_group((D * np.float32(2.0 ** -e)).astype(np.float32), M)
+        l = dp.dictproj_pack_layer(C.col_ptr, C.atom_idx, (C.vals * np.float32(2.0 ** e)).astype(np.float32), 128, 200)
+        dp.dictproj_group_reserve_backward(g, 200)
+        dX = torch.empty(M, 256, dtype=torch.float16, device="cuda")
+        dp.dictproj_backward_input(dY.data_ptr(), M, l, g, dX.data_ptr(), stream())
+        torch.cuda.synchronize()
+        out.append(dX)
+    assert torch.isfinite(out[0]).all() and out[0].abs().max() > 0
+    assert torch.equal(out[0], out[1])
+
+
+@pytest.mark.parametrize("M", [9, 200])
+def test_an_infinity_or_nan_stays_in_its_row(M):
+    g, l, D, C = projection(544, 272, 328, "u8", M)
+    dY = torch.randn(M, 328, generator=torch.Generator().manual_seed(M)).half().cuda()
+    clean, dX = (torch.empty(M, 544, dtype=torch.float16, device="cuda") for _ in range(2))
+    dp.dictproj_backward_input(dY.data_ptr(), M, l, g, clean.data_ptr(), stream())
+    bad = [1, M // 2, M - 1]
+    dY[1, 7], dY[M // 2, 0], dY[M - 1] = float("inf"), float("nan"), -float("inf")
+    dp.dictproj_backward_input(dY.data_ptr(), M, l, g, dX.data_ptr(), stream())
+    torch.cuda.synchronize()
+    keep = [m for m in range(M) if m not in bad]
+    assert torch.equal(dX[keep], clean[keep])
+    assert not torch.isfinite(dX[bad]).any()
+
+
 SHAPES = [(32, 16, 8, 1), (256, 128, 200, 5), (544, 272, 328, 37), (1376, 1040, 1000, 129), (4096, 2048, 4096, 64), (288, 304, 72, 300)]
 
 
