@@ -68,9 +68,12 @@ __device__ __forceinline__ Updated adamw_element(float p, float grad, float m, f
   return u;
 }
 
-// Largest of the warp's non-negative values (their bits order as integers; a NaN wins).
-__device__ __forceinline__ float warp_max(float x) {
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+// The scale of a block from a lane's four values: amax / 448, at least kTinyScale. Magnitudes
+// order as their bits do, a NaN above the infinities, so that it is the maximum and the scale.
+__device__ __forceinline__ float block_scale(float a, float b, float c, float d) {
+  const uint32_t m = max(max(__float_as_uint(fabsf(a)), __float_as_uint(fabsf(b))), max(__float_as_uint(fabsf(c)), __float_as_uint(fabsf(d))));
+  const float s = __fmul_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, m)), kScalePerAmax);
+  return s < kTinyScale ? kTinyScale : s;
 }
 
 // Four consecutive values of a lane, zeros past n; one load where the arrays allow it.
@@ -160,9 +163,10 @@ __device__ __forceinline__ void adamw_chunk(const AdamwChunk& c, const AdamwFact
       store4<MODE>(static_cast<float*>(c.v), i, n, make_float4(u[0].v, u[1].v, u[2].v, u[3].v));
       continue;
     }
-    // past n every value is what zeros become: p = m = v = 0, which decides no scale
-    const Divisor dm = divisor(fmaxf(__fmul_rn(warp_max(fmaxf(fmaxf(fabsf(u[0].m), fabsf(u[1].m)), fmaxf(fabsf(u[2].m), fabsf(u[3].m)))), kScalePerAmax), kTinyScale));
-    const Divisor dr = divisor(fmaxf(__fmul_rn(warp_max(fmaxf(fmaxf(u[0].r, u[1].r), fmaxf(u[2].r, u[3].r))), kScalePerAmax), kTinyScale));
+    // past n nothing decides a scale (a zero code times a scale that is not finite would)
+    const int left = MODE == 2 ? 4 : n - i;
+    const Divisor dm = divisor(block_scale(left > 0 ? u[0].m : 0.f, left > 1 ? u[1].m : 0.f, left > 2 ? u[2].m : 0.f, left > 3 ? u[3].m : 0.f));
+    const Divisor dr = divisor(block_scale(left > 0 ? u[0].r : 0.f, left > 1 ? u[1].r : 0.f, left > 2 ? u[2].r : 0.f, left > 3 ? u[3].r : 0.f));
     if (lane == 0) {
       c.m_scale[blk] = dm.s;
       c.v_scale[blk] = dr.s;

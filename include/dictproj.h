@@ -550,7 +550,8 @@ int dictproj_backward_input(const void* dY, int M, const dictproj_layer* layer, 
  *   h *= 0xBB67AE85; h ^= h >> 15; h *= 0x6A09E667; d = h >> 12. The same inputs
  *   give the same bits.
  * A gradient that is not finite spreads into its element, and with 8-bit states
- * into its block: check before the step.
+ * into its block: a NaN among m' or r' makes the block's scale NaN, an infinity makes
+ * it infinite (code 0 beside it is then NaN). Check before the step.
  *
  * p, g, m, v (32 bits) and the scales must be 4-byte aligned, copy 2-byte; 16-byte
  * alignment of all (4 for the codes) is faster. Only gradients may overlap one another. */

@@ -77,6 +77,47 @@ def test_steps_bit_for_bit(bits, shift):
             check(d, want, f"n={t['p'].size}")
 
 
+BAD = {"one nan": {5: np.nan}, "a lane of nans": {132: np.nan, 133: np.nan, 134: np.nan, 135: np.nan}, "an infinity": {300: np.inf},
+       "minus infinity": {511: -np.inf}, "both": {640: np.inf, 700: np.nan}, "the last": {999: np.nan}, "an infinity in a short block": {990: np.inf},
+       "a whole block of nans": {i: np.nan for i in range(256, 384)}}
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("what", list(BAD))
+def test_a_gradient_that_is_not_finite_spreads_as_stated(what, shift, bits):
+    n = 1000
+    t = host_tensor(n, bits, 77)
+    t["g"][list(BAD[what])] = list(BAD[what].values())
+    d = on_device(t, shift)
+    plan = dp.dictproj_adamw_create([entry(d)], bits)
+    touched = np.zeros(n, bool)
+    for i in BAD[what]:
+        touched[i if bits == 32 else slice(i // 128 * 128, i // 128 * 128 + 128)] = True
+    value = lambda t, k: ref.e4m3_value(t[k]) * ref.each(t[k + "_scale"], n) if bits == 8 else t[k]  # noqa: E731
+    for step in (1, 2):  # the second with a clean gradient: what the states carry on
+        dp.dictproj_adamw_step(plan, step, stream=stream(), **HYPER)
+        with np.errstate(invalid="ignore", over="ignore"):
+            t = ref.adamw(t, step, bits=bits, **HYPER)
+        torch.cuda.synchronize()
+        got = {k: x.cpu().numpy() for k, x in d.items()}
+        with np.errstate(invalid="ignore"):
+            values = {k: (value(got, k), value(t, k)) for k in ("m", "v")}
+        for k, (a, b) in values.items():
+            assert np.array_equal(a, b, equal_nan=True), (step, k)
+            assert np.array_equal(got[k][~touched], t[k][~touched]), (step, k)  # and what they are held as
+            assert not np.isfinite(a[list(BAD[what])]).any()
+        for k in ("p", "copy", "m_scale", "v_scale"):
+            if k in t:
+                assert np.array_equal(got[k], t[k], equal_nan=True), (step, k)
+        assert np.isfinite(got["p"][~touched]).all() and np.isfinite(values["m"][0][~touched]).all()
+        if bits == 8:
+            assert not np.isfinite(values["m"][0][touched]).any()
+        clean = host_tensor(n, bits, 78)["g"]
+        t["g"] = clean
+        d["g"].copy_(torch.from_numpy(clean))
+
+
 def test_what_lies_between_the_tensors_is_not_touched():
     n, total = 130, 400
     arena = {k: torch.full((total,), 5.0, device="cuda") for k in "pgmv"}
