@@ -26,9 +26,11 @@ __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t two) {
 
 // x / s for many x and one s, correctly rounded. Markstein (1990): with y the correctly
 // rounded 1 / s, q = x y and q + y (x - q s), the residual by fma, is the rounded
-// quotient as long as nothing leaves the normal range. For 2^-90 <= s <= 2^100 only an x
-// below 2^-125 can make the residual subnormal; then x / s < 2^-35, which is code 0 with
-// and without the dither. Other scales (a block of zeros, of overflowing moments) divide.
+// quotient as long as the residual is exact. With 2^-90 <= s <= 2^100 that holds for every
+// quotient from 2^-11 on: the residual is a multiple of ulp(q) ulp(s) >= 2^-34 2^-113 = 2^-147.
+// A smaller quotient, right in its last bit or not, is code 0 for m (2^-10 is half the smallest
+// code) and code 1 for r > 0 (its bits are below 2^18 and the dither's below 2^20: 0 or 1, and r > 0
+// has at least 1). Other scales (a block of zeros, of overflowing moments) divide.
 struct Divisor {
   float s, y;
   bool fast;

@@ -118,6 +118,30 @@ def test_a_gradient_that_is_not_finite_spreads_as_stated(what, shift, bits):
         d["g"].copy_(torch.from_numpy(clean))
 
 
+def test_scales_at_the_ends_of_the_fast_quotient():
+    # blocks whose scale crosses 2^-90 and 2^100, elements down to the subnormals: bit for bit all the same
+    r = np.random.default_rng(11)
+    n = 128 * 96
+    top = np.concatenate([np.linspace(-93, -87, 48), np.linspace(97, 103, 48)])[:, None]  # of log2 of the block's scale
+    size = np.minimum(2.0 ** (top + 8.7 - 45 * r.random((96, 128)) ** 2), 2.0 ** 127)
+    size[:, 0] = 2.0 ** (top[:, 0] + 8.7)
+    g = (size * r.choice([-1, 1], size.shape) * 10).reshape(-1).astype(np.float32)  # m' = 0.1 g
+    t = {"p": r.standard_normal(n).astype(np.float32), "g": g, "m": np.zeros(n, np.uint8), "v": np.zeros(n, np.uint8),
+         "m_scale": np.ones(n // 128, np.float32), "v_scale": np.ones(n // 128, np.float32)}
+    d = on_device(t)
+    plan = dp.dictproj_adamw_create([entry(d)], 8)
+    hyper = {**HYPER, "grad_scale": 1.0, "lr": 0.0}
+    dp.dictproj_adamw_step(plan, 1, stream=stream(), **hyper)
+    torch.cuda.synchronize()
+    with np.errstate(over="ignore", under="ignore", invalid="ignore"):
+        t = ref.adamw(t, 1, bits=8, **hyper)
+    assert (np.abs(np.log2(t["m_scale"][:48].astype(float)) + 90) < 4).all()
+    for k in ("m", "m_scale"):
+        assert np.array_equal(d[k].cpu().numpy(), t[k]), k
+    low = slice(0, 128 * 48)  # above, v' overflows
+    assert np.array_equal(d["v"].cpu().numpy()[low], t["v"][low]) and np.array_equal(d["p"].cpu().numpy()[low], t["p"][low])
+
+
 def test_what_lies_between_the_tensors_is_not_touched():
     n, total = 130, 400
     arena = {k: torch.full((total,), 5.0, device="cuda") for k in "pgmv"}
