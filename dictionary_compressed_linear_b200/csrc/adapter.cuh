@@ -37,7 +37,6 @@ struct RowsArgs {
   const float* scale;
   int rp, pp, n_slots, rows, cluster;
   int only;  // -1: every tile; 0: no crowds' tiles; 1: crowds' tiles alone
-  int last;  // the expansion follows the weight gradients (see launch_adapter_backward), not the contraction
 };
 
 struct GradPass {

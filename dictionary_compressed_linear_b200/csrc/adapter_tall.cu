@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_expand_tall(const __grid_con
     };
     const int first = min(stages, nb);
     for (int i = 0; i < first; ++i) load(i);
-    if (!g.last) grid_dependency_wait();
+    grid_dependency_wait();
     {  // T: chunks of 64 of a row's 2 R elements, 64 rows a box; past the tile's rows whatever is there
       const int half = S::kTChunks / 2, used = R <= 64 ? S::kTChunks : r16 > 64 ? 4 : 2;
       if (lane == 0) mbar_arrive_expect_tx(&tfull, used * kTallRows * 128);
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_expand_tall(const __grid_con
   }
   __syncwarp();
   if (warp >= 2) {
-    if (!g.last) grid_dependency_wait();  // the units are the contraction's
+    grid_dependency_wait();  // the units are the contraction's
     const int q = warp & 3, h = (warp - 2) >> 2, tr = 32 * q + lane;
     const uint32_t mine = smem_u32(smem + S::kTBytes) + (warp - 2) * 2048;
     const float back = __ldcg(a.unit + tile.w + (tr >= kWideRows && count > kWideRows ? 1 : 0));
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
   const int which = (int)blockIdx.x < g.pass[0].blocks ? 0 : 1;
   const GradPass& a = g.pass[which];
   const int col0 = ((int)blockIdx.x - (which ? g.pass[0].blocks : 0)) * kGradCols;
-  // The launch before is the expansion or the contraction of the same call: what was there
+  // The launch before is the contraction of the same call: what was there
   // before the call (plan, ranks, In) is complete and may be read before the wait.
   const int p0 = __ldcg(g.start + slot), rows = __ldcg(g.start + slot + 1) - p0, tile0 = __ldcg(g.first64 + slot);
   const int r = rows ? __ldcg(g.rank + slot) : 0, r16 = (r + 15) & ~15;
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
       gather(s);
     }
     grid_dependency_wait();
-    trigger_dependents();  // all CTAs hold their tensor memory; the expansion may start on the contraction's end
+    trigger_dependents();  // all CTAs hold their tensor memory; the expansion's first loads may go out
     for (int s = 0; s < first; ++s) parts(s);
     for (int s = first; s < nt; ++s) {
       bool ok = true;
