@@ -444,7 +444,9 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_c
   constexpr int TM = S::TM, CW = S::CW, PITCH = S::kPitch, PIECES = PITCH / 16, STEP = kRowThreads / PIECES;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int srow[TM];
-  __shared__ __align__(16) float smax[kRowThreads / 32], cmax[8];
+  // largest values (bits) of the share's rows, of the ranks in it, and of the ranks by CTA
+  __shared__ uint32_t rowmax[TM], rankmax[R], allmax[8][R];
+  __shared__ __align__(16) float units[R];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cluster = g.cluster, rankc = blockIdx.x % cluster, tile_no = blockIdx.x / cluster;
   const RowsPass& a = g.pass[blockIdx.y];
@@ -458,6 +460,7 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_c
   const int count = tile.z & (kCrowdTile - 1), slot = tile.x, r = g.rank[slot], r16 = (r + 15) & ~15;
   if (r == 0) return;
   if (tid < TM) srow[tid] = tid < count ? g.perm[tile.y + tid] : tile.w;
+  for (int i = tid; i < TM + R; i += kRowThreads) (i < TM ? rowmax[i] : rankmax[i - TM]) = 0;
   const bool vec = (a.K & 7) == 0;
   const int kc = (a.K + CW - 1) / CW, nk = (kc - rankc + cluster - 1) / cluster;  // blocks in turn
   const float scale = g.scale[slot];
@@ -551,41 +554,45 @@ __global__ void __launch_bounds__(kRowThreads) k_adapter_contract(const __grid_c
   float* own = reinterpret_cast<float*>(smem);  // [TM / cluster][R], over the drained ring
   const uint32_t pbase = smem_u32(part);
   const int share = TM / cluster, row_lo = rankc * share;
-  float m = 0.f;
+  // a thread's ranks are always the same four
+  static_assert(4 * kRowThreads % R == 0, "ranks of a thread");
+  const int j = 4 * tid % R;
+  uint4 most = make_uint4(0, 0, 0, 0);
   for (int i = 4 * tid; i < share * R; i += 4 * kRowThreads) {
-    const int j = i % R, row = row_lo + i / R;
+    const int row = row_lo + i / R;
     if (j >= r16 || row >= count) continue;
-    const uint32_t at = pbase + 4 * (row * R + j);
-    const float4 x = sum_peers(at, cluster);
-    const float v[4] = {j < r ? x.x * scale : 0.f, j + 1 < r ? x.y * scale : 0.f, j + 2 < r ? x.z * scale : 0.f,
-                        j + 3 < r ? x.w * scale : 0.f};
-    *reinterpret_cast<float4*>(own + i) = make_float4(v[0], v[1], v[2], v[3]);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (fabsf(v[e]) <= 3.0e38f) m = fmaxf(m, fabsf(v[e]));  // an infinity or NaN does not decide the others' digits
+    const float4 x = sum_peers(pbase + 4 * (row * R + j), cluster);
+    const float4 t = make_float4(j < r ? x.x * scale : 0.f, j + 1 < r ? x.y * scale : 0.f, j + 2 < r ? x.z * scale : 0.f,
+                                 j + 3 < r ? x.w * scale : 0.f);
+    *reinterpret_cast<float4*>(own + i) = t;
+    const uint4 bits = finite_bits(t);
+    if (a.parts) atomicMax(&rowmax[i / R], largest(bits));
+    most = larger(most, bits);
   }
-  m = warp_max_bits(m);
-  if (lane == 0) smax[warp] = m;
+  if (a.gparts && j < r16) atomic_larger(rankmax + j, most);
   __syncthreads();
-  if (tid < cluster) {
-#pragma unroll
-    for (int w = 0; w < kRowThreads / 32; ++w) m = fmaxf(m, smax[w]);
-    st_peer_f32(peer_smem(smem_u32(cmax + rankc), tid), m);
-  }
+  if (a.gparts)
+    for (int i = tid; i < r16 * cluster; i += kRowThreads)
+      st_peer_u32(peer_smem(smem_u32(&allmax[rankc][i % r16]), i / r16), rankmax[i % r16]);
   cluster_arrive();
+  auto value = [&](int i) { return row_lo + i / R < count ? *reinterpret_cast<const float4*>(own + i) : make_float4(0.f, 0.f, 0.f, 0.f); };
+  auto at = [&](__half* parts, int i) { return parts + (size_t)(tile_no * TM + row_lo + i / R) * (2 * g.pp) + j; };
+  if (a.parts) {
+    for (int i = 4 * tid; i < share * R && j < r16; i += 4 * kRowThreads) {
+      const float u = split_unit(__uint_as_float(rowmax[i / R]));
+      write_parts(at(a.parts, i), g.pp, value(i), make_float4(u, u, u, u));
+    }
+    if (tid < share) a.unit[(size_t)tile_no * TM + row_lo + tid] = 1.f / split_unit(__uint_as_float(rowmax[tid]));
+  }
   cluster_wait();
-  m = 0.f;
-  for (int c = 0; c < cluster; ++c) m = fmaxf(m, cmax[c]);
-  const float unit = split_unit(m);
-  if (rankc == 0 && tid == 0) a.unit[tile_no] = 1.f / unit;
-  for (int i = 4 * tid; i < share * R; i += 4 * kRowThreads) {
-    const int j = i % R, row = row_lo + i / R;
-    if (j >= r16) continue;
-    const float4 x = row < count ? *reinterpret_cast<const float4*>(own + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const Split s0 = split_half(x.x * unit), s1 = split_half(x.y * unit), s2 = split_half(x.z * unit), s3 = split_half(x.w * unit);
-    __half* at = a.parts + (size_t)(tile_no * TM + row) * (2 * g.pp) + j;
-    *reinterpret_cast<uint2*>(at) = make_uint2(half2_bits(s0.hi, s1.hi), half2_bits(s2.hi, s3.hi));
-    *reinterpret_cast<uint2*>(at + g.pp) = make_uint2(half2_bits(s0.lo, s1.lo), half2_bits(s2.lo, s3.lo));
+  if (a.gparts) {
+    if (tid < r16) {
+      units[tid] = rank_unit(&allmax[0][tid], R, cluster);
+      if (rankc == 0) a.gunit[(size_t)tile_no * g.pp + tid] = 1.f / units[tid];
+    }
+    __syncthreads();
+    const float4 u = *reinterpret_cast<const float4*>(units + j);
+    for (int i = 4 * tid; i < share * R && j < r16; i += 4 * kRowThreads) write_parts(at(a.gparts, i), g.pp, value(i), u);
   }
 }
 
@@ -677,7 +684,7 @@ __global__ void __launch_bounds__(kRowThreads, R <= 32 ? 3 : 2) k_adapter_expand
       thi[t][q] = in ? __ldcg(reinterpret_cast<const uint32_t*>(at)) : 0u;
       tlo[t][q] = in ? __ldcg(reinterpret_cast<const uint32_t*>(at + g.pp)) : 0u;
     }
-  const float back = __ldcg(a.unit + tile_no);
+  const float back[2] = {__ldcg(a.unit + (size_t)tile_no * TM + g0), __ldcg(a.unit + (size_t)tile_no * TM + g0 + 8)};
   constexpr int NT = CW / 16;  // 8-column tiles of a warp
   const int cw = 8 * NT * half;
   for (int i = 0; i < nb; ++i) {
@@ -709,7 +716,7 @@ __global__ void __launch_bounds__(kRowThreads, R <= 32 ? 3 : 2) k_adapter_expand
         const uint32_t at = st + swz<PITCH>(g0 + 8 * q, cw / 8 + n) + 2 * c0;
         const uint32_t bw = a.base ? lds_u32(at) : 0u;
         const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&bw));
-        const __half2 o = __floats2half2_rn(fmaf(acc[n][2 * q], back, b.x), fmaf(acc[n][2 * q + 1], back, b.y));
+        const __half2 o = __floats2half2_rn(fmaf(acc[n][2 * q], back[q], b.x), fmaf(acc[n][2 * q + 1], back[q], b.y));
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(*reinterpret_cast<const uint32_t*>(&o)) : "memory");
       }
     __syncthreads();
@@ -726,7 +733,7 @@ __global__ void __launch_bounds__(kRowThreads, R <= 32 ? 3 : 2) k_adapter_expand
 // rows x kGradCols. A CTA owns kGradCols columns of one slot's gradient; a cluster
 // splits the slot's 64-row tiles and sums through distributed shared memory in rank
 // order. Per tile the products of T's two parts are accumulated by the MMA and then
-// added, times the tile's unit, to fp32 sums: a long sum is rounded to nearest once a
+// added, times the rank's unit, to fp32 sums: a long sum is rounded to nearest once a
 // tile, not truncated at each MMA.
 constexpr int kGradThreads = 256;
 
@@ -828,7 +835,7 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
     issue_in(i + S::kStages - 1);
     issue_t(i + S::kStages - 1);
     const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
-    const float unit = __ldcg(a.unit + tile0 + t_lo + i);
+    const float* unit = a.unit + (size_t)(tile0 + t_lo + i) * g.pp + (lane >> 2);
     uint32_t bf[4][4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -837,6 +844,7 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
     for (int t = 0; t < R / 16; ++t) {
       if (16 * t >= r16) break;
       float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      const float back[2] = {__ldcg(unit + 16 * t), __ldcg(unit + 16 * t + 8)};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t hi[4], lo[4];
@@ -851,7 +859,7 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) sum[t][n][q] = fmaf(acc[n][q], unit, sum[t][n][q]);
+        for (int q = 0; q < 4; ++q) sum[t][n][q] = fmaf(acc[n][q], back[q >> 1], sum[t][n][q]);
     }
   }
   cp_async_wait<0>();
@@ -1142,10 +1150,15 @@ cudaError_t launch_rows_plan(const dictproj_rows* r, const int* ids, int M, cuda
                     ((size_t)kPlanWarps * (ns + 1) + 4 * (ns + 2)) * sizeof(int), stream, args);
 }
 
-static void set_parts(const dictproj_adapters* a, RowsArgs& g) {
-  for (int i = 0; i < 2; ++i) {
-    g.pass[i].parts = reinterpret_cast<__half*>(a->parts[i]);
-    g.pass[i].unit = a->unit[i];
+// What a contraction leaves: pass 0 for an expansion, both passes for the weight gradients.
+static void set_parts(const dictproj_adapters* a, RowsArgs& g, bool expand, bool grads) {
+  if (expand) {
+    g.pass[0].parts = reinterpret_cast<__half*>(a->parts);
+    g.pass[0].unit = a->unit;
+  }
+  for (int i = 0; i < 2 && grads; ++i) {
+    g.pass[i].gparts = reinterpret_cast<__half*>(a->gparts[i]);
+    g.pass[i].gunit = a->gunit[i];
   }
 }
 
@@ -1172,7 +1185,7 @@ cudaError_t launch_adapter_forward(const dictproj_adapters* a, const dictproj_ro
   RowsArgs g = rows_args(a, r, true);
   g.pass[0] = rows_pass(a, true, X, base, Y);
   if (!all) g.only = 1;
-  set_parts(a, g);
+  set_parts(a, g, true, false);
   e = launch_contract(g, 1, false, a, r, stream);
   return e == cudaSuccess ? launch_expand(g, a, r, stream) : e;
 }
@@ -1196,12 +1209,12 @@ cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_r
   RowsArgs g = rows_args(a, r, true);
   g.pass[0] = rows_pass(a, false, dY, base, dX);
   g.pass[1] = rows_pass(a, true, X, nullptr, nullptr);
-  set_parts(a, g);
+  set_parts(a, g, dX != nullptr, dA != nullptr);
   GradArgs w = {};
   for (int i = 0; i < 2; ++i) {
     w.pass[i].in = i ? dY : X;
-    w.pass[i].parts = g.pass[i].parts;
-    w.pass[i].unit = a->unit[i];
+    w.pass[i].parts = g.pass[i].gparts;
+    w.pass[i].unit = g.pass[i].gunit;
     w.pass[i].g = i ? dB : dA;
     w.pass[i].K = i ? a->d_out : a->d_in;
     w.pass[i].blocks = (w.pass[i].K + kGradCols - 1) / kGradCols;
@@ -1227,7 +1240,7 @@ cudaError_t launch_adapter_backward(const dictproj_adapters* a, const dictproj_r
     RowsArgs f = rows_args(a, r, false);
     for (int i = 0; i < 2; ++i) {
       f.pass[i] = g.pass[i];
-      w.pass[i].sums = f.pass[i].sums = dA ? reinterpret_cast<float*>(a->parts[i]) : nullptr;
+      w.pass[i].sums = f.pass[i].sums = dA ? reinterpret_cast<float*>(a->gparts[i]) : nullptr;
       w.pass[i].blocks = (w.pass[i].K + kFewGradCols - 1) / kFewGradCols;
     }
     const cudaError_t e = launch_few(f, dA ? 2 : 1, r, stream);

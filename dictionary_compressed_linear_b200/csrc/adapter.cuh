@@ -19,10 +19,14 @@ struct RowsPass {
   const __half* Q;
   const __half* base;
   __half* out;
-  // many rows: the two parts of scale * T, [tile][kWideRows][high pp | low pp], zeros past
-  // a tile's rows, and what the parts of a tile are multiplied with
+  // many rows: scale * T in two parts, [64-row tile][kWideRows][high pp | low pp], zeros past a
+  // tile's rows, and what the parts are multiplied with: for the expansion, which sums over the
+  // ranks, a number for each row; for the weight gradients, which sum over the rows, one for each
+  // tile and rank ([tile][pp]). Null: not wanted.
   __half* parts;
   float* unit;
+  __half* gparts;
+  float* gunit;
   float* sums;  // few rows, backward: scale * T in plan order, [rows][pp], or null
   int K, N, ld_p, ld_q;
 };
@@ -101,18 +105,19 @@ __device__ __forceinline__ float4 sum_peers(uint32_t local, int cluster) {
     if (c < cluster) v[0].x += v[c].x, v[0].y += v[c].y, v[0].z += v[c].z, v[0].w += v[c].w;
   return v[0];
 }
-__device__ __forceinline__ void st_peer_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void st_peer_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ uint32_t half2_bits(__half a, __half b) {
   const __half2 h = __halves2half2(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// T in two fp16 parts: t * unit = high + low with |t * unit| < 2^14, so that the two
-// together keep 22 bits of it, or 2^-24 absolute (2^-38 of the tile's largest): the
-// MMA's fp16 operands then carry T as exactly as the fp32 sums that made it, whatever
-// its size. unit is a power of two.
+// T in two fp16 parts: t * unit = high + low, unit a power of two that brings the largest
+// of the values it serves (a row's, or a rank's in a tile) to 2^13 or more, below 2^14. The
+// two parts keep 22 bits of a value down to 2^-16 of that largest one; below, what they
+// leave out is at most 2^-38 of the largest (half of fp16's smallest step, 2^-25, of 2^13).
+// With one unit for all of a tile, rows or ranks 2^-26 below the largest kept 12 bits.
 struct Split {
   __half hi, lo;
 };
@@ -248,9 +253,35 @@ __device__ __forceinline__ void zero_columns(float* out, int K, int width, int n
   }
 }
 
-// Largest of the warp's finite non-negative values.
-__device__ __forceinline__ float warp_max_bits(float m) {
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+// The magnitude's bits, which order as it does; an infinity or NaN does not decide the others'
+// digits.
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+  return fabsf(x) <= 3.0e38f ? __float_as_uint(fabsf(x)) : 0u;
+}
+__device__ __forceinline__ uint4 finite_bits(const float4& x) {
+  return make_uint4(finite_bits(x.x), finite_bits(x.y), finite_bits(x.z), finite_bits(x.w));
+}
+__device__ __forceinline__ uint32_t largest(const uint4& x) { return max(max(x.x, x.y), max(x.z, x.w)); }
+__device__ __forceinline__ uint4 larger(const uint4& a, const uint4& b) {
+  return make_uint4(max(a.x, b.x), max(a.y, b.y), max(a.z, b.z), max(a.w, b.w));
+}
+__device__ __forceinline__ void atomic_larger(uint32_t* at, const uint4& x) {
+  atomicMax(at, x.x);
+  atomicMax(at + 1, x.y);
+  atomicMax(at + 2, x.z);
+  atomicMax(at + 3, x.w);
+}
+// The unit of a rank from the largest values that n CTAs found, `stride` apart.
+__device__ __forceinline__ float rank_unit(const uint32_t* maxima, int stride, int n) {
+  uint32_t m = 0;
+  for (int c = 0; c < n; ++c) m = max(m, maxima[c * stride]);
+  return split_unit(__uint_as_float(m));
+}
+// Four values of T times their units, in two parts.
+__device__ __forceinline__ void write_parts(__half* at, int pp, const float4& x, const float4& u) {
+  const Split s0 = split_half(x.x * u.x), s1 = split_half(x.y * u.y), s2 = split_half(x.z * u.z), s3 = split_half(x.w * u.w);
+  *reinterpret_cast<uint2*>(at) = make_uint2(half2_bits(s0.hi, s1.hi), half2_bits(s2.hi, s3.hi));
+  *reinterpret_cast<uint2*>(at + pp) = make_uint2(half2_bits(s0.lo, s1.lo), half2_bits(s2.lo, s3.lo));
 }
 
 }  // namespace dictproj

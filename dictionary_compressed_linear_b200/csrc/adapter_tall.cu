@@ -39,7 +39,8 @@ constexpr int kCols = 64;          // columns of a stage (one 128-byte swizzle r
 // A cluster splits the K columns of one tile of up to 128 rows of one slot. Per 64-column
 // stage 128 gathered rows of In (16 KB) and r rows of P_s; D = In P^T, rows x r, in tensor
 // memory. The CTAs' partial sums meet through distributed shared memory, in rank order;
-// each CTA writes its share of the rows as two fp16 parts, with a unit for each 64 rows.
+// each CTA writes its share of the rows as two fp16 parts, with a unit for each row and, for
+// the weight gradients, once more with one for each rank of 64 rows.
 // A long accumulation on the tensor cores is less exact than fp32 sums: with all of K in one
 // accumulator the weight gradients of 2048 rows came out more than 1e-6 off (relative norm).
 // For them every `flush` stages get an accumulator of their own (two in turn), which the
@@ -58,6 +59,9 @@ struct TallContract {
   static constexpr int kInBytes = kTallRows * 128, kStageBytes = kInBytes + R * 128;
   static constexpr int kPitch = R + 4;  // floats of a row of the partial sums, which lie over the drained ring
   static constexpr int kPart = kTallRows * kPitch * 4;
+  // behind the ring, largest values (bits) of the share's rows [64] and of the ranks in it [R], of
+  // the ranks by CTA [4][R] (those of 64 rows are half a cluster), and the ranks' units [R]
+  static constexpr int kFixed = (kWideRows + 6 * R) * 4;
   static constexpr int kTmem = 2 * R;
 };
 
@@ -68,11 +72,14 @@ __global__ void __launch_bounds__(kTallThreads) k_contract_tall(const __grid_con
   uint8_t* smem = align1024(smem_raw);
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], dfull[2], dempty[2];
   __shared__ uint32_t tmem_slot;
-  __shared__ float smax[2][kTallThreads / 32], cmax[2][8];
   const RowsArgs& g = args.g;
   const RowsPass& a = g.pass[blockIdx.y];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, stages = args.stages;
   const int cluster = g.cluster, rankc = blockIdx.x % cluster, tile_no = blockIdx.x / cluster;
+  uint32_t* rowmax = reinterpret_cast<uint32_t*>(smem + stages * S::kStageBytes);
+  uint32_t *rankmax = rowmax + kWideRows, *allmax = rankmax + R;
+  float* units = reinterpret_cast<float*>(allmax + 4 * R);
+  for (int i = threadIdx.x; i < kWideRows + R; i += kTallThreads) rowmax[i] = 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -216,64 +223,57 @@ __global__ void __launch_bounds__(kTallThreads) k_contract_tall(const __grid_con
     tmem_dealloc(tmem, S::kTmem);
   }
   // the cluster's sum of this CTA's share of the rows, CTAs in order: scale * T, zero past
-  // the slot's rank and the tile's rows
+  // the slot's rank and the tile's rows. A share lies in one 64-row tile, whose CTAs are half of
+  // the cluster. A thread takes the same four ranks of every `step`-th row.
   const uint32_t pbase = smem_u32(part);
-  const int share = kTallRows / cluster, row_lo = rankc * share, quads = r16 / 4;
-  constexpr int kMine = (kTallRows / 2 * R / 4 + kTallThreads - 1) / kTallThreads;  // quads of a thread, cluster >= 2
+  const int share = kTallRows / cluster, row_lo = rankc * share, quads = r16 / 4, step = kTallThreads / quads;
+  const int half = row_lo / kWideRows, near = cluster / 2, j = 4 * (threadIdx.x % quads), at_row = threadIdx.x / quads;
+  const bool there = half == 0 || count > kWideRows;  // the 64-row tile exists
+  constexpr int kLeast = kTallThreads / (R / 4), kMine = (kWideRows + kLeast - 1) / kLeast;  // rows of a thread, cluster >= 2
   float4 mine[kMine];
-  float m[2] = {0.f, 0.f};
+  uint4 most = make_uint4(0, 0, 0, 0);
 #pragma unroll
   for (int q = 0; q < kMine; ++q) {
-    const int i = threadIdx.x + q * kTallThreads, row = row_lo + i / quads, j = 4 * (i % quads);
+    const int in = at_row + q * step, row = row_lo + in;
     mine[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (i >= share * quads || row >= count) continue;
-    const uint32_t at = pbase + 4 * (row * S::kPitch + j);
-    const float4 x = sum_peers(at, cluster);
-    const float v[4] = {j < r ? x.x * scale : 0.f, j + 1 < r ? x.y * scale : 0.f, j + 2 < r ? x.z * scale : 0.f,
-                        j + 3 < r ? x.w * scale : 0.f};
-    mine[q] = make_float4(v[0], v[1], v[2], v[3]);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (fabsf(v[e]) <= 3.0e38f) {  // an infinity or NaN does not decide the others' digits
-        if (row < kWideRows) m[0] = fmaxf(m[0], fabsf(v[e]));
-        else m[1] = fmaxf(m[1], fabsf(v[e]));
-      }
+    if (at_row >= step || in >= share || row >= count) continue;
+    const float4 x = sum_peers(pbase + 4 * (row * S::kPitch + j), cluster);
+    mine[q] = make_float4(j < r ? x.x * scale : 0.f, j + 1 < r ? x.y * scale : 0.f, j + 2 < r ? x.z * scale : 0.f,
+                          j + 3 < r ? x.w * scale : 0.f);
+    const uint4 bits = finite_bits(mine[q]);
+    if (a.parts) atomicMax(rowmax + in, largest(bits));
+    most = larger(most, bits);
   }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    m[h] = warp_max_bits(m[h]);
-    if (lane == 0) smax[h][warp] = m[h];
-  }
+  if (a.gparts && at_row < step) atomic_larger(rankmax + j, most);
   __syncthreads();
-  if ((int)threadIdx.x < cluster) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float x = smax[h][0];
-#pragma unroll
-      for (int w = 1; w < kTallThreads / 32; ++w) x = fmaxf(x, smax[h][w]);
-      st_peer_f32(peer_smem(smem_u32(&cmax[h][rankc]), threadIdx.x), x);
-    }
-  }
+  if (a.gparts)
+    for (int i = threadIdx.x; i < r16 * near; i += kTallThreads)
+      st_peer_u32(peer_smem(smem_u32(allmax + (rankc - half * near) * R + i % r16), half * near + i / r16), rankmax[i % r16]);
   cluster_arrive();
-  cluster_wait();
-  float unit[2];
+  auto write = [&](__half* parts, int q, const float4& u) {
+    const int in = at_row + q * step;
+    if (there && at_row < step && in < share)
+      write_parts(parts + ((size_t)tile.w * kWideRows + row_lo + in) * (2 * g.pp) + j, g.pp, mine[q], u);
+  };
+  if (a.parts) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float x = 0.f;
-    for (int c = 0; c < cluster; ++c) x = fmaxf(x, cmax[h][c]);
-    unit[h] = split_unit(x);
+    for (int q = 0; q < kMine; ++q) {
+      const float u = split_unit(__uint_as_float(rowmax[min(at_row + q * step, share - 1)]));
+      write(a.parts, q, make_float4(u, u, u, u));
+    }
+    if (there && (int)threadIdx.x < share)
+      a.unit[(size_t)tile.w * kWideRows + row_lo + threadIdx.x] = 1.f / split_unit(__uint_as_float(rowmax[threadIdx.x]));
   }
-  const bool two = count > kWideRows;
-  if (rankc == 0 && (int)threadIdx.x < (two ? 2 : 1)) a.unit[tile.w + threadIdx.x] = 1.f / unit[threadIdx.x];
+  cluster_wait();
+  if (a.gparts) {
+    if ((int)threadIdx.x < r16) {
+      units[threadIdx.x] = rank_unit(allmax + threadIdx.x, R, near);
+      if (there && rankc == half * near) a.gunit[(size_t)(tile.w + half) * g.pp + threadIdx.x] = 1.f / units[threadIdx.x];
+    }
+    __syncthreads();
+    const float4 u = *reinterpret_cast<const float4*>(units + j);
 #pragma unroll
-  for (int q = 0; q < kMine; ++q) {
-    const int i = threadIdx.x + q * kTallThreads, row = row_lo + i / quads, j = 4 * (i % quads);
-    if (i >= share * quads || (row >= kWideRows && !two)) continue;
-    const float u = row < kWideRows ? unit[0] : unit[1];
-    const Split s0 = split_half(mine[q].x * u), s1 = split_half(mine[q].y * u), s2 = split_half(mine[q].z * u), s3 = split_half(mine[q].w * u);
-    __half* at = a.parts + ((size_t)tile.w * kWideRows + row) * (2 * g.pp) + j;
-    *reinterpret_cast<uint2*>(at) = make_uint2(half2_bits(s0.hi, s1.hi), half2_bits(s2.hi, s3.hi));
-    *reinterpret_cast<uint2*>(at + g.pp) = make_uint2(half2_bits(s0.lo, s1.lo), half2_bits(s2.lo, s3.lo));
+    for (int q = 0; q < kMine; ++q) write(a.gparts, q, u);
   }
 }
 
@@ -296,6 +296,7 @@ struct TallExpand {
   static constexpr int kTChunks = R <= 32 ? 1 : R / 32, kTBytes = kTChunks * kTallRows * 128;
   static constexpr int kBaseBytes = kTallRows * 128, kStageBytes = kBaseBytes + R * 128;
   static constexpr int kPart = 0, kOutBytes = 8 * 2048;  // a warp's 32 rows of 32 columns on their way out
+  static constexpr int kFixed = kTBytes + kOutBytes;
   static constexpr int kTmem = 2 * kCols;
 };
 
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kExpandThreads) k_expand_tall(const __grid_con
     grid_dependency_wait();  // the units are the contraction's
     const int q = warp & 3, h = (warp - 2) >> 2, tr = 32 * q + lane;
     const uint32_t mine = smem_u32(smem + S::kTBytes) + (warp - 2) * 2048;
-    const float back = __ldcg(a.unit + tile.w + (tr >= kWideRows && count > kWideRows ? 1 : 0));
+    const float back = tr < count ? __ldcg(a.unit + (size_t)tile.w * kWideRows + tr) : 0.f;
     RingPos at;
     for (int i = 0; i < nb; ++i, at.next(stages)) {
       const uint32_t st = smem_u32(ring + at.slot * S::kStageBytes);
@@ -467,10 +468,10 @@ __global__ void __launch_bounds__(kExpandThreads) k_expand_tall(const __grid_con
 }
 
 // ---- weight gradients ------------------------------------------------------------------------
-// G_s[j][i] (+)= sum over the slot's 64-row tiles of unit * (T parts)^T In, as G^T: 128
+// G_s[j][i] (+)= sum over the slot's 64-row tiles of unit_j * (T parts)^T In, as G^T: 128
 // columns of In are the MMA's rows (A, gathered, MN-major), the ranks its columns (B, T's
 // parts, MN-major), 64 rows its reduction. Each tile gets an accumulator of its own in
-// tensor memory (two in turn), which the epilogue warps add, times the tile's unit, to
+// tensor memory (two in turn), which the epilogue warps add, times the ranks' units, to
 // fp32 sums in registers (thread = column): a long sum is rounded to nearest once a tile.
 // A cluster splits the tiles and sums through distributed shared memory in rank order.
 struct TallGradArgs {
@@ -486,7 +487,7 @@ struct TallGrad {
   static constexpr int kTChunks = R <= 32 ? 1 : R / 32, kTBytes = kTChunks * kWideRows * 128;
   static constexpr int kLow = R <= 32 ? 2 * R : kTBytes / 2;  // bytes from the high part to the low
   static constexpr int kStageBytes = kInBytes + kTBytes;
-  static constexpr int kPart = R * kGradCols * 4;  // the partial sums lie over the drained ring
+  static constexpr int kPart = R * kGradCols * 4, kFixed = 0;  // the partial sums lie over the drained ring
   // up to rank 32 both parts are one operand of 2 R columns, so that In is read once
   static constexpr bool kBoth = R <= 32;
   static constexpr int kD = kBoth ? 2 * R : R;  // columns of an accumulator
@@ -500,6 +501,7 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
   uint8_t* smem = align1024(smem_raw);
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], dfull[2], dempty[2];
   __shared__ uint32_t tmem_slot;
+  __shared__ __align__(16) float units[4][2][R];  // each epilogue warp's own, of two tiles in turn
   const GradArgs& g = args.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, stages = args.stages;
   const int split = blockIdx.z, nsplit = gridDim.z, slot = grad_slot(g);
@@ -627,10 +629,23 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
     float sum[R];
 #pragma unroll
     for (int j = 0; j < R; ++j) sum[j] = 0.f;
-    float next = nt > 0 ? __ldcg(a.unit + tile0 + t_lo) : 0.f;
+    // the ranks' units, loaded a tile ahead
+    constexpr int kUnits = (R + 31) / 32;
+    const float* unit_at = a.unit + (size_t)(tile0 + t_lo) * g.pp + lane;
+    float next[kUnits];
+    auto fetch = [&](int s) {
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) next[u] = s < nt && lane + 32 * u < r16 ? __ldcg(unit_at + (size_t)s * g.pp + 32 * u) : 0.f;
+    };
+    fetch(0);
     for (int s = 0; s < nt; ++s) {
-      const float unit = next;
-      if (s + 1 < nt) next = __ldcg(a.unit + tile0 + t_lo + s + 1);
+      float* own = units[warp - 2][s & 1];  // read two tiles ago
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u)
+        if (lane + 32 * u < r16) own[lane + 32 * u] = next[u];
+      __syncwarp();
+      fetch(s + 1);
+      const float4* unit = reinterpret_cast<const float4*>(own);
       if (!mbar_wait_bounded(&dfull[s & 1], (s / 2) & 1)) break;
       tc_fence_after();
 #pragma unroll
@@ -643,10 +658,14 @@ __global__ void __launch_bounds__(kTallThreads) k_grad_tall(const __grid_constan
           uint32_t w[16];
           tmem_ld16(at + R, w);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) sum[16 * t + e] = fmaf(__uint_as_float(v[e]) + __uint_as_float(w[e]), unit, sum[16 * t + e]);
-        } else {
+          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(w[e]));
+        }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) sum[16 * t + e] = fmaf(__uint_as_float(v[e]), unit, sum[16 * t + e]);
+        for (int e = 0; e < 16; e += 4) {
+          const float4 u = unit[4 * t + e / 4];
+          float* y = sum + 16 * t + e;
+          y[0] = fmaf(__uint_as_float(v[e]), u.x, y[0]), y[1] = fmaf(__uint_as_float(v[e + 1]), u.y, y[1]);
+          y[2] = fmaf(__uint_as_float(v[e + 2]), u.z, y[2]), y[3] = fmaf(__uint_as_float(v[e + 3]), u.w, y[3]);
         }
       }
       tc_fence_before();
@@ -787,11 +806,12 @@ cudaError_t encode_adapter_maps(dictproj_adapters* a) {
       (e = encode_tiled_2d(&a->b_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a->B, (uint64_t)a->ld_b, ranks, (uint64_t)a->ld_b * 2,
                            kCols, 16, CU_TENSOR_MAP_SWIZZLE_128B)))
     return e;
-  for (int i = 0; i < 2; ++i)
-    if ((e = encode_tiled_2d(&a->part_map[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a->parts[i], (uint64_t)2 * a->pp, rows,
-                             (uint64_t)4 * a->pp, 64, kWideRows, CU_TENSOR_MAP_SWIZZLE_128B)))
-      return e;
-  return cudaSuccess;
+  auto parts = [&](CUtensorMap* map, const uint16_t* p) {
+    return encode_tiled_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p, (uint64_t)2 * a->pp, rows, (uint64_t)4 * a->pp, 64, kWideRows,
+                           CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if ((e = parts(&a->part_map, a->parts)) || (e = parts(&a->gpart_map[0], a->gparts[0]))) return e;
+  return parts(&a->gpart_map[1], a->gparts[1]);
 }
 
 // Rows that TMA can read, and enough of them to fill 128-row tiles: up to rank 32 the
@@ -805,9 +825,9 @@ bool tall_serves(const dictproj_adapters* a, const dictproj_rows* r) {
 
 struct TallKernel {
   const void* fn;
-  int stage_bytes, part_bytes;
+  int stage_bytes, part_bytes, fixed_bytes;
 };
-#define DICTPROJ_TALL_R(kernel, shape, R) TallKernel{(const void*)kernel<R>, shape<R>::kStageBytes, shape<R>::kPart}
+#define DICTPROJ_TALL_R(kernel, shape, R) TallKernel{(const void*)kernel<R>, shape<R>::kStageBytes, shape<R>::kPart, shape<R>::kFixed}
 #define DICTPROJ_TALL(rp, kernel, shape)                  \
   ((rp) <= 16   ? DICTPROJ_TALL_R(kernel, shape, 16)      \
    : (rp) <= 32 ? DICTPROJ_TALL_R(kernel, shape, 32)      \
@@ -831,7 +851,7 @@ cudaError_t launch_contract_tall(RowsArgs& g, int passes, bool exact_sums, const
   while (args.g.cluster < 8 && full * args.g.cluster < 3 * a->n_sm / 2) args.g.cluster *= 2;
   const TallKernel k = DICTPROJ_TALL(g.rp, k_contract_tall, TallContract);
   const int kc = (std::max(g.pass[0].K, g.pass[passes - 1].K) + kCols - 1) / kCols;
-  const Ring ring = plan_ring(k.stage_bytes, k.part_bytes, 0, (kc + args.g.cluster - 1) / args.g.cluster,
+  const Ring ring = plan_ring(k.stage_bytes, k.part_bytes, k.fixed_bytes, (kc + args.g.cluster - 1) / args.g.cluster,
                               sm_share((long)full * args.g.cluster, a->n_sm));
   args.stages = ring.stages;
   args.flush = exact_sums ? 2 : 1 << 20;
@@ -847,17 +867,17 @@ cudaError_t launch_expand_tall(const RowsArgs& g, const dictproj_adapters* a, co
   cudaError_t e = encode_rows(&args.in, &args.box, p.base ? p.base : p.out, p.N, r->M);
   if (e != cudaSuccess) return e;
   args.q = reinterpret_cast<const uint16_t*>(p.Q) == a->A ? a->a_map : a->b_map;
-  args.parts = a->part_map[0];
+  args.parts = a->part_map;
   args.g = g;
   args.g.tiles = r->tiles[2];
   args.g.n_tiles = r->n_tiles + 4;
   args.g.runs = r->runs[1];
   const TallKernel k = DICTPROJ_TALL(g.rp, k_expand_tall, TallExpand);
-  const int fixed = (g.rp <= 32 ? 1 : a->pp / 32) * kTallRows * 128 + 8 * 2048, blocks = (p.N + kCols - 1) / kCols;
+  const int blocks = (p.N + kCols - 1) / kCols;
   const int share = g.rp <= 64 ? 2 : 1, full = std::max(1, r->M / kTallRows);  // tiles that do exist, about
   const int ragged = std::min(a->n_slots, full) / 2;  // and those that end a slot's rows
   const int parts = std::min(blocks, std::max(1, share * a->n_sm / (full + ragged)));  // as many CTAs as run at once
-  const Ring ring = plan_ring(k.stage_bytes, 0, fixed, (blocks + parts - 1) / parts, share);
+  const Ring ring = plan_ring(k.stage_bytes, 0, k.fixed_bytes, (blocks + parts - 1) / parts, share);
   args.stages = ring.stages;
   void* pp[] = {(void*)&args};
   return launch_pdl_cluster(k.fn, dim3(parts, adapter_tiles(r->M, r->n_slots, kTallRows)), ring.smem, stream, pp, dim3(1, 1, 1),
@@ -882,7 +902,7 @@ cudaError_t launch_grad_tall(const GradArgs& w, const dictproj_adapters* a, cons
   cudaError_t e;
   for (int i = 0; i < 2; ++i) {
     if ((e = encode_rows(&args.in[i], &args.box[i], w.pass[i].in, w.pass[i].K, r->M)) != cudaSuccess) return e;
-    args.parts[i] = a->part_map[i];
+    args.parts[i] = a->gpart_map[i];
   }
   args.g = w;
   const int blocks = w.pass[0].blocks + w.pass[1].blocks;

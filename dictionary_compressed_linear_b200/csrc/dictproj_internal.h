@@ -119,13 +119,16 @@ struct dictproj_adapters {
   uint16_t* B;             // fp16 [n_slots][rp][ld_b]
   int* rank;               // [n_slots], 0 = empty
   float* scale;            // [n_slots]
-  // batches of many rows: scale * T (forward), or scale * U (index 0) and scale * T (1) of
-  // the backward pass, as two fp16 parts times a power of two per 64-row tile (adapter.cuh)
+  // batches of many rows: scale * T of the forward, scale * U of the backward pass for the
+  // expansion (parts), scale * U (index 0) and scale * T (1) for the weight gradients (gparts),
+  // as two fp16 parts times powers of two (adapter.cuh); of few rows, gparts hold them in fp32
   int pp;                  // ranks of a part's row: rp rounded up to 16, 32, 64 or 128
-  uint16_t* parts[2];      // [pass] fp16 [adapter_tiles(64)][64][high pp | low pp]
-  float* unit[2];          // [pass] what a tile's parts are multiplied with, [adapter_tiles(64)]
-  CUtensorMap a_map, b_map;      // A and B as [n_slots * rp] rows, box 64 columns x 16 rows
-  CUtensorMap part_map[2];       // the parts, box 64 columns x 64 rows
+  uint16_t* parts;         // fp16 [adapter_tiles(64)][64][high pp | low pp]
+  uint16_t* gparts[2];
+  float* unit;             // what a row's parts are multiplied with, [adapter_tiles(64)][64]
+  float* gunit[2];         // what a rank's are, [adapter_tiles(64)][pp]
+  CUtensorMap a_map, b_map;            // A and B as [n_slots * rp] rows, box 64 columns x 16 rows
+  CUtensorMap part_map, gpart_map[2];  // the parts, box 64 columns x 64 rows
 };
 
 // Most tiles of `rows` rows that M rows over n_slots slots (and no slot) can form.

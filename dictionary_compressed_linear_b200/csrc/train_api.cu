@@ -137,8 +137,9 @@ int dictproj_adapters_create(int d_in, int d_out, int max_rank, int n_slots, int
   const size_t t64 = (size_t)adapter_tiles(max_tokens, n_slots, 64), pb = t64 * 64 * a->pp * 4, ub = t64 * sizeof(float);
   if ((e = dmalloc((void**)&a->A, ab)) || (e = dmalloc((void**)&a->B, bb)) ||
       (e = dmalloc((void**)&a->rank, (size_t)n_slots * 4)) || (e = dmalloc((void**)&a->scale, (size_t)n_slots * 4)) ||
-      (e = dmalloc((void**)&a->parts[0], pb)) || (e = dmalloc((void**)&a->parts[1], pb)) ||
-      (e = dmalloc((void**)&a->unit[0], ub)) || (e = dmalloc((void**)&a->unit[1], ub))) {
+      (e = dmalloc((void**)&a->parts, pb)) || (e = dmalloc((void**)&a->unit, ub * 64)) ||
+      (e = dmalloc((void**)&a->gparts[0], pb)) || (e = dmalloc((void**)&a->gparts[1], pb)) ||
+      (e = dmalloc((void**)&a->gunit[0], ub * a->pp)) || (e = dmalloc((void**)&a->gunit[1], ub * a->pp))) {
     dictproj_free_adapters(a);
     cudaGetLastError();
     return fail(DICTPROJ_ERR_OOM, "adapters_create: device allocation failed (%s)", cudaGetErrorName(e));
@@ -164,9 +165,11 @@ void dictproj_free_adapters(dictproj_adapters* a) {
   cudaFree(a->B);
   cudaFree(a->rank);
   cudaFree(a->scale);
+  cudaFree(a->parts);
+  cudaFree(a->unit);
   for (int i = 0; i < 2; ++i) {
-    cudaFree(a->parts[i]);
-    cudaFree(a->unit[i]);
+    cudaFree(a->gparts[i]);
+    cudaFree(a->gunit[i]);
   }
   delete a;
 }

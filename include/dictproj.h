@@ -465,8 +465,9 @@ int dictproj_rows_set(dictproj_rows* rows, const int* ids, int M, void* stream);
  * dictproj_rows_set: X device fp16 [M][d_in], base and Y device fp16 [M][d_out].
  * base may be Y itself (the result of a dictproj_forward*: rows without an adapter
  * are then not touched at all) or NULL (base = 0); rows without an adapter get
- * base. T is summed in fp32 and used in fp32 or in two fp16 parts (22 bits or
- * more); Y is rounded once. Rows do not reach other rows: an infinity or NaN
+ * base. T is summed in fp32 and used in fp32 or, in batches of many rows, in two fp16
+ * parts, off by at most 2^-22 of itself or 2^-38 of the largest finite T of its row; Y is
+ * rounded once. Rows do not reach other rows: an infinity or NaN
  * stays in its own. Asynchronous on `stream`; up to three launches.
  * Errors: NULL, RANGE (no rows planned, more than the pool's max_tokens, the plan
  * made for another n_slots, Y overlapping X, or overlapping base without being
@@ -496,7 +497,9 @@ int dictproj_forward_adapters(const void* X, const dictproj_layer* layer, const 
  * rows in the batch and past a slot's rank. accumulate != 0 adds. dX may be NULL
  * (no input gradient) and dA and dB may both be NULL (only dX); not all three. The
  * sums run in fp32 in a fixed order: repeated calls give the same bits. A slot's
- * gradients are its own rows' alone. At most four launches.
+ * gradients are its own rows' alone, a rank's its own T's: in batches of many rows T is
+ * off by at most 2^-22 of itself or 2^-38 of the largest finite T of the same rank
+ * among 64 rows of the slot (in dX, of its row, as in the forward). At most four launches.
  * Asynchronous on `stream`. Errors as dictproj_adapter_forward (dX must not overlap
  * X or dY, dA and dB must not overlap anything), NULL also when only one of dA, dB
  * is given. */

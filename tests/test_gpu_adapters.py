@@ -283,6 +283,55 @@ def test_small_and_large_activations_keep_their_digits(size):
     ref.assert_float(dB, w["dB"], w["WB"], 512 + 70)
 
 
+@pytest.mark.parametrize("M,d_out,R", [(16, 96, 16), (300, 77, 16), (300, 1001, 64), (700, 96, 16), (700, 264, 32), (300, 1024, 64), (300, 1024, 128)])
+def test_ranks_of_different_size_keep_their_digits(M, d_out, R):
+    # 2^26 between the first rank's weights and the last one's: every rank's gradients are as exact as they would
+    # be alone. Bound as for the long sums, and T in two parts, 2^-22 of it.
+    pool = ref.Pool(512, d_out, R, [R], seed=4)
+    size = 2.0 ** (10 - 26 * torch.arange(R, device="cuda") / (R - 1))[:, None]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    pool.A, pool.B = ([(torch.randn(R, n, generator=g, device="cuda") * size).half()] for n in (512, d_out))
+    ids = torch.zeros(M, dtype=torch.int32, device="cuda")
+    X, dY = normal(M, 512), normal(M, d_out, seed=3, scale=0.05)
+    h, rows = pool.upload(dp, M, stream()), planned(ids, 1)
+    dA, dB = torch.empty(1, R, 512, device="cuda"), torch.empty(1, R, d_out, device="cuda")
+    dp.dictproj_adapter_backward(h, rows, X.data_ptr(), dY.data_ptr(), 0, 0, dA.data_ptr(), dB.data_ptr(), False, stream())
+    torch.cuda.synchronize()
+    w = ref.backward(pool, ids, X, dY)
+    limit = 8 * 2.0 ** -23 + 2.0 ** -24 * 150 ** 0.5 + 2.0 ** -22
+    for got, want in ((dA, w["dA"]), (dB, w["dB"])):
+        off = (got.double() - want).norm(dim=2) / want.norm(dim=2)
+        assert off.max().item() <= limit, (off.argmax().item(), off.max().item())
+
+
+@pytest.mark.parametrize("M,d_out,R", [(40, 96, 16), (300, 77, 16), (300, 1001, 64), (600, 96, 16), (700, 264, 32), (300, 1024, 128)])
+def test_rows_of_different_size_keep_their_digits(M, d_out, R):
+    # rows of 2^13 and of 2^-17 in turn: the small ones' results are rounded once, as if they were alone
+    ids = torch.zeros(M, dtype=torch.int32, device="cuda")
+    size = torch.where(torch.arange(M, device="cuda") % 2 == 0, 2.0 ** -17, 2.0 ** 13)[:, None]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    X, dY = ((torch.randn(M, n, generator=g, device="cuda") * size).half() for n in (512, d_out))
+    rows = planned(ids, 1)
+    pool = ref.Pool(512, d_out, R, [R], seed=4)
+    pool.B = [(torch.randn(R, d_out, generator=g, device="cuda") * 2.0 ** 8).half()]
+    Y = torch.full_like(dY, NAN)
+    dp.dictproj_adapter_forward(pool.upload(dp, M, stream()), rows, X.data_ptr(), 0, Y.data_ptr(), stream())
+    torch.cuda.synchronize()
+    want, W = ref.forward(pool, ids, X)
+    ref.assert_half(Y[::2], want[::2], W[::2], 512 + R, "Y")
+    pool = ref.Pool(512, d_out, R, [R], seed=4)
+    pool.A = [(torch.randn(R, 512, generator=g, device="cuda") * 2.0 ** 8).half()]
+    h = pool.upload(dp, M, stream())
+    for grads in (False, True):
+        dX = torch.full_like(X, NAN)
+        dA, dB = torch.empty(1, R, 512, device="cuda"), torch.empty(1, R, d_out, device="cuda")
+        dp.dictproj_adapter_backward(h, rows, X.data_ptr(), dY.data_ptr(), 0, dX.data_ptr(), dA.data_ptr() if grads else 0,
+                                     dB.data_ptr() if grads else 0, False, stream())
+        torch.cuda.synchronize()
+        w = ref.backward(pool, ids, X, dY)
+        ref.assert_half(dX[::2], w["dX"][::2], w["WX"][::2], d_out + R, "dX")
+
+
 def test_a_slot_is_replaced_and_emptied():
     pool, other = ref.Pool(64, 41, 24, [24, 20], seed=1), ref.Pool(64, 41, 24, [3, 24], seed=9)
     ids, X = ids_of("each", 6, 2), normal(6, 64)
