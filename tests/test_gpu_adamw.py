@@ -154,6 +154,25 @@ def test_what_lies_between_the_tensors_is_not_touched():
     assert (arena["g"] == 5).all()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_neighbours_in_one_arena_and_shared_gradients(bits):
+    # arrays that touch and gradients that several tensors read are accepted, and every tensor gets its own step
+    n, count = 640, 3
+    hosts = [host_tensor(n, bits, 40 + i) for i in range(count)]
+    arena = {k: torch.from_numpy(np.concatenate([t[k] for t in hosts])).cuda() for k in hosts[0]}
+    for t in hosts:
+        t["g"] = hosts[0]["g"]
+    at = lambda k, i: arena[k].data_ptr() + i * hosts[0][k].nbytes  # noqa: E731
+    plan = dp.dictproj_adamw_create([{"n": n, **{k: at(k, 0 if k == "g" else i) for k in arena}} for i in range(count)], bits)
+    dp.dictproj_adamw_step(plan, 3, stream=stream(), **HYPER)
+    torch.cuda.synchronize()
+    want = [ref.adamw(t, 3, bits=bits, **HYPER) for t in hosts]
+    for k in arena:
+        if k != "g":
+            got, exact = arena[k].cpu().numpy(), np.concatenate([w[k] for w in want])
+            assert got.tobytes() == exact.tobytes(), k
+
+
 def test_a_state_in_8_bits_follows_its_32_bit_one():
     # a constant spread of gradients: v tends to g^2. The dithered codes are unbiased, each step adds a
     # rounding of at most 2^-3 of r, forgotten at the rate 1 - beta2; over 4096 elements the mean of

@@ -268,6 +268,47 @@ def test_long_sums_keep_the_accuracy_of_fp32(M, R):
         assert ((got.double() - want).norm() / want.norm()).item() <= limit
 
 
+@pytest.mark.parametrize("M,d_in,d_out,R", [(1300, 4096, 1025, 16), (300, 4096, 1024, 16), (520, 2048, 2047, 64), (16, 4096, 4096, 16), (12, 4096, 1001, 128)])
+def test_long_sums_of_the_other_kernels_keep_the_accuracy_of_fp32(M, d_in, d_out, R):
+    # as above, for rows on mma.sync (any width, or too few rows for tcgen05) and for few rows (fp32 throughout)
+    pool = ref.Pool(d_in, d_out, R, [R], seed=4)
+    ids = torch.zeros(M, dtype=torch.int32, device="cuda")
+    X, dY = normal(M, d_in), normal(M, d_out, seed=3)
+    h, rows = pool.upload(dp, M, stream()), planned(ids, 1)
+    dA, dB = torch.empty(1, R, d_in, device="cuda"), torch.empty(1, R, d_out, device="cuda")
+    dp.dictproj_adapter_backward(h, rows, X.data_ptr(), dY.data_ptr(), 0, 0, dA.data_ptr(), dB.data_ptr(), False, stream())
+    torch.cuda.synchronize()
+    w = ref.backward(pool, ids, X, dY)
+    limit = 8 * 2.0 ** -23 + 2.0 ** -24 * 150 ** 0.5
+    for got, want in ((dA, w["dA"]), (dB, w["dB"])):
+        assert ((got.double() - want).norm() / want.norm()).item() <= limit
+
+
+@pytest.mark.parametrize("M", [12, 600])
+@pytest.mark.parametrize("d_out", [96, 75])
+@pytest.mark.parametrize("mode", ["zero", "apart", "in place"])
+def test_every_row_of_dx_is_written(M, d_out, mode):
+    # rows of foreign slots are full of infinities and NaN, those without an adapter get base, or zeros
+    pool = ref.Pool(128, d_out, 16, [16, 16], seed=2)
+    ids = ids_of("some", M, 2, seed=5)
+    X, dY, base = normal(M, 128), normal(M, d_out, seed=3), normal(M, 128, seed=4)
+    X[ids != 0], dY[ids != 0] = float("inf"), NAN
+    h, rows = pool.upload(dp, M, stream()), planned(ids, 2)
+    for grads in (False, True):
+        dX = base.clone() if mode == "in place" else torch.full_like(base, NAN)
+        dA, dB = torch.empty(2, 16, 128, device="cuda"), torch.empty(2, 16, d_out, device="cuda")
+        dp.dictproj_adapter_backward(h, rows, X.data_ptr(), dY.data_ptr(), {"zero": 0, "apart": base.data_ptr(), "in place": dX.data_ptr()}[mode],
+                                     dX.data_ptr(), dA.data_ptr() if grads else 0, dB.data_ptr() if grads else 0, False, stream())
+        torch.cuda.synchronize()
+        none = ids == -1
+        assert none.any() and torch.equal(dX[none], torch.zeros_like(dX[none]) if mode == "zero" else base[none])
+        mine = ids == 0
+        one = ref.Pool(128, d_out, 16, [16], seed=2)
+        one.A, one.B, one.scale = pool.A[:1], pool.B[:1], pool.scale[:1]
+        w = ref.backward(one, ids[mine], X[mine], dY[mine], None if mode == "zero" else base[mine])
+        ref.assert_half(dX[mine], w["dX"], w["WX"], d_out + 16)
+
+
 @pytest.mark.parametrize("size", [1e-7, 1e4])
 def test_small_and_large_activations_keep_their_digits(size):
     # T is far outside fp16's comfortable range: small gradients must not fall to zero in a sum
