@@ -15,8 +15,8 @@
 // dense dictionary (a product of E2M1 and E4M3 has at most six bits) is exact in it. Two parts
 // hold 16 bits (2^-16 of an element at most beside dX's own 2^-11). One fp16 part made dX's
 // error 2.9e-4 (2.1e-4 now: its own rounding), lost what lay below 2^-24 and gave NaN above
-// 65504; it took 40 us where two take 44 (128 rows, 4096 <- 2048 <- 4096), and 130 where they
-// take 171 (2048 rows, 4096 <- 2048 <- 11008). Up to
+// 65504; it took 40 us where two take 42 (128 rows, 4096 <- 2048 <- 4096), and 130 where they
+// take 161 (2048 rows, 4096 <- 2048 <- 11008). Up to
 // kFineRows rows, where the second product waits for its loads and not for the tensor cores,
 // a third part makes it fp32's 24 bits.
 //
@@ -53,27 +53,40 @@ struct DictCopy {
   __nv_bfloat16* dd;
   long n_blocks;
 };
-__device__ __forceinline__ void densify_block(const DictCopy& d, long b) {
-  const uint2 c = ld_stream_v2(d.codes + 8 * b);
-  const uint32_t sv = dup_lo(e4m3x2_to_f16x2(d.scales[b]));
-  uint32_t v[8];
-  e2m1x8_to_f16x2x4(c.x, *reinterpret_cast<uint32_t(*)[4]>(v));
-  e2m1x8_to_f16x2x4(c.y, *reinterpret_cast<uint32_t(*)[4]>(v + 4));
+// N blocks, `step` apart; those past the end are left out.
+template <int N>
+__device__ __forceinline__ void densify_blocks(const DictCopy& d, long b, long step) {
+  uint2 c[N];
+  uint32_t sc[N];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t h = hmul2_u32(v[i], sv);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    v[i] = bf16x2_bits(f.x, f.y);
+  for (int i = 0; i < N; ++i) {
+    const long at = min(b + i * step, d.n_blocks - 1);
+    c[i] = ld_stream_v2(d.codes + 8 * at);
+    sc[i] = d.scales[at];
   }
-  uint4* dst = reinterpret_cast<uint4*>(d.dd + 16 * b);
-  dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
-  dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (b + i * step >= d.n_blocks) break;
+    const uint32_t sv = dup_lo(e4m3x2_to_f16x2(sc[i]));
+    uint32_t v[8];
+    e2m1x8_to_f16x2x4(c[i].x, *reinterpret_cast<uint32_t(*)[4]>(v));
+    e2m1x8_to_f16x2x4(c[i].y, *reinterpret_cast<uint32_t(*)[4]>(v + 4));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t h = hmul2_u32(v[e], sv);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      v[e] = bf16x2_bits(f.x, f.y);
+    }
+    uint4* dst = reinterpret_cast<uint4*>(d.dd + 16 * (b + i * step));
+    dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 __global__ void __launch_bounds__(256) k_densify_dict(DictCopy d) {
   grid_dependency_wait();  // Dd may still be read by the previous input-gradient GEMM
   trigger_dependents();
   const long b = (long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (b < d.n_blocks) densify_block(d, b);
+  if (b < d.n_blocks) densify_blocks<1>(d, b, 0);
 }
 
 constexpr int kNnM = 128, kNnK = 64, kNnMaxN = 256, kNnStages = 4;
@@ -147,7 +160,8 @@ __global__ void __launch_bounds__(kNnThreads, 1)
     grid_dependency_wait();
     trigger_dependents();
     const long step = (long)(gridDim.x - tiles) * kNnThreads;
-    for (long b = (long)(blockIdx.x - tiles) * kNnThreads + threadIdx.x; b < copy.n_blocks; b += step) densify_block(copy, b);
+    // four blocks at a time, their loads together
+    for (long b = (long)(blockIdx.x - tiles) * kNnThreads + threadIdx.x; b < copy.n_blocks; b += 4 * step) densify_blocks<4>(copy, b, step);
     return;
   }
   const int n0 = blockIdx.x % nx * bn, m0 = blockIdx.x / nx * kNnM, split = blockIdx.z, nsplit = gridDim.z;
@@ -176,14 +190,21 @@ __global__ void __launch_bounds__(kNnThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       RingPos at;
-      for (int s = 0; s < nk; ++s, at.next(kNnStages)) {
+      // A's part and column of a stage, advanced without a division (one took 10 us of 82, a
+      // stage waiting for its coordinates)
+      int part = FIRST ? 0 : s_lo / nk_one, kx = (s_lo - part * nk_one) * kNnK;
+      const CUtensorMap* tm_a = FIRST || part == 0 ? &maps.a[0] : part == 1 ? &maps.a[1] : &maps.a[2];
+      for (int s = 0; s < nk; ++s, at.next(kNnStages), kx += kNnK) {
+        if (!FIRST && kx >= K) {
+          tm_a = ++part == 1 ? &maps.a[1] : &maps.a[2];
+          kx = 0;
+        }
         if (s >= kNnStages && !mbar_wait_bounded(&empty[at.slot], at.phase ^ 1)) {
           drain(full, kNnStages, s);
           break;
         }
         mbar_arrive_expect_tx(&full[at.slot], kNnABytes + bn * kNnK * 2);
-        const int part = (s_lo + s) / nk_one, kx = (s_lo + s - part * nk_one) * kNnK;
-        tma_load_2d(smem_u32(smem + at.slot * kNnABytes), &maps.a[part], kx, m0, &full[at.slot]);
+        tma_load_2d(smem_u32(smem + at.slot * kNnABytes), tm_a, kx, m0, &full[at.slot]);
         for (int c = 0; c < bn / 64; ++c)
           tma_load_2d(smem_u32(sb + at.slot * kNnBBytes + c * kMnChunk), &maps.b, n0 + 64 * c, kx, &full[at.slot]);
       }
