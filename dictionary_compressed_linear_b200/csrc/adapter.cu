@@ -421,8 +421,8 @@ __global__ void __launch_bounds__(kRowThreads, R <= 32 ? 4 : 2) k_adapter_few(co
 // Two launches, so that each has a grid of its own: tiles x K-splits for the contraction,
 // tiles x column blocks for the expansion (one launch for both, a cluster a tile, left
 // each CTA a chain of eight loads and two cluster barriers, and at 2048 rows of rank 32
-// took 27 us). T passes through the pool's workspace in its two fp16 parts; the weight
-// gradients read the same parts.
+// took 27 us). T passes through the pool's workspace in two fp16 parts, with a
+// unit per row for the expansion and once more with one per rank for the weight gradients.
 //
 // Contraction: a cluster splits the K columns of one tile of up to kWideRows rows; every
 // CTA streams its share in 64-column stages (cp.async) through mma.sync, the partial sums

@@ -441,7 +441,8 @@ int dictproj_adapters_set(dictproj_adapters* a, int slot, int rank, float scale,
 /* Where a slot's weights lie on the device, for an optimiser that writes them in
  * place: *A fp16 [rank][d_in] and *B fp16 [rank][*ld_B], row stride *ld_B >= d_out
  * elements (equal to d_out when d_out % 8 == 0; the columns past d_out must stay
- * zero). Any output may be NULL. Errors: NULL, RANGE (slot). */
+ * zero, so that an optimiser whose copies are contiguous takes one tensor a row of B
+ * otherwise). Any output may be NULL. Errors: NULL, RANGE (slot). */
 int dictproj_adapters_slot(const dictproj_adapters* a, int slot, void** A, void** B, int* ld_B);
 
 /* A plan for batches of up to max_rows rows over a pool's n_slots slots (the
@@ -468,7 +469,7 @@ int dictproj_rows_set(dictproj_rows* rows, const int* ids, int M, void* stream);
  * base. T is summed in fp32 and used in fp32 or, in batches of many rows, in two fp16
  * parts, off by at most 2^-22 of itself or 2^-38 of the largest finite T of its row; Y is
  * rounded once. Rows do not reach other rows: an infinity or NaN
- * stays in its own. Asynchronous on `stream`; up to three launches.
+ * stays in its own (where an infinity is the result, it may come out as NaN). Asynchronous on `stream`; up to three launches.
  * Errors: NULL, RANGE (no rows planned, more than the pool's max_tokens, the plan
  * made for another n_slots, Y overlapping X, or overlapping base without being
  * base), ALIGN (16 bytes), MISMATCH (device), CUDA. */

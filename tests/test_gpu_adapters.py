@@ -373,6 +373,31 @@ def test_rows_of_different_size_keep_their_digits(M, d_out, R):
         ref.assert_half(dX[::2], w["dX"][::2], w["WX"][::2], d_out + R, "dX")
 
 
+@pytest.mark.parametrize("M", [256, 511, 2048, 4096])
+@pytest.mark.parametrize("slots,used,R", [(64, 1, 16), (64, 4, 16), (64, 2, 64), (9, 1, 32), (1024, 3, 16)])
+def test_large_pools_of_which_a_batch_uses_few(M, slots, used, R):
+    # the kernels are chosen by the pool's slots; the others' gradients are zeros
+    at = np.linspace(0, slots - 1, used).astype(int)  # the first slot and the last among them
+    ranks = [0] * slots
+    for i, s in enumerate(at):
+        ranks[s] = R - i
+    pool = ref.Pool(160, 96, R, ranks, seed=M)
+    ids = torch.tensor(np.repeat(at, -(-M // used))[:M], dtype=torch.int32, device="cuda")
+    X, dY, base = normal(M, 160), normal(M, 96, seed=3, scale=0.05), normal(M, 96, seed=4)
+    h, rows = pool.upload(dp, M, stream()), planned(ids, slots)
+    Y, dX = torch.full_like(base, NAN), torch.full_like(X, NAN)
+    dA, dB = torch.full((slots, R, 160), NAN, device="cuda"), torch.full((slots, R, 96), NAN, device="cuda")
+    dp.dictproj_adapter_forward(h, rows, X.data_ptr(), base.data_ptr(), Y.data_ptr(), stream())
+    dp.dictproj_adapter_backward(h, rows, X.data_ptr(), dY.data_ptr(), 0, dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), False, stream())
+    torch.cuda.synchronize()
+    want, W = ref.forward(pool, ids, X, base)
+    ref.assert_half(Y, want, W, 160 + R)
+    w = ref.backward(pool, ids, X, dY)
+    ref.assert_half(dX, w["dX"], w["WX"], 96 + R)
+    ref.assert_float(dA, w["dA"], w["WA"], 96 + M)
+    ref.assert_float(dB, w["dB"], w["WB"], 160 + M)
+
+
 def test_a_slot_is_replaced_and_emptied():
     pool, other = ref.Pool(64, 41, 24, [24, 20], seed=1), ref.Pool(64, 41, 24, [3, 24], seed=9)
     ids, X = ids_of("each", 6, 2), normal(6, 64)
