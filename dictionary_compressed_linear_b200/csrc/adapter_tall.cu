@@ -775,9 +775,8 @@ Ring plan_ring(int stage_bytes, int part_bytes, int fixed_bytes, int work, int s
   return r;
 }
 // CTAs of an SM: two (clusters of eight with one an SM leave SMs idle: 16 of them fit a
-// GPU of 148), or three where there are more than that anyway
-// (384 CTAs of the gradients, 8192 rows of rank 64: the whole pass 101.8 us with two, 106.4
-// with three).
+// GPU of 148), or three where there are more than that anyway (384 CTAs of the gradients: a
+// whole pass took 101.8 us with two, 106.4 with three).
 int sm_share(long ctas, int n_sm) { return ctas > 3l * n_sm ? 3 : 2; }
 
 template <int R>
@@ -910,7 +909,10 @@ cudaError_t launch_grad_tall(const GradArgs& w, const dictproj_adapters* a, cons
   const int split = grad_split(blocks * slots, r->M / (kWideRows * slots), a->n_sm * (w.rp <= 32 ? 3 : w.rp <= 64 ? 2 : 1));
   const TallKernel k = DICTPROJ_TALL(w.rp, k_grad_tall, TallGrad);
   const int tiles = (r->M / (kWideRows * slots) + split) / split;
-  const Ring ring = plan_ring(k.stage_bytes, k.part_bytes, 0, tiles, sm_share((long)blocks * slots * split, a->n_sm));
+  // above rank 32 the sums' registers let two CTAs run on an SM (8192 rows, 4096 and 11008 wide,
+  // rank 64: the whole pass 158 us with rings for two, 166 with rings for three)
+  const int share = w.rp > 32 ? 2 : sm_share((long)blocks * slots * split, a->n_sm);
+  const Ring ring = plan_ring(k.stage_bytes, k.part_bytes, 0, tiles, share);
   args.stages = ring.stages;
   void* p[] = {(void*)&args};
   return launch_pdl_cluster(k.fn, dim3(blocks, slots, split), ring.smem, stream, p, dim3(1, 1, split));
