@@ -824,6 +824,15 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
   grid_dependency_wait();  // T is the call's own; the rest was there before the call
   trigger_dependents();    // the expansion's first loads may go out
   for (int i = 0; i < S::kStages - 1; ++i) issue_t(i);
+  float ahead[R / 16][2];  // the units of this thread's ranks, a tile ahead
+  auto fetch_units = [&](int i) {
+#pragma unroll
+    for (int t = 0; t < R / 16; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        ahead[t][h] = i < nt && 16 * t < r16 ? __ldcg(a.unit + (size_t)(tile0 + t_lo + i) * g.pp + 16 * t + 8 * h + (lane >> 2)) : 0.f;
+  };
+  fetch_units(0);
   float sum[R / 16][2][4];
 #pragma unroll
   for (int t = 0; t < R / 16; ++t)
@@ -835,7 +844,10 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
     issue_in(i + S::kStages - 1);
     issue_t(i + S::kStages - 1);
     const uint32_t st = ring + (uint32_t)(i % S::kStages) * S::kStageBytes;
-    const float* unit = a.unit + (size_t)(tile0 + t_lo + i) * g.pp + (lane >> 2);
+    float back[R / 16][2];
+#pragma unroll
+    for (int t = 0; t < R / 16; ++t) back[t][0] = ahead[t][0], back[t][1] = ahead[t][1];
+    fetch_units(i + 1);
     uint32_t bf[4][4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -844,7 +856,6 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
     for (int t = 0; t < R / 16; ++t) {
       if (16 * t >= r16) break;
       float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      const float back[2] = {__ldcg(unit + 16 * t), __ldcg(unit + 16 * t + 8)};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t hi[4], lo[4];
@@ -859,7 +870,7 @@ __global__ void __launch_bounds__(kGradThreads) k_adapter_grad(const __grid_cons
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) sum[t][n][q] = fmaf(acc[n][q], back[q >> 1], sum[t][n][q]);
+        for (int q = 0; q < 4; ++q) sum[t][n][q] = fmaf(acc[n][q], back[t][q >> 1], sum[t][n][q]);
     }
   }
   cp_async_wait<0>();
